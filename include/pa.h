@@ -389,6 +389,111 @@ pa_status pa_copy_blocks(void* key_cache, void* value_cache, const int32_t* bloc
                          int32_t block_size, int32_t num_blocks, pa_dtype dtype,
                          int32_t* status_dev, pa_stream stream);
 
+/* ------------------------------------------------------------------------------ */
+/* Chunks of new tokens (prompts, and prompts taken in pieces beside running decodes)  */
+/* ------------------------------------------------------------------------------ */
+/* pa_rope_and_cache: rotary positions on the query and key rows of new tokens, and their
+ * K and V rows into the paged pools, in one pass.  It replaces pa_reshape_and_cache where
+ * the model rotates its heads.
+ *   query [num_tokens][num_q_heads][head_size], key / value [num_tokens][num_kv_heads]
+ *   [head_size], fp16 or bf16; the rows of one token are dense, and query_stride /
+ *   key_stride / value_stride (multiples of 8 elements) lead from one token's rows to the
+ *   next's, so that slices of a fused projection can be passed as they are.
+ *   positions int64 [num_axes][num_tokens]: the token's position on each of 1 .. 4 axes
+ *   (text: one; images and video: time, height, width), any integer within +-2^31 (beyond,
+ *   angles lose accuracy).  pair_axes: HOST int32 [rot_dim / 2], the axis of each rotated
+ *   pair; NULL for one axis.  inv_freq: device fp32 [rot_dim / 2], radians per position,
+ *   finite.
+ * The first rot_dim dimensions of a query or key row turn in pairs, the others stay:
+ *   (x, y) -> (x cos a - y sin a, x sin a + y cos a),
+ *   a = positions[pair_axes[i]][token] * inv_freq[i] for pair i,
+ * pair i being dimensions (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved.  The
+ * angle's turns are taken modulo one in 64-bit fixed point, the rest in fp32, rounded once.
+ * query_out [num_tokens][num_q_heads][head_size] (dense) takes the rotated query rows; it may
+ * be query itself when query is dense.  The rotated key row and the value row go to slot_mapping[token] as in
+ * pa_reshape_and_cache; a negative slot writes no K or V (the query row is still written), a
+ * slot past the pool is skipped and flagged PA_DEVERR_BAD_SLOT.  Two tokens with one slot
+ * race.  head_size a multiple of 16 up to 1024, rot_dim a multiple of 16 up to head_size
+ * and 256. */
+pa_status pa_rope_and_cache(void* query_out, const void* query, const void* key, const void* value,
+                            int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                            void* key_cache, void* value_cache, const int32_t* slot_mapping,
+                            const int64_t* positions, int32_t num_axes, const int32_t* pair_axes,
+                            const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                            int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                            int32_t head_size, int32_t block_size, int32_t num_blocks,
+                            pa_dtype dtype, int32_t* status_dev, pa_stream stream);
+
+/* The same into fp8 E4M3 pools: the fp32 rotated key, and the value, each become
+ * e4m3(x * r) as in pa_reshape_and_cache_fp8 (no 16-bit rounding in between). */
+pa_status pa_rope_and_cache_fp8(void* query_out, const void* query, const void* key,
+                                const void* value, int64_t query_stride, int64_t key_stride,
+                                int64_t value_stride, void* key_cache, void* value_cache,
+                                const int32_t* slot_mapping, const int64_t* positions,
+                                int32_t num_axes, const int32_t* pair_axes, const float* inv_freq,
+                                int32_t rot_dim, int32_t interleaved, int32_t num_tokens,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                                int32_t block_size, int32_t num_blocks, pa_dtype dtype, float k_scale,
+                                float v_scale, int32_t* status_dev, pa_stream stream);
+
+/* pa_prefill: attention of a ragged chunk of new tokens over the paged cache.  Sequence s
+ * brings C = query_starts[s+1] - query_starts[s] >= 0 new tokens (any number, different for
+ * each sequence; prompts' chunks and single decode tokens may share a call), rows
+ * query_starts[s] .. of query and out, already in the pools; context_lens[s] = L counts
+ * them.  New token j sits at position L - C + j and attends to the tokens before and at it:
+ *   out[query_starts[s] + j][h] = sum_t softmax_t(scale * q . k_t) v_t, t < L - C + j + 1;
+ * a row with nothing to attend to (L < C - j) is a zero row.  A token's row does not depend
+ * on what the pools hold past its own position, infinities and NaN included.
+ *   query, out    [num_tokens][num_q_heads][head_size], fp16 or bf16 (also the pools' type)
+ *   query_starts  int32 [num_seqs + 1], ascending, within 0 .. num_tokens; rows outside
+ *                 query_starts[0] .. query_starts[num_seqs] are left as they are
+ * and the rest as for pa_decode_v2.  num_tokens is at most 2^24.  Scores and sums are fp32;
+ * the softmax weights enter the product with V rounded to the cache's 16-bit type.
+ * Bad query_starts (descending, outside the rows) or lengths are clamped and flagged
+ * PA_DEVERR_BAD_LEN; block-table entries outside the pool read as zero rows and are flagged
+ * PA_DEVERR_BAD_BLOCK.
+ * `workspace` (device, 256-byte aligned) of pa_prefill_workspace_size bytes needs no
+ * initialisation and is dead after the call; calls that may overlap on the GPU need
+ * workspaces of their own.  The size is 0 for bad arguments. */
+size_t pa_prefill_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_size, int32_t max_context_len);
+pa_status pa_prefill(void* out, const void* query, const void* key_cache, const void* value_cache,
+                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                     const int32_t* context_lens, const int32_t* query_starts, int32_t num_tokens,
+                     int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                     int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
+                     pa_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                     pa_stream stream);
+
+/* pa_prefill over fp8 E4M3 pools (head_size 128): k_t, v_t = e4m3(byte) * k_scale, * v_scale.
+ * Tiles are widened to fp16 (exact) and queries rounded to fp16, so |q| <= 65504, as for
+ * pa_decode_fp8. */
+pa_status pa_prefill_fp8(void* out, const void* query, const void* key_cache,
+                         const void* value_cache, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* context_lens,
+                         const int32_t* query_starts, int32_t num_tokens, int32_t num_seqs,
+                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                         int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                         float scale, float k_scale, float v_scale, pa_dtype dtype, void* workspace,
+                         size_t workspace_bytes, int32_t* status_dev, pa_stream stream);
+
+/* pa_move_blocks: compaction of the pools.  For each pair i and every layer l, block
+ * block_pairs[2i+1] of key_caches[l] and value_caches[l] takes the contents of block
+ * block_pairs[2i] (a bit-exact copy), and every entry of block_tables equal to
+ * block_pairs[2i] becomes block_pairs[2i+1].  block_pairs is a device int32 array
+ * [num_pairs][2], ascending by its first column, e.g. the pairs of pa_alloc_shrink copied to
+ * the device; key_caches / value_caches are HOST arrays of num_layers device pointers to
+ * pools of one shape and type (PA_F16, PA_BF16 or PA_FP8_E4M3); block_tables (device, int32
+ * [num_rows][max_blocks_per_seq], NULL: none) may hold -1 padding.  A pair outside the pool
+ * is skipped, and it or a pair out of order is flagged PA_DEVERR_BAD_BLOCK (out of order,
+ * the tables' entries are unspecified; the copies are not).  A block that is a source and a
+ * destination, or two destinations, race.  One launch per 64 layers. */
+pa_status pa_move_blocks(void* const* key_caches, void* const* value_caches, int32_t num_layers,
+                         const int32_t* block_pairs, int32_t num_pairs, int32_t* block_tables,
+                         int32_t num_rows, int32_t max_blocks_per_seq, int32_t num_kv_heads,
+                         int32_t head_size, int32_t block_size, int32_t num_blocks, pa_dtype dtype,
+                         int32_t* status_dev, pa_stream stream);
+
 /* Self-test of the failure path: launches a one-warp kernel that waits on a pipeline
  * barrier nobody arrives on, gives up after limit_us (1 .. 2,000,000) microseconds and
  * ORs PA_DEVERR_TIMEOUT into *status_dev, exactly as the decode kernel does when a copy
@@ -454,6 +559,17 @@ int32_t pa_alloc_refcount(const pa_alloc* alloc, int32_t block);
 /* Drops seq_id's reference to each of its blocks (blocks no longer referenced return
  * to the free list, in logical order) and forgets the sequence. */
 pa_status pa_alloc_free_seq(pa_alloc* alloc, int32_t seq_id);
+/* Shrinks the pool to its first num_blocks blocks (1 .. the present number).  Blocks in use
+ * at or past num_blocks, in ascending order, move to the free blocks below it, the lowest
+ * first: tables and reference counts follow, the free ids at or past num_blocks leave the
+ * free list, whose order stays, and the pairs (from, to) go to pairs_out [max_pairs][2],
+ * *n_out of them, ascending.  Move the contents with pa_move_blocks before anything else
+ * uses the pools; the memory past num_blocks is then unused.  PA_ERR_NO_BLOCKS when more
+ * blocks are in use than num_blocks; PA_ERR_INVALID_ARG when copy-on-write pairs are
+ * pending (take and copy them first) or the pairs do not fit (*n_out set); nothing changes
+ * then. */
+pa_status pa_alloc_shrink(pa_alloc* alloc, int32_t num_blocks, int32_t* pairs_out,
+                          int32_t max_pairs, int32_t* n_out);
 /* Slots of positions [start, start + n) of seq_id. */
 pa_status pa_alloc_slots(const pa_alloc* alloc, int32_t seq_id, int32_t start, int32_t n,
                          int32_t* out);

@@ -53,6 +53,7 @@ def _load():
     lib = ctypes.CDLL(path)
     P, i32, u64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64, ctypes.c_float,
                             ctypes.c_size_t)
+    i64 = ctypes.c_int64
     sig = {
         "pa_last_error": ([], ctypes.c_char_p),
         "pa_version": ([], i32),
@@ -88,6 +89,17 @@ def _load():
         "pa_decode_step_host_overlapped": ([P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32,
                                             i32, i32, f32, i32, P, sz, P, sz, P, P, P, P, P, P],
                                            i32),
+        "pa_prefill_workspace_size": ([i32] * 6, sz),
+        "pa_prefill": ([P, P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, i32,
+                        P, sz, P, P], i32),
+        "pa_prefill_fp8": ([P, P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                            f32, f32, i32, P, sz, P, P], i32),
+        "pa_rope_and_cache": ([P, P, P, P, i64, i64, i64, P, P, P, P, i32, P, P, i32, i32, i32, i32,
+                               i32, i32, i32, i32, i32, P, P], i32),
+        "pa_rope_and_cache_fp8": ([P, P, P, P, i64, i64, i64, P, P, P, P, i32, P, P, i32, i32, i32,
+                                   i32, i32, i32, i32, i32, i32, f32, f32, P, P], i32),
+        "pa_move_blocks": ([P, P, i32, P, i32, P, i32, i32, i32, i32, i32, i32, i32, P, P], i32),
+        "pa_alloc_shrink": ([P, i32, P, i32, ctypes.POINTER(i32)], i32),
         "pa_alloc_create": ([i32, i32, u64, ctypes.POINTER(P)], i32),
         "pa_alloc_destroy": ([P], None),
         "pa_alloc_num_free": ([P], i32),
@@ -503,6 +515,173 @@ def pa_copy_blocks(key_cache, value_cache, block_pairs, status=None, stream=None
                                _opt_dev(status, "status"), _stream(stream)))
 
 
+def pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_size,
+                              max_context_len) -> int:
+    return int(_lib.pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads,
+                                              head_size, max_context_len))
+
+
+def _prefill_sizes(out, query, key_cache, value_cache, block_tables, context_lens, query_starts):
+    T, Hq, D = query.shape
+    NB, Hkv, bs, D2 = key_cache.shape
+    if out.shape != query.shape or value_cache.shape != key_cache.shape or D2 != D:
+        raise ValueError("prefill: inconsistent shapes")
+    S = context_lens.shape[0]
+    if (context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S
+            or query_starts.shape != (S + 1,)):
+        raise ValueError("prefill: block_tables [S, max_blocks], context_lens [S] and "
+                         "query_starts [S + 1] expected")
+    if out.dtype != query.dtype:
+        raise TypeError("out dtype differs from query")
+    return T, S, Hq, Hkv, D, bs, NB
+
+
+def pa_prefill(out, query, key_cache, value_cache, block_tables, context_lens, query_starts,
+               max_context_len: int, scale: float, workspace=None, status=None, stream=None):
+    """Attention of a ragged chunk of new tokens over the paged cache: query/out [T, Hq, D],
+    rows query_starts[s] .. query_starts[s+1]-1 belonging to sequence s's last tokens."""
+    import torch
+    sizes = _prefill_sizes(out, query, key_cache, value_cache, block_tables, context_lens,
+                           query_starts)
+    for t, n in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        if t.dtype != query.dtype:
+            raise TypeError(f"{n} dtype differs from query")
+    wp, wb = _ws(workspace)
+    _check(_lib.pa_prefill(
+        _dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"),
+        _dev(value_cache, "value_cache"), _dev(block_tables, "block_tables", torch.int32),
+        int(block_tables.shape[1]), _dev(context_lens, "context_lens", torch.int32),
+        _dev(query_starts, "query_starts", torch.int32), *sizes, int(max_context_len), float(scale),
+        _dt(query), wp, wb, _opt_dev(status, "status"), _stream(stream)))
+
+
+def pa_prefill_fp8(out, query, key_cache, value_cache, block_tables, context_lens, query_starts,
+                   max_context_len: int, scale: float, k_scale: float, v_scale: float,
+                   workspace=None, status=None, stream=None):
+    """pa_prefill over fp8 E4M3 pools (uint8 or float8_e4m3fn), head_size 128."""
+    import torch
+    sizes = _prefill_sizes(out, query, key_cache, value_cache, block_tables, context_lens,
+                           query_starts)
+    wp, wb = _ws(workspace)
+    _check(_lib.pa_prefill_fp8(
+        _dev(out, "out"), _dev(query, "query"), _u8(key_cache, "key_cache"),
+        _u8(value_cache, "value_cache"), _dev(block_tables, "block_tables", torch.int32),
+        int(block_tables.shape[1]), _dev(context_lens, "context_lens", torch.int32),
+        _dev(query_starts, "query_starts", torch.int32), *sizes, int(max_context_len), float(scale),
+        float(k_scale), float(v_scale), _dt(query), wp, wb, _opt_dev(status, "status"),
+        _stream(stream)))
+
+
+def _rows(t, name):
+    """Pointer and token stride of a [T, H, D] CUDA tensor whose rows of one token are dense
+    (a slice of a fused projection, for example)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    T, H, D = t.shape
+    s0, s1, s2 = t.stride()
+    if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
+        raise ValueError(f"{name}: the rows of one token must be dense")
+    return ctypes.c_void_p(t.data_ptr()), (s0 if T > 1 else H * D)
+
+
+_AXES = {}     # pair_axes as the host arrays the C call reads, by their values
+
+
+def _pair_axes(pair_axes):
+    key = tuple(pair_axes)
+    a = _AXES.get(key)
+    if a is None:
+        if len(_AXES) >= 64:
+            _AXES.clear()
+        a = _AXES[key] = _np_i32(key)
+    return a
+
+
+def _rope(fn, query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
+          inv_freq, pair_axes, interleaved, status, stream, pool, scales=()):
+    import torch
+    T, Hq, D = query.shape
+    Hkv = key.shape[1]
+    NB, Hkv2, bs, D2 = key_cache.shape
+    if (key.shape != (T, Hkv, D) or value.shape != key.shape or query_out.shape != query.shape
+            or value_cache.shape != key_cache.shape or (Hkv2, D2) != (Hkv, D)):
+        raise ValueError("rope_and_cache: inconsistent shapes")
+    if slot_mapping.shape != (T,) or positions.dim() != 2 or positions.shape[1] != T:
+        raise ValueError("rope_and_cache: slot_mapping [T] and positions [axes, T] expected")
+    if inv_freq.dim() != 1:
+        raise ValueError("rope_and_cache: inv_freq [rot_dim / 2] expected")
+    for t, n in ((key, "key"), (value, "value"), (query_out, "query_out")):
+        if t.dtype != query.dtype:
+            raise TypeError(f"{n} dtype differs from query")
+    axes = None
+    if pair_axes is not None:
+        axes = _pair_axes(pair_axes)
+        if axes.shape != inv_freq.shape:
+            raise ValueError("rope_and_cache: pair_axes must name one axis per pair")
+    (qp, qs), (kp, ks), (vp, vs) = _rows(query, "query"), _rows(key, "key"), _rows(value, "value")
+    _check(fn(
+        _dev(query_out, "query_out"), qp, kp, vp, qs, ks, vs, pool(key_cache, "key_cache"),
+        pool(value_cache, "value_cache"), _dev(slot_mapping, "slot_mapping", torch.int32),
+        _dev(positions, "positions", torch.int64), int(positions.shape[0]),
+        None if axes is None else _nptr(axes), _dev(inv_freq, "inv_freq", torch.float32),
+        2 * int(inv_freq.shape[0]), 1 if interleaved else 0, T, Hq, Hkv, D, bs, NB, _dt(query),
+        *scales, _opt_dev(status, "status"), _stream(stream)))
+
+
+def pa_rope_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
+                      inv_freq, pair_axes=None, interleaved: bool = False, status=None, stream=None):
+    """Rotary positions on query/key [T, H, D] and the K/V rows into the pools.  positions
+    int64 [axes, T]; inv_freq fp32 [rot_dim / 2]; pair_axes (a sequence of ints on the host)
+    names the axis of each rotated pair, needed for more than one axis.  query/key/value may
+    be slices of a fused projection; query_out is dense."""
+    for t, n in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        if t.dtype != query.dtype:
+            raise TypeError(f"{n} dtype differs from query")
+    _rope(_lib.pa_rope_and_cache, query_out, query, key, value, key_cache, value_cache,
+          slot_mapping, positions, inv_freq, pair_axes, interleaved, status, stream, _dev)
+
+
+def pa_rope_and_cache_fp8(query_out, query, key, value, key_cache, value_cache, slot_mapping,
+                          positions, inv_freq, k_scale: float, v_scale: float, pair_axes=None,
+                          interleaved: bool = False, status=None, stream=None):
+    """pa_rope_and_cache into fp8 E4M3 pools (uint8 or float8_e4m3fn)."""
+    _rope(_lib.pa_rope_and_cache_fp8, query_out, query, key, value, key_cache, value_cache,
+          slot_mapping, positions, inv_freq, pair_axes, interleaved, status, stream, _u8,
+          (float(k_scale), float(v_scale)))
+
+
+def pa_move_blocks(key_caches, value_caches, block_pairs, block_tables=None, status=None,
+                   stream=None):
+    """Moves block `from` to block `to` for each row (from, to) of block_pairs (int32 [n, 2]
+    on the device, ascending `from`) in every layer's pools (lists of [NB, Hkv, bs, D]
+    tensors), and rewrites block_tables (int32 [rows, max_blocks] on the device)."""
+    import torch
+    L = len(key_caches)
+    if L == 0 or len(value_caches) != L:
+        raise ValueError("move_blocks: key_caches and value_caches of at least one layer expected")
+    if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
+        raise ValueError("move_blocks: pairs [n, 2] expected")
+    k0 = key_caches[0]
+    NB, Hkv, bs, D = k0.shape
+    pools = (ctypes.c_void_p * (2 * L))()
+    for i, t in enumerate((*key_caches, *value_caches)):
+        if t.shape != k0.shape or t.dtype != k0.dtype:
+            raise ValueError("move_blocks: the pools must have one shape and type")
+        pools[i] = _dev(t, "pool").value
+    rows, width = 0, 1
+    if block_tables is not None:
+        if block_tables.dim() != 2:
+            raise ValueError("move_blocks: block_tables [rows, max_blocks] expected")
+        rows, width = block_tables.shape
+    dt = PA_FP8_E4M3 if k0.element_size() == 1 else _dt(k0)
+    base = ctypes.addressof(pools)
+    _check(_lib.pa_move_blocks(
+        ctypes.c_void_p(base), ctypes.c_void_p(base + L * ctypes.sizeof(ctypes.c_void_p)), L,
+        _dev(block_pairs, "block_pairs", torch.int32), int(block_pairs.shape[0]),
+        None if block_tables is None else _dev(block_tables, "block_tables", torch.int32), rows,
+        width, Hkv, D, bs, NB, dt, _opt_dev(status, "status"), _stream(stream)))
+
+
 def pa_selftest_wait_timeout(status, limit_us: int, stream=None):
     """Runs the bounded-wait self-test kernel; sets PA_DEVERR_TIMEOUT in `status`."""
     import torch
@@ -599,6 +778,15 @@ class PagedAllocator:
 
     def pa_alloc_free_seq(self, seq_id: int):
         _check(_lib.pa_alloc_free_seq(self._h, int(seq_id)))
+
+    def pa_alloc_shrink(self, num_blocks: int) -> np.ndarray:
+        """Shrinks the pool to num_blocks blocks; the moved blocks' pairs [n, 2] (from, to)."""
+        room = max(self.num_blocks - int(num_blocks), 0)
+        out = np.zeros((max(room, 1), 2), dtype=np.int32)
+        got = ctypes.c_int32(0)
+        _check(_lib.pa_alloc_shrink(self._h, int(num_blocks), _nptr(out), room, ctypes.byref(got)))
+        self.num_blocks = int(num_blocks)
+        return out[:got.value]
 
     def pa_alloc_slots(self, seq_id: int, start: int, n: int) -> np.ndarray:
         out = np.empty(int(n), dtype=np.int32)

@@ -28,9 +28,14 @@ SOURCES = [
     "pa_decode_mq_f16.cu",
     "pa_decode_mq_bf16.cu",
     "pa_decode_tc.cu",
+    "pa_prefill_bf16.cu",
+    "pa_prefill_f16.cu",
+    "pa_prefill_fp8.cu",
     "pa_aux.cu",
+    "pa_chunk_aux.cu",
     "pa_noalloc.cu",
     "pa_host.cpp",
+    "pa_chunk_host.cpp",
     "pa_alloc.cpp",
 ]
 

@@ -23,6 +23,8 @@
 //  10. take_copies returns the pending pairs in order and clears them.
 //  11. reserve(id, extra) pops blocks until the sequence owns ceil((len + extra) /
 //      block_size) of them (after rule 9); len does not change.
+//  12. shrink(n): the used ids >= n, ascending, move to the free ids < n, ascending (tables and
+//      counts follow); ids >= n leave the free list, the moved-to ids too; its order stays.
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
@@ -253,6 +255,43 @@ pa_status pa_alloc_free_seq(pa_alloc* a, int32_t seq_id) {
     for (int32_t b : it->second.blocks)
         if (--a->refcount[b] == 0) a->free_list.push_back(b);
     a->seqs.erase(it);
+    return ok();
+}
+
+pa_status pa_alloc_shrink(pa_alloc* a, int32_t num_blocks, int32_t* pairs_out, int32_t max_pairs,
+                          int32_t* n_out) {
+    if (!a || !n_out || max_pairs < 0) return fail(PA_ERR_INVALID_ARG, "alloc_shrink: bad args");
+    *n_out = 0;
+    if (num_blocks <= 0 || num_blocks > a->num_blocks)
+        return fail(PA_ERR_INVALID_ARG, "alloc_shrink: num_blocks %d (1 .. %d)", num_blocks, a->num_blocks);
+    if (!a->copies.empty())
+        return fail(PA_ERR_INVALID_ARG, "alloc_shrink: %zu copy-on-write pairs are pending", a->copies.size() / 2);
+    std::vector<int32_t> high, low;
+    for (int32_t b = 0; b < a->num_blocks; ++b) {
+        if (b < num_blocks && a->refcount[b] == 0) low.push_back(b);
+        if (b >= num_blocks && a->refcount[b] > 0) high.push_back(b);
+    }
+    if (high.size() > low.size())
+        return fail(PA_ERR_NO_BLOCKS, "alloc_shrink: %zu blocks are in use, more than %d",
+                    (size_t)a->num_blocks - a->free_list.size(), num_blocks);
+    *n_out = (int32_t)high.size();
+    if (*n_out > max_pairs)
+        return fail(PA_ERR_INVALID_ARG, "alloc_shrink: %d pairs, room for %d", *n_out, max_pairs);
+    if (*n_out > 0 && !pairs_out) return fail(PA_ERR_INVALID_ARG, "alloc_shrink: null output");
+    std::vector<int32_t> place((size_t)a->num_blocks);
+    for (int32_t b = 0; b < a->num_blocks; ++b) place[b] = b;
+    for (size_t i = 0; i < high.size(); ++i) {
+        pairs_out[2 * i] = high[i];
+        pairs_out[2 * i + 1] = low[i];
+        place[high[i]] = low[i];
+        a->refcount[low[i]] = a->refcount[high[i]];
+    }
+    for (auto& kv : a->seqs)
+        for (int32_t& b : kv.second.blocks) b = place[b];
+    a->refcount.resize(num_blocks);
+    auto gone = [&](int32_t b) { return b >= num_blocks || a->refcount[b] > 0; };
+    a->free_list.erase(std::remove_if(a->free_list.begin(), a->free_list.end(), gone), a->free_list.end());
+    a->num_blocks = num_blocks;
     return ok();
 }
 

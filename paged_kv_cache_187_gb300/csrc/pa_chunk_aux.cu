@@ -1,0 +1,397 @@
+// pa_chunk_aux.cu -- the kernels around the chunk attention: the plan that cuts a ragged
+// batch into work items, rotary positions fused with the write into the paged pools, and
+// the moving of blocks when a pool is compacted.
+#include <algorithm>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "pa_chunk.h"
+#include "pa_device.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int32_t kBadSlot = 1, kBadBlock = 2, kBadLen = 4;
+
+// Block-wide exclusive scan of x over blockDim.x (a multiple of 32) threads; *total
+// receives the sum.  `buf` holds 32 ints of shared memory.
+__device__ __forceinline__ int32_t block_scan(int32_t x, int32_t* buf, int32_t* total) {
+    const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int32_t v = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    if (lane == 31) buf[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        int32_t w = lane < nw ? buf[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        buf[lane] = w;
+    }
+    __syncthreads();
+    const int32_t excl = (warp > 0 ? buf[warp - 1] : 0) + v - x;
+    *total = buf[31];
+    __syncthreads();
+    return excl;
+}
+
+constexpr int kPlanThreads = 512;
+constexpr int kBuckets = 256;
+
+// Cuts a ragged batch into the work list of the attention kernel.  Row tiles are the runs
+// of up to 2 * tpt new tokens of a sequence; a row tile needs the 128-token tiles up to the
+// last token its last row sees.  When there are too few row tiles to fill the CTAs, long
+// ones are cut into equal partitions of the context, none longer than the mean work per
+// CTA.  Longest items first, so that the last ones handed out are the cheapest.
+__global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillParams p) {
+    __shared__ int32_t buf[32];
+    __shared__ int32_t hist[kBuckets], first[kBuckets];
+    __shared__ unsigned long long work;
+    __shared__ int32_t longest;
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int32_t tid = threadIdx.x, span = 2 * p.tpt;
+    if (tid < kBuckets) hist[tid] = 0;
+    if (tid == 0) {
+        work = 0;
+        longest = 0;
+    }
+    // the sequences: chunk, context, first row tile; bad metadata is clamped and reported
+    int32_t row_tiles = 0;
+    const int64_t row_cap = (int64_t)p.max_blocks_per_seq * p.block_size;
+    const int32_t cap = row_cap < p.max_context_len ? (int32_t)row_cap : p.max_context_len;
+    for (int32_t base = 0; base < p.num_seqs; base += kPlanThreads) {
+        const int32_t s = base + tid;
+        int32_t lo = 0, n = 0, len = 0, tiles = 0;
+        if (s < p.num_seqs) {
+            const int32_t a = p.query_starts[s], b = p.query_starts[s + 1], l = p.context_lens[s];
+            lo = min(max(a, 0), p.num_tokens);
+            const int32_t hi = min(max(b, lo), p.num_tokens);
+            n = hi - lo;
+            len = min(max(l, 0), cap);
+            if ((lo != a || hi != b || len != l) && p.status) atomicOr(p.status, kBadLen);
+            tiles = n / span + (n % span != 0);
+        }
+        int32_t sum;
+        const int32_t at = row_tiles + block_scan(tiles, buf, &sum);
+        if (s < p.num_seqs) p.seqs[s] = make_int4(lo, n, len, at);
+        // chunks that overlap could ask for more row tiles than there is room for
+        row_tiles = min(row_tiles + sum, p.max_row_tiles + 1);
+    }
+    if (row_tiles > p.max_row_tiles) {
+        if (tid == 0 && p.status) atomicOr(p.status, kBadLen);
+        row_tiles = p.max_row_tiles;
+    }
+    __syncthreads();
+    // row tile i: its sequence (the last whose first row tile is at or before i) and tiles
+    auto locate = [&](int32_t i, int4& q, int32_t& s, int32_t& tok0) {
+        int32_t a = 0, b = p.num_seqs;
+        while (b - a > 1) {
+            const int32_t m = (a + b) >> 1;
+            if (p.seqs[m].w <= i) a = m;
+            else b = m;
+        }
+        s = a;
+        q = p.seqs[a];
+        tok0 = (i - q.w) * span;
+        const int32_t last = min(tok0 + span, q.y);
+        return (max(q.z - q.y + last, 0) + kPfTok - 1) / kPfTok;
+    };
+    int4 q;
+    int32_t s, tok0;
+    {
+        unsigned long long mine = 0;
+        int32_t most = 0;
+        for (int32_t i = tid; i < row_tiles; i += kPlanThreads) {
+            const int32_t n = locate(i, q, s, tok0);
+            mine += (unsigned)n;
+            most = max(most, n);
+        }
+        if (mine) atomicAdd(&work, mine);
+        if (most) atomicMax(&longest, most);
+    }
+    __syncthreads();
+    const unsigned long long all = work * (unsigned long long)p.num_kv_heads;
+    const int32_t P =
+        (int32_t)max((unsigned long long)kPfMinPart, min((all + p.grid - 1) / p.grid, 1ull << 28));
+    auto parts_of = [&](int32_t n) { return n <= P ? 1 : (n + P - 1) / P; };
+    const int32_t scale = min(longest, P) + 1;
+    auto bucket = [&](int32_t n, int32_t np) {
+        return kBuckets - 1 - min(kBuckets - 1, (int32_t)((int64_t)((n + np - 1) / np) * kBuckets / scale));
+    };
+    for (int32_t i = tid; i < row_tiles; i += kPlanThreads) {
+        const int32_t n = locate(i, q, s, tok0), np = parts_of(n);
+        atomicAdd(&hist[bucket(n, np)], np);
+    }
+    __syncthreads();
+    {
+        int32_t sum;
+        const int32_t at = block_scan(tid < kBuckets ? hist[tid] : 0, buf, &sum);
+        if (tid < kBuckets) first[tid] = at;
+        __syncthreads();
+    }
+    int32_t slots = 0, splits = 0;
+    for (int32_t base = 0; base < row_tiles; base += kPlanThreads) {
+        const int32_t i = base + tid;
+        int32_t n = 0, np = 0;
+        if (i < row_tiles) {
+            n = locate(i, q, s, tok0);
+            np = parts_of(n);
+        }
+        int32_t ss, us;
+        const int32_t slot0 = slots + block_scan(np > 1 ? np : 0, buf, &ss);
+        const int32_t split = splits + block_scan(np > 1 ? 1 : 0, buf, &us);
+        if (i < row_tiles) {
+            const int32_t pos = atomicAdd(&first[bucket(n, np)], np);
+            for (int32_t k = 0; k < np; ++k) {
+                PfEntry e;
+                e.seq = s;
+                e.len = q.z;
+                e.q_start = q.x;
+                e.q_len = q.y;
+                e.tok0 = tok0;
+                e.tile0 = (int32_t)((int64_t)n * k / np);
+                e.tile1 = (int32_t)((int64_t)n * (k + 1) / np);
+                e.nparts = np;
+                e.part = k;
+                e.slot0 = slot0;
+                e.split = split;
+                e.pad = 0;
+                p.list[pos + k] = e;
+            }
+        }
+        slots += ss;
+        splits += us;
+    }
+    const int32_t counters = splits * p.num_kv_heads * 2;
+    for (int32_t i = tid; i < counters; i += kPlanThreads) p.arrive[i] = 0;
+    if (tid == 0) {
+        p.hdr->counter = 0;
+        p.hdr->total_items = (uint32_t)((row_tiles - splits + slots) * p.num_kv_heads);
+    }
+}
+
+// ------------------------------------------------------------------ rotary + cache write
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;     // tokens per CTA
+
+// Rotates the query and key rows of new tokens and writes K and V into the pools.
+//
+// Pair i of a row turns by the angle positions[axis(i)][token] * inv_freq[i].  In turns,
+// that product is taken in 64-bit fixed point: inv_freq / 2 pi is a 64-bit fraction of a
+// turn, its product with the integer position wraps modulo one turn exactly, and what is
+// left is rounded once, to fp32, so that far positions lose nothing: the fraction is
+// within 2^-53 of itself, 2^-22 radians at position 2^31.
+//
+// A CTA takes kRopeTokens tokens: first the cosines and sines of their pairs, one thread
+// per pair, into shared memory, then 32 bytes of a row per thread and step.
+template <bool BF16, bool KV8>
+__global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const RopeParams p) {
+    __shared__ float2 turn[kRopeTokens][kMaxRopePairs];
+    __shared__ int32_t slots[kRopeTokens];
+    allow_dependent_launch();   // what follows waits for this kernel before it reads the pools
+    grid_dependency_wait();
+    const int32_t i0 = blockIdx.x * kRopeTokens;
+    const int32_t n = min(kRopeTokens, p.num_tokens - i0);
+    const int32_t half = p.rot_dim / 2;
+    for (int32_t e = threadIdx.x; e < n * half; e += kRopeThreads) {
+        const int32_t t = e / half, i = e - t * half;
+        double f = (double)p.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+        f -= floor(f);
+        const unsigned long long step = (unsigned long long)(f * 18446744073709551616.0);
+        const unsigned long long pos =
+            (unsigned long long)p.positions[(int64_t)p.axis[i] * p.num_tokens + i0 + t];
+        // the upper half, as a signed number of half turns in [-1, 1)
+        const float x = (float)(int32_t)((step * pos) >> 32) * 4.656612873077392578125e-10f;
+        float sn, cs;
+        sincospif(x, &sn, &cs);
+        turn[t][i] = make_float2(cs, sn);
+    }
+    if (threadIdx.x < n) {
+        const int32_t slot = p.slot_mapping[i0 + threadIdx.x];
+        const bool bad = (int64_t)slot >= (int64_t)p.num_blocks * p.block_size;
+        if (bad && p.status) atomicOr(p.status, kBadSlot);
+        slots[threadIdx.x] = bad ? -1 : slot;
+    }
+    __syncthreads();
+    const int32_t units = p.head_size / 16;                        // 32-byte units of a row
+    const int32_t rot_units = p.rot_dim / 16;
+    const int32_t heads = p.num_q_heads + 2 * p.num_kv_heads, per = heads * units;
+    for (int32_t e = threadIdx.x; e < n * per; e += kRopeThreads) {
+        const int32_t t = e / per, r = e - t * per, h = r / units, c = r - h * units;
+        const int32_t kind = h < p.num_q_heads ? 0 : h < p.num_q_heads + p.num_kv_heads ? 1 : 2;
+        const int32_t head = kind == 0 ? h : kind == 1 ? h - p.num_q_heads : h - p.num_q_heads - p.num_kv_heads;
+        const int32_t slot = slots[t];
+        if (kind != 0 && slot < 0) continue;                        // a padding token's K and V
+        const bool rot = kind != 2 && c < rot_units;
+        // the unit's two 16-byte pieces: pairs (d, d + half) or adjacent elements
+        const int32_t d0 = rot && !p.interleaved ? 8 * c : 16 * c;
+        const int32_t d1 = rot && !p.interleaved ? half + 8 * c : 16 * c + 8;
+        const int64_t i = i0 + t;
+        const uint16_t* src = kind == 0 ? static_cast<const uint16_t*>(p.query) + i * p.q_stride
+                              : kind == 1 ? static_cast<const uint16_t*>(p.key) + i * p.k_stride
+                                          : static_cast<const uint16_t*>(p.value) + i * p.v_stride;
+        src += (int64_t)head * p.head_size;
+        const uint4 xa = *reinterpret_cast<const uint4*>(src + d0), xb = *reinterpret_cast<const uint4*>(src + d1);
+        float a[8], b[8];
+        unpack2<BF16>(xa.x, a[0], a[1]);
+        unpack2<BF16>(xa.y, a[2], a[3]);
+        unpack2<BF16>(xa.z, a[4], a[5]);
+        unpack2<BF16>(xa.w, a[6], a[7]);
+        unpack2<BF16>(xb.x, b[0], b[1]);
+        unpack2<BF16>(xb.y, b[2], b[3]);
+        unpack2<BF16>(xb.z, b[4], b[5]);
+        unpack2<BF16>(xb.w, b[6], b[7]);
+        if (rot) {
+            if (!p.interleaved) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 w = turn[t][8 * c + k];
+                    const float x = a[k], y = b[k];
+                    a[k] = x * w.x - y * w.y;
+                    b[k] = x * w.y + y * w.x;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 w = turn[t][8 * c + k], v = turn[t][8 * c + 4 + k];
+                    const float x = a[2 * k], y = a[2 * k + 1], z = b[2 * k], u = b[2 * k + 1];
+                    a[2 * k] = x * w.x - y * w.y;
+                    a[2 * k + 1] = x * w.y + y * w.x;
+                    b[2 * k] = z * v.x - u * v.y;
+                    b[2 * k + 1] = z * v.y + u * v.x;
+                }
+            }
+        }
+        const int64_t row = kind == 0
+                                ? i * p.num_q_heads + head
+                                : ((int64_t)(slot / p.block_size) * p.num_kv_heads + head) * p.block_size +
+                                      slot % p.block_size;
+        if (KV8 && kind != 0) {
+            // e4m3(x * (1 / scale)): fp32 product, nearest-even, saturated
+            uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? p.key_cache : p.value_cache) + row * p.head_size;
+            const float inv = kind == 1 ? p.k_inv : p.v_inv;
+            uint32_t qa[4], qb[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                qa[k] = f32x2_to_e4m3x2(__fmul_rn(a[2 * k], inv), __fmul_rn(a[2 * k + 1], inv));
+                qb[k] = f32x2_to_e4m3x2(__fmul_rn(b[2 * k], inv), __fmul_rn(b[2 * k + 1], inv));
+            }
+            *reinterpret_cast<uint2*>(dst + d0) = make_uint2(qa[0] | (qa[1] << 16), qa[2] | (qa[3] << 16));
+            *reinterpret_cast<uint2*>(dst + d1) = make_uint2(qb[0] | (qb[1] << 16), qb[2] | (qb[3] << 16));
+        } else {
+            uint16_t* dst = static_cast<uint16_t*>(kind == 0 ? p.query_out : kind == 1 ? p.key_cache : p.value_cache) +
+                            row * p.head_size;
+            // a piece that is not rotated goes out as it came in
+            uint4 ya = xa, yb = xb;
+            if (rot) {
+                ya = make_uint4(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]), pack2<BF16>(a[4], a[5]),
+                                pack2<BF16>(a[6], a[7]));
+                yb = make_uint4(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]), pack2<BF16>(b[4], b[5]),
+                                pack2<BF16>(b[6], b[7]));
+            }
+            *reinterpret_cast<uint4*>(dst + d0) = ya;
+            *reinterpret_cast<uint4*>(dst + d1) = yb;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ block moves
+constexpr int kMoveThreads = 256;
+constexpr int kMoveTableCtas = 8;
+
+// Copies block `from` to block `to` in both pools of every layer, and rewrites the block
+// tables' entries.  CTA (i, y): pair i of pool y (2 * layer, + 1 for V), or, past the
+// pairs and for y = 0, a share of the table entries: each entry looks itself up among the
+// pairs, which ascend by `from`.
+__global__ void __launch_bounds__(kMoveThreads) move_blocks_kernel(const __grid_constant__ MoveParams p) {
+    const int32_t i = blockIdx.x;
+    if (i >= p.num_pairs) {
+        if (blockIdx.y != 0 || !p.block_tables) return;
+        for (int64_t e = (int64_t)(i - p.num_pairs) * kMoveThreads + threadIdx.x; e < p.num_entries;
+             e += (int64_t)kMoveTableCtas * kMoveThreads) {
+            const int32_t b = p.block_tables[e];
+            if (b < 0 || b >= p.num_blocks) continue;
+            int32_t lo = 0, hi = p.num_pairs;
+            while (lo < hi) {
+                const int32_t m = (lo + hi) >> 1;
+                if (p.pairs[2 * m] < b) lo = m + 1;
+                else hi = m;
+            }
+            if (lo < p.num_pairs && p.pairs[2 * lo] == b) {
+                const int32_t to = p.pairs[2 * lo + 1];
+                if (to >= 0 && to < p.num_blocks) p.block_tables[e] = to;
+            }
+        }
+        return;
+    }
+    const int32_t from = p.pairs[2 * i], to = p.pairs[2 * i + 1];
+    const bool bad = from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks;
+    if (p.report && blockIdx.y == 0 && threadIdx.x == 0 && p.status &&
+        (bad || (i > 0 && p.pairs[2 * i - 2] >= from)))
+        atomicOr(p.status, kBadBlock);
+    const int32_t layer = blockIdx.y >> 1;
+    if (bad || layer >= p.num_layers) return;
+    uint4* const pool = static_cast<uint4*>((blockIdx.y & 1) ? p.value[layer] : p.key[layer]);
+    const uint4* src = pool + (int64_t)from * p.vecs_per_block;
+    uint4* dst = pool + (int64_t)to * p.vecs_per_block;
+    int64_t e = threadIdx.x;
+    // eight 16-byte loads in flight per thread
+    for (; e + 7 * kMoveThreads < p.vecs_per_block; e += 8 * kMoveThreads) {
+        uint4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __ldcs(src + e + k * kMoveThreads);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) __stcs(dst + e + k * kMoveThreads, x[k]);
+    }
+    for (; e < p.vecs_per_block; e += kMoveThreads) dst[e] = src[e];
+}
+
+// Launches `kern` as a programmatic dependent of the kernel before it on `stream`.
+template <class Arg>
+cudaError_t launch_pdl(dim3 grid, dim3 block, cudaStream_t stream, void (*kern)(Arg), const Arg& arg) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, arg);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_plan(const PrefillParams& p, cudaStream_t stream) {
+    return launch_pdl<PrefillParams>(dim3(1), dim3(kPlanThreads), stream,
+                                     prefill_plan_kernel, p);
+}
+
+cudaError_t launch_rope_and_cache(const RopeParams& p, bool bf16, bool kv8, cudaStream_t stream) {
+    if (p.num_tokens <= 0) return cudaSuccess;
+    using Kern = void (*)(RopeParams);
+    const Kern kern = kv8 ? (bf16 ? (Kern)rope_and_cache_kernel<true, true> : (Kern)rope_and_cache_kernel<false, true>)
+                          : (bf16 ? (Kern)rope_and_cache_kernel<true, false> : (Kern)rope_and_cache_kernel<false, false>);
+    return launch_pdl<RopeParams>(dim3((unsigned)((p.num_tokens + kRopeTokens - 1) / kRopeTokens)),
+                                  dim3(kRopeThreads), stream, kern, p);
+}
+
+cudaError_t launch_move_blocks(const MoveParams& p, cudaStream_t stream) {
+    // An ordinary launch: the tables it rewrites may be read early by a kernel after it.
+    move_blocks_kernel<<<dim3((unsigned)(p.num_pairs + (p.block_tables ? kMoveTableCtas : 0)),
+                              (unsigned)std::max(2 * p.num_layers, 1)),
+                         kMoveThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace pa

@@ -1,0 +1,837 @@
+// pa_prefill.cuh -- attention of a ragged chunk of new tokens over the paged cache, on the
+// 5th-generation tensor cores (tcgen05, tensor memory).
+//
+// What it computes: sequence s brings C_s new tokens (rows query_starts[s] ..
+// query_starts[s+1]-1 of query and out), already in the pools; token j of them sits at
+// position L_s - C_s + j and attends to every token before and at it:
+//     out[i][h] = sum_t softmax_t(scale q[i][h] . k_t) v_t,   t < L_s - C_s + j + 1.
+//
+// One work item is (row tile, kv head, partition of the context).  A row tile is two
+// streams of 128 query rows each; row r of a stream is new token r / group and query head
+// kvh * group + r % group, so that the heads of a group share every K/V tile.  Per tile of
+// 128 tokens and stream:
+//     S = Q K^T   M = 128 rows, N = 128 tokens, Q and K in shared memory, S in tensor memory
+//     P = 2^(S scale - ref)  one thread per row, written back over S as 16-bit pairs
+//     O += P V    M = 128 rows, N = head dims, P read from tensor memory, V MN-major
+// The MMA thread issues PV of one stream and its next QK^T back to back, stream by stream,
+// so the tensor pipe works on one stream while the other's softmax runs.  A row's
+// reference moves (and O is rescaled in tensor memory) only when a score passes it by
+// 2^8: the weights stay below 2^8 and their sum is held in fp32.
+//
+// Weights enter PV as one 16-bit term: rounding them costs at most half a step of the
+// 16-bit type relative to each weight (2^-8 bf16, 2^-11 fp16), as much as rounding the
+// output itself; a second term would cost half of PV's matrix rate again.
+//
+// Rows must not see what they are masked from, and a weight of 0 times an infinite or NaN
+// value would be NaN.  Only tiles that some row sees in part can hold such values; there
+// the fixing warps zero the V rows past the context, replace non-finite V elements by 0,
+// and note for each head dim the first token with +inf, -inf and NaN; the rows that do see
+// that token get the value added at the end.
+//
+// Warps: 0-3 and 4-7 softmax and epilogue of streams 0 and 1; 8 producer (claims items,
+// TMA of Q, K and V); 9 MMA issuer; 12-15 fix V tiles (16-bit caches), or widen the fp8
+// K/V tiles to fp16 and fix them.  Every wait is bounded; the four warps of a stream
+// decide together after each item whether to stop.
+#pragma once
+
+#include "pa_chunk.h"
+#include "pa_decode.cuh"
+
+namespace pa {
+namespace pf {
+
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix0 = 12;
+constexpr int kThreads = 512;
+constexpr int kBarStream = 1;          // named barriers 1, 2: the warps of a stream
+constexpr float kRefSlack = 8.f;       // a reference is left behind by at most this (log2)
+constexpr int32_t kNoToken = 0x7fffffff;
+// Registers per thread: 128 at launch, re-divided among the four warpgroups.
+constexpr int kRegLaunch = 128, kRegSoft = 184, kRegAux = 64, kRegFix = 80;
+static_assert(2 * kRegSoft + kRegAux + kRegFix <= 4 * kRegLaunch, "register split");
+
+// BF16: type of the MMA operands (fp16 for fp8 caches); QBF16: type of query and out.
+template <bool BF16_, bool QBF16_, int D_, int BS_, bool KV8_>
+struct Cfg {
+    static constexpr bool kBf16 = BF16_, kQBf16 = QBF16_, kKv8 = KV8_;
+    static constexpr int D = D_, BS = BS_;
+    static constexpr int BLOCKS = kPfTok / BS_;
+    static constexpr int HALVES = D_ / 64;                   // 128-byte swizzle spans per row
+    static constexpr uint32_t HALF = kPfTok * 128;           // one span of 128 rows
+    static constexpr uint32_t TILE = HALVES * HALF;          // a 16-bit tile of K, V or Q
+    static constexpr uint32_t TILE8 = kPfTok * 128;          // an fp8 tile (head_size 128)
+    // K and V tiles alternate in one ring, as large as shared memory admits
+    static constexpr int NST = KV8_ ? 3 : (D_ == 128 ? 4 : 8);
+    static constexpr int N8 = KV8_ ? 3 : 0;                  // fp8 tiles on their way
+    static constexpr uint32_t COL_S = 0, COL_O = 2 * kPfTok; // tensor-memory columns
+    static_assert(!KV8_ || (D_ == 128 && !BF16_), "fp8 tiles are widened to fp16");
+};
+
+struct Unit {
+    int32_t seq;          // -1: no more items
+    int32_t kvh, len, q_start, q_len, tok0, tile0;
+    int32_t cnt[2];       // tiles each stream needs
+    int32_t fix0;         // tiles at or past this one (within the item) are fixed
+    int32_t nparts, part, slot0, split;
+    int32_t pad[2];
+};
+
+template <class C>
+struct alignas(1024) Smem {
+    uint8_t q[2][C::TILE];
+    uint8_t kv[C::NST][C::TILE];
+    uint8_t kv8[C::N8 ? C::N8 : 1][C::N8 ? C::TILE8 : 16];
+    // A tile lands on kv_full; a V tile of a 16-bit cache that has to be fixed lands on
+    // kv_raw, and the fixing warps arrive on kv_fixed.  Each of the three counts only its
+    // own tiles of the stage: a warp that skips tiles could not tell a barrier two phases
+    // behind from one that is ready.
+    uint64_t kv_full[C::NST], kv_raw[C::NST], kv_fixed[C::NST], kv_empty[C::NST];
+    uint64_t kv8_full[C::N8 ? C::N8 : 1], kv8_empty[C::N8 ? C::N8 : 1];
+    uint64_t q_full, q_ready, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t u_full[2], u_empty[2], drain;
+    Unit unit[2];
+    // first token with +inf / -inf / NaN of each head dim among an item's fixed tiles
+    int32_t nonfinite[2][3][C::D];
+    int32_t any_nonfinite[2];
+    int32_t last_part[2];
+    uint32_t tmem_base;
+    volatile int32_t abort;
+};
+
+template <class C>
+constexpr size_t smem_bytes() {
+    return sizeof(Smem<C>) + 1024;
+}
+
+// D (TMEM) (+)= A (TMEM) x B (shared); one thread issues it.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// 32 consecutive 32-bit tensor-memory columns of this thread's lane (no wait).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 3-D tiled TMA load (Q: head dims, heads, tokens).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                            int32_t z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_keep(void* dst, const CUtensorMap* map, int32_t x,
+                                                 int32_t y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Is any of the eight 16-bit values infinite or NaN?  x * 0 is NaN for exactly those.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t taint(uint32_t acc, uint32_t x) {
+    uint32_t r;
+    if constexpr (kBf16)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    return r;
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const PrefillParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem<C>& sm = *reinterpret_cast<Smem<C>*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int D = C::D;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NST; ++i) {
+            mbar_init(&sm.kv_full[i], C::kKv8 ? 4 : 1);   // the widening warps, or TMA
+            mbar_init(&sm.kv_empty[i], 1);
+            mbar_init(&sm.kv_raw[i], 1);
+            mbar_init(&sm.kv_fixed[i], 4);
+        }
+        for (int i = 0; i < C::N8; ++i) {
+            mbar_init(&sm.kv8_full[i], 1);
+            mbar_init(&sm.kv8_empty[i], 4);
+        }
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_ready, 4);
+        mbar_init(&sm.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.o_free[i], 4);
+            mbar_init(&sm.u_full[i], 1);
+            mbar_init(&sm.u_empty[i], 13);   // MMA thread, 8 softmax warps, 4 fixing warps
+            sm.any_nonfinite[i] = 1;         // the producer clears the tables first
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        fence_barrier_init();
+        prefetch_tensor_map(&qmap);
+        prefetch_tensor_map(&kmap);
+        prefetch_tensor_map(&vmap);
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    grid_dependency_wait();   // the plan kernel, and with it everything before it, has finished
+
+    const int32_t Hkv = p.num_kv_heads, G = p.group;
+    auto fail = [&]() {
+        flag_error(p.status, PA_DEVERR_TIMEOUT_);
+        sm.abort = 1;
+    };
+
+    if (warp >= kWarpLoad && warp < kWarpFix0) {
+        warpgroup_reg_release<kRegAux>();
+        if (warp == kWarpLoad) {
+            // ------------------------------------------------------------ producer
+            const int32_t total = (int32_t)p.hdr->total_items;
+            int32_t w = (int32_t)blockIdx.x;
+            uint32_t kt = 0, nq = 0;   // K/V tiles and Q loads issued
+            uint32_t full_phase = 0, raw_phase = 0;   // bit s: parity of stage s's next such tile
+            bool ok = true;
+            for (uint32_t it = 0; ok; ++it) {
+                const uint32_t us = it & 1;
+                if (lane == 0) ok = mbar_wait(&sm.u_empty[us], ((it >> 1) & 1) ^ 1);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                const bool done = w >= total || warp_sees_abort(sm.abort);
+                int32_t claimed = total;
+                if (!done && lane == 0)
+                    claimed = (int32_t)(gridDim.x + atomicAdd(&p.hdr->counter, 1u));
+                Unit u;
+                u.seq = -1;
+                u.cnt[0] = u.cnt[1] = 0;
+                if (!done) {
+                    const PfEntry e = p.list[w / Hkv];
+                    u.seq = e.seq;
+                    u.kvh = w % Hkv;
+                    u.len = e.len;
+                    u.q_start = e.q_start;
+                    u.q_len = e.q_len;
+                    u.tok0 = e.tok0;
+                    u.tile0 = e.tile0;
+                    u.nparts = e.nparts;
+                    u.part = e.part;
+                    u.slot0 = e.slot0;
+                    u.split = e.split;
+                    u.pad[0] = u.pad[1] = 0;
+                    // tiles a stream needs: up to the last token its last row sees
+                    for (int i = 0; i < 2; ++i) {
+                        const int32_t a = e.tok0 + i * p.tpt, b = min(a + p.tpt, e.q_len);
+                        const int32_t n = a < e.q_len ? max(e.len - e.q_len + b, 0) : 0;
+                        u.cnt[i] = max(min((n + kPfTok - 1) / kPfTok, e.tile1) - e.tile0, 0);
+                    }
+                    // first tile that some row does not see whole
+                    u.fix0 = max(e.len - e.q_len + e.tok0 + 1, 0) / kPfTok - e.tile0;
+                }
+                // no one reads the table of two items ago any more
+                if (sm.any_nonfinite[us]) {
+                    __syncwarp();
+                    for (int i = lane; i < 3 * D; i += 32) (&sm.nonfinite[us][0][0])[i] = kNoToken;
+                    if (lane == 0) sm.any_nonfinite[us] = 0;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    sm.unit[us] = u;
+                    mbar_arrive(&sm.u_full[us]);
+                }
+                if (u.seq < 0) {
+                    if (lane == 0) allow_dependent_launch();
+                    break;
+                }
+                const int32_t nt = max(u.cnt[0], u.cnt[1]);
+                if (nt > 0) {
+                    if (lane == 0) {
+                        ok = mbar_wait(&sm.q_empty, (nq & 1) ^ 1);
+                        if (ok) {
+                            const uint32_t rows = (uint32_t)(p.tpt * G);
+                            mbar_arrive_expect_tx(&sm.q_full, ((u.cnt[0] > 0) + (u.cnt[1] > 0)) * rows *
+                                                                  C::HALVES * 128u);
+                            for (int i = 0; i < 2; ++i)
+                                for (int h = 0; h < C::HALVES && u.cnt[i] > 0; ++h)
+                                    tma_load_3d(sm.q[i] + h * C::HALF, &qmap, h * 64, u.kvh * G,
+                                                u.q_start + u.tok0 + i * p.tpt, &sm.q_full);
+                        }
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (ok) ++nq;
+                }
+                // block-table entries, 32 at a time, one per lane, the next 32 in flight; an
+                // entry outside the pool becomes a row past the tensor map (TMA reads zeros)
+                const int32_t nb0 = u.tile0 * C::BLOCKS;
+                const int32_t nb1 = min(nb0 + nt * C::BLOCKS, (u.len + C::BS - 1) / C::BS);
+                auto entries = [&](int32_t first) {
+                    int32_t phys = p.num_blocks;
+                    if (first + lane < nb1) {
+                        phys = p.block_tables[(size_t)u.seq * p.max_blocks_per_seq + first + lane];
+                        if (phys < 0 || phys >= p.num_blocks) {
+                            flag_error(p.status, PA_DEVERR_BAD_BLOCK_);
+                            phys = p.num_blocks;
+                        }
+                    }
+                    return phys;
+                };
+                int32_t chunk = 0, cur = p.num_blocks, nxt = p.num_blocks;
+                if (nt > 0) {
+                    cur = entries(nb0);
+                    nxt = entries(nb0 + 32);
+                }
+                for (int32_t j = 0; j < nt && ok; ++j) {
+                    const int32_t tb = j * C::BLOCKS;
+                    if ((tb >> 5) != chunk) {
+                        chunk = tb >> 5;
+                        cur = nxt;
+                        nxt = entries(nb0 + 32 * (chunk + 1));
+                    }
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!ok) break;
+                        const uint32_t ns = C::kKv8 ? C::N8 : C::NST;
+                        const uint32_t st = kt % ns, ph = ((kt / ns) & 1) ^ 1;
+                        const bool raw = !C::kKv8 && kv == 1 && j >= u.fix0;
+                        uint64_t* const full =
+                            C::kKv8 ? &sm.kv8_full[st] : raw ? &sm.kv_raw[st] : &sm.kv_full[st];
+                        uint64_t* const empty = C::kKv8 ? &sm.kv8_empty[st] : &sm.kv_empty[st];
+                        if (lane == 0) {
+                            ok = mbar_wait(empty, ph);
+                            if (ok) mbar_arrive_expect_tx(full, C::kKv8 ? C::TILE8 : C::TILE);
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                        if (!ok) break;
+                        __syncwarp();   // the expected bytes are posted before any copy
+                        constexpr int kCopies = C::kKv8 ? C::BLOCKS : C::BLOCKS * C::HALVES;
+                        const int b = C::kKv8 ? lane % C::BLOCKS : (lane / C::HALVES) % C::BLOCKS;
+                        const int h = C::kKv8 ? 0 : lane % C::HALVES;
+                        const int32_t pb = __shfl_sync(0xffffffffu, cur, (tb & 31) + b);
+                        if (lane < kCopies) {
+                            const int32_t y = (pb * Hkv + u.kvh) * C::BS;
+                            uint8_t* const dst = C::kKv8 ? sm.kv8[st] + b * C::BS * 128
+                                                         : sm.kv[st] + h * C::HALF + b * C::BS * 128;
+                            tma_load_2d_keep(dst, kv == 0 ? &kmap : &vmap, h * 64, y, full);
+                        }
+                        ++kt;
+                        if (raw) raw_phase ^= 1u << st;
+                        else full_phase ^= 1u << st;
+                    }
+                }
+                w = __shfl_sync(0xffffffffu, claimed, 0);
+            }
+            if (!ok && lane == 0) fail();
+            // after an abort, copies may still be landing: wait (bounded) for all of them
+            if (lane == 0 && sm.abort) {
+                // (the last copy on each barrier has the parity before its next)
+                for (uint32_t st = 0; st < (uint32_t)(C::kKv8 ? C::N8 : C::NST); ++st) {
+                    (void)mbar_wait(C::kKv8 ? &sm.kv8_full[st] : &sm.kv_full[st],
+                                    ((full_phase >> st) & 1) ^ 1);
+                    if (!C::kKv8) (void)mbar_wait(&sm.kv_raw[st], ((raw_phase >> st) & 1) ^ 1);
+                }
+                if (nq > 0) (void)mbar_wait(&sm.q_full, (nq - 1) & 1);
+            }
+            __syncwarp();
+        } else if (warp == kWarpMma) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t kIdQK = mma_idesc_f16(C::kBf16, 0, 0, kPfRows, kPfTok);
+                constexpr uint32_t kIdPV = mma_idesc_f16(C::kBf16, 0, 1, kPfRows, D);
+                uint32_t kt = 0, nq = 0, np[2] = {0, 0}, no[2] = {0, 0};
+                uint32_t full_phase = 0, fix_phase = 0;   // bit s: parity of stage s's next such tile
+                bool ok = true;
+                for (uint32_t it = 0; ok; ++it) {
+                    const uint32_t us = it & 1;
+                    ok = mbar_wait(&sm.u_full[us], (it >> 1) & 1);
+                    if (!ok) break;
+                    const int32_t seq = sm.unit[us].seq, fix0 = sm.unit[us].fix0;
+                    const int32_t cnt[2] = {sm.unit[us].cnt[0], sm.unit[us].cnt[1]};
+                    mbar_arrive(&sm.u_empty[us]);
+                    if (seq < 0) break;
+                    const int32_t nt = max(cnt[0], cnt[1]);
+                    if (nt == 0) continue;
+                    ok = mbar_wait(C::kKv8 && C::kQBf16 ? &sm.q_ready : &sm.q_full, nq & 1);
+                    if (!ok) break;
+                    ++nq;
+                    auto wait_kv = [&](uint32_t n, bool fixed) {
+                        const uint32_t st = n % C::NST;
+                        uint32_t& phase = fixed ? fix_phase : full_phase;
+                        const bool here = mbar_wait(fixed ? &sm.kv_fixed[st] : &sm.kv_full[st], (phase >> st) & 1);
+                        phase ^= 1u << st;
+                        return here;
+                    };
+                    // S of stream i = Q K^T with the K tile of ring place n
+                    auto qk = [&](int i, uint32_t n) {
+                        const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[i]), 16, 1024);
+                        const uint64_t kd = smem_desc_sw128(smem_u32(sm.kv[n % C::NST]), 16, 1024);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t off = (uint64_t)(((k >> 2) * C::HALF + (k & 3) * 32) >> 4);
+                            mma_f16_ss(tmem + C::COL_S + i * kPfTok, qd + off, kd + off, kIdQK, k > 0);
+                        }
+                        mma_commit(&sm.s_full[i]);
+                    };
+                    const uint32_t base = kt;   // tile j: K at base + 2 j, V at base + 2 j + 1
+                    ok = wait_kv(base, false);
+                    if (!ok) break;
+                    tmem_fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (cnt[i] > 0) qk(i, base);
+                    mma_commit(&sm.kv_empty[base % C::NST]);
+                    if (nt == 1) mma_commit(&sm.q_empty);
+                    for (int32_t j = 0; j < nt && ok; ++j) {
+                        const uint32_t nv = base + 2 * j + 1, nk = base + 2 * j + 2;
+                        const int vlast = j < cnt[1] ? 1 : 0, klast = j + 1 < cnt[1] ? 1 : 0;
+                        bool v_here = false, k_here = false;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (!ok || j >= cnt[i]) continue;
+                            if (!v_here) {
+                                ok = wait_kv(nv, !C::kKv8 && j >= fix0);
+                                v_here = true;
+                            }
+                            if (ok) ok = mbar_wait(&sm.p_full[i], np[i] & 1);
+                            if (ok && j == 0) ok = mbar_wait(&sm.o_free[i], (no[i] & 1) ^ 1);
+                            if (!ok) continue;
+                            ++np[i];
+                            tmem_fence_after_sync();
+                            {
+                                const uint64_t vd =
+                                    smem_desc_sw128(smem_u32(sm.kv[nv % C::NST]), C::HALF, 1024);
+#pragma unroll
+                                for (int k = 0; k < kPfTok / 16; ++k)
+                                    mma_f16_ts(tmem + C::COL_O + i * D, tmem + C::COL_S + i * kPfTok + 8 * k,
+                                               vd + (uint64_t)(k * (2048 >> 4)), kIdPV, j > 0 || k > 0);
+                            }
+                            if (i == vlast) mma_commit(&sm.kv_empty[nv % C::NST]);
+                            if (j + 1 < cnt[i]) {
+                                if (!k_here) {
+                                    ok = wait_kv(nk, false);
+                                    k_here = true;
+                                    if (!ok) continue;
+                                    tmem_fence_after_sync();
+                                }
+                                qk(i, nk);
+                                if (i == klast) {
+                                    mma_commit(&sm.kv_empty[nk % C::NST]);
+                                    if (j + 2 == nt) mma_commit(&sm.q_empty);
+                                }
+                            } else {
+                                mma_commit(&sm.o_full[i]);
+                                ++no[i];
+                            }
+                        }
+                    }
+                    kt = base + 2 * nt;
+                }
+                if (!ok) fail();
+                // every MMA this thread issued has completed before tensor memory is freed
+                mma_commit(&sm.drain);
+                (void)mbar_wait(&sm.drain, 0);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= kWarpFix0) {
+        // ---------------------------------------------------------- fixing / widening warps
+        warpgroup_reg_release<kRegFix>();
+        const int fw = warp - kWarpFix0, tid = fw * 32 + lane;
+        uint32_t kt = 0, nq = 0;
+        uint32_t raw_phase = 0;   // bit s: parity of stage s's next tile to fix
+        bool ok = true;
+        for (uint32_t it = 0; ok; ++it) {
+            const uint32_t us = it & 1;
+            ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
+            if (!ok) break;
+            const int32_t seq = sm.unit[us].seq, fix0 = sm.unit[us].fix0;
+            const int32_t cnt0 = sm.unit[us].cnt[0], cnt1 = sm.unit[us].cnt[1];
+            const int32_t len = sm.unit[us].len, tile0 = sm.unit[us].tile0;
+            const int32_t nt = max(cnt0, cnt1);
+            __syncwarp();
+            // (the slot is released by the softmax warps at the item's end as well, so the
+            // table of non-finite values stays this item's until then)
+            if (lane == 0) mbar_arrive(&sm.u_empty[us]);
+            if (seq < 0) break;
+            if (nt == 0) continue;
+            auto note = [&](int d, int32_t tok, int cls) {
+                atomicMin(&sm.nonfinite[us][cls][d], tok);
+                sm.any_nonfinite[us] = 1;
+            };
+            // V row `row` of a 16-bit tile in `buf`: zeroed past the context; else its
+            // infinite and NaN elements noted and replaced by 0
+            auto fix_row = [&](uint8_t* buf, int row, int32_t tok) {
+                if (tok >= len) {
+#pragma unroll
+                    for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4*>(buf + h * C::HALF + row * 128 +
+                                                      (((c + row) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    return;
+                }
+                uint32_t acc = 0;
+#pragma unroll
+                for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(buf + h * C::HALF + row * 128 +
+                                                                        (((c + row) & 7) << 4));
+                        acc = taint<C::kBf16>(acc, x.x);
+                        acc = taint<C::kBf16>(acc, x.y);
+                        acc = taint<C::kBf16>(acc, x.z);
+                        acc = taint<C::kBf16>(acc, x.w);
+                    }
+                constexpr uint32_t kExp = C::kBf16 ? 0x7F80u : 0x7C00u;
+                if ((acc & kExp) != kExp && ((acc >> 16) & kExp) != kExp) return;
+                for (int d = 0; d < D; ++d) {
+                    uint16_t* x = reinterpret_cast<uint16_t*>(
+                        buf + (d >> 6) * C::HALF + row * 128 + ((((d >> 3) & 7) ^ (row & 7)) << 4) + (d & 7) * 2);
+                    const uint32_t v = *x;
+                    if ((v & kExp) == kExp) {
+                        note(d, tok, (v & 0x7FFFu) != kExp ? 2 : (v >> 15));
+                        *x = 0;
+                    }
+                }
+            };
+            if constexpr (!C::kKv8) {
+                for (int32_t j = max(fix0, 0); j < nt && ok; ++j) {
+                    const uint32_t n = kt + 2 * j + 1, vs = n % C::NST;
+                    ok = mbar_wait_warp(&sm.kv_raw[vs], (raw_phase >> vs) & 1);
+                    if (!ok) break;
+                    raw_phase ^= 1u << vs;
+                    fix_row(sm.kv[vs], tid, (tile0 + j) * kPfTok + tid);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.kv_fixed[vs]);
+                }
+                kt += 2 * nt;
+            } else {
+                if constexpr (C::kQBf16) {
+                    // bf16 queries as fp16 (|q| <= 65504), in place
+                    ok = mbar_wait_warp(&sm.q_full, nq & 1);
+                    if (!ok) break;
+                    for (int i = 0; i < 2; ++i) {
+                        if ((i ? cnt1 : cnt0) == 0) continue;
+                        uint4* q = reinterpret_cast<uint4*>(sm.q[i]);
+#pragma unroll 4
+                        for (int c = tid; c < (int)(C::TILE / 16); c += 128) {
+                            uint4 x = q[c];
+                            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float a, b;
+                                unpack2<true>(w[k], a, b);
+                                w[k] = pack2<false>(a, b);
+                            }
+                            q[c] = x;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.q_ready);
+                    ++nq;
+                }
+                for (int32_t t = 0; t < 2 * nt && ok; ++t, ++kt) {
+                    const uint32_t s8 = kt % C::N8, st = kt % C::NST;
+                    ok = mbar_wait_warp(&sm.kv8_full[s8], (kt / C::N8) & 1) &&
+                         mbar_wait_warp(&sm.kv_empty[st], ((kt / C::NST) & 1) ^ 1);
+                    if (!ok) break;
+                    const bool fix = (t & 1) && (t >> 1) >= fix0;
+                    uint8_t* const dst = sm.kv[st];
+                    // 16 elements per step: lanes 0..7 of a row take its eight 16-byte pieces
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = i * 16 + (tid >> 3), c = tid & 7;
+                        uint4 x = *reinterpret_cast<const uint4*>(sm.kv8[s8] + row * 128 + ((c ^ (row & 7)) << 4));
+                        if (fix) {
+                            const int32_t tok = (tile0 + (t >> 1)) * kPfTok + row;
+                            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (tok >= len) w[k] = 0;
+                                // a byte of E4M3 is NaN when its low seven bits are all set
+                                const uint32_t nan = ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                                if (nan) {
+                                    for (int b = 0; b < 4; ++b)
+                                        if ((nan >> (8 * b)) & 0x80u) {
+                                            note(16 * c + 4 * k + b, tok, 2);
+                                            w[k] &= ~(0xFFu << (8 * b));
+                                        }
+                                }
+                            }
+                        }
+                        uint4 lo, hi;
+                        e4m3x4_to_f16x2x2(x.x, lo.x, lo.y);
+                        e4m3x4_to_f16x2x2(x.y, lo.z, lo.w);
+                        e4m3x4_to_f16x2x2(x.z, hi.x, hi.y);
+                        e4m3x4_to_f16x2x2(x.w, hi.z, hi.w);
+                        // pieces of the second half go out in the other order, so that eight
+                        // lanes always write to eight different bank groups
+                        uint8_t* const r = dst + (c >> 2) * C::HALF + row * 128;
+                        const int c0 = (2 * c) & 7, odd = c >> 2;
+                        *reinterpret_cast<uint4*>(r + (((c0 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4*>(r + (((c0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.kv8_empty[s8]);
+                        mbar_arrive(&sm.kv_full[st]);
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) fail();
+    } else {
+        // ---------------------------------------------------------- softmax and epilogue
+        warpgroup_reg_alloc<kRegSoft>();
+        const int si = warp >> 2, sw = warp & 3;
+        const int row = sw * 32 + lane;                 // query row of the stream = TMEM lane
+        const uint32_t taddr = tmem + ((uint32_t)(sw * 32) << 16);
+        const uint32_t ts = taddr + C::COL_S + si * kPfTok, to = taddr + C::COL_O + si * D;
+        const int32_t qtok = row / G;                   // new token of this row, within the stream
+        uint32_t ns = 0, no = 0;                        // scores seen, outputs taken
+        for (uint32_t it = 0;; ++it) {
+            const uint32_t us = it & 1;
+            bool ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
+            Unit u = {};
+            u.seq = -1;
+            if (ok) u = sm.unit[us];
+            const int32_t cnt = ok ? u.cnt[si] : 0;
+            const int32_t tok = ok ? u.tok0 + si * p.tpt + qtok : 0;
+            // tokens this row sees, and the fewest any row of the stream sees
+            const int32_t limit = min(u.len - u.q_len + tok + 1, u.len);
+            const int32_t whole = u.len - u.q_len + u.tok0 + si * p.tpt + 1;
+            float ref = -INFINITY, sum = 0.f;
+            if (ok && u.seq >= 0) {
+                for (int32_t j = 0; j < cnt; ++j) {
+                    ok = mbar_wait_warp(&sm.s_full[si], ns & 1);
+                    if (!ok) break;
+                    ++ns;
+                    tmem_fence_after_sync();
+                    float x[kPfTok];
+#pragma unroll
+                    for (int c = 0; c < kPfTok / 32; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
+                    tmem_wait_ld();
+                    if (p.negate) {
+#pragma unroll
+                        for (int c = 0; c < kPfTok; ++c) x[c] = -x[c];
+                    }
+                    const int32_t t0 = (u.tile0 + j) * kPfTok;
+                    if (t0 + kPfTok > whole) {
+                        const int32_t seen = limit - t0;
+#pragma unroll
+                        for (int c = 0; c < kPfTok; ++c) x[c] = c < seen ? x[c] : -INFINITY;
+                    }
+                    float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int c = 4; c < kPfTok; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+                    const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    // (m is NaN for an infinite score times a zero scale: the reference stays)
+                    const bool move = m > ref + kRefSlack || (ref == -INFINITY && m > -INFINITY);
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float next = move ? m : ref;
+                        const float a = move ? fast_exp2(ref - next) : 1.f;
+                        sum *= a;
+                        ref = next;
+                        if (j > 0) {
+                            // (the wait for S has also seen the previous tile's PV complete)
+#pragma unroll
+                            for (int h = 0; h < D / 32; ++h) {
+                                float o[32];
+                                tmem_ld32(to + 32 * h, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) o[c] *= a;
+                                tmem_st32(to + 32 * h, reinterpret_cast<const uint32_t*>(o));
+                            }
+                        }
+                    }
+                    const float nref = ref == -INFINITY ? 0.f : -ref;
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t w[kPfTok / 2];
+#pragma unroll
+                    for (int c = 0; c < kPfTok; c += 2) {
+                        const float a = fast_exp2(fmaf(x[c], p.scale_log2, nref));
+                        const float b = fast_exp2(fmaf(x[c + 1], p.scale_log2, nref));
+                        s4[c & 2] += a;
+                        s4[(c & 2) + 1] += b;
+                        w[c / 2] = pack2<C::kBf16>(a, b);
+                    }
+                    tmem_st32(ts, w);
+                    tmem_st32(ts + 32, w + 32);
+                    sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    tmem_wait_st();
+                    tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_full[si]);
+                }
+                // ---- the item's rows
+                if (ok && cnt > 0) {
+                    ok = mbar_wait_warp(&sm.o_full[si], no & 1);
+                    if (ok) {
+                        ++no;
+                        tmem_fence_after_sync();
+                    }
+                }
+            }
+            // the four warps of the stream stop together
+            if (consumers_any(!ok, 128, kBarStream + si)) {
+                if (lane == 0) fail();
+                break;
+            }
+            if (u.seq < 0) break;
+            const bool mine = qtok < p.tpt && tok < u.q_len;
+            const bool nonfinite = sm.any_nonfinite[us] != 0;
+            const size_t orow = ((size_t)(u.q_start + tok) * p.num_q_heads + (size_t)u.kvh * G + row % G) * D;
+            // 32 head dims of O (0 where the stream had no tile), with the infinite and NaN
+            // values this row sees
+            auto load_o = [&](int h, float (&o)[32]) {
+                if (cnt > 0) {
+                    tmem_ld32(to + 32 * h, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = 0.f;
+                }
+                if (nonfinite) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const int d = 32 * h + c;
+                        if (sm.nonfinite[us][0][d] < limit) o[c] += INFINITY;
+                        if (sm.nonfinite[us][1][d] < limit) o[c] -= INFINITY;
+                        if (sm.nonfinite[us][2][d] < limit) o[c] = __int_as_float(0x7fc00000);
+                    }
+                }
+            };
+            auto store_row = [&](int h, const float (&o)[32], float f) {
+                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow + 32 * h);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    dst[k] = make_uint4(pack2<C::kQBf16>(o[8 * k] * f, o[8 * k + 1] * f),
+                                        pack2<C::kQBf16>(o[8 * k + 2] * f, o[8 * k + 3] * f),
+                                        pack2<C::kQBf16>(o[8 * k + 4] * f, o[8 * k + 5] * f),
+                                        pack2<C::kQBf16>(o[8 * k + 6] * f, o[8 * k + 7] * f));
+            };
+            if (u.nparts == 1) {
+                const float f = sum == 0.f ? 0.f : p.out_scale / sum;
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) {
+                    float o[32];
+                    load_o(h, o);
+                    if (mine) store_row(h, o, f);
+                }
+                tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (cnt > 0) mbar_arrive(&sm.o_free[si]);
+                    mbar_arrive(&sm.u_empty[us]);
+                }
+            } else {
+                // partial rows, [dim][row] so that a warp's accesses are contiguous
+                auto place = [&](int part) {
+                    return (((size_t)(u.slot0 + part) * Hkv + u.kvh) * 2 + si) * kPfRows;
+                };
+                const size_t at = place(u.part);
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) {
+                    float o[32];
+                    load_o(h, o);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) p.part_acc[at * D + (32 * h + c) * kPfRows + row] = o[c];
+                }
+                p.part_ml[at + row] = make_float2(ref, sum);
+                tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (cnt > 0) mbar_arrive(&sm.o_free[si]);
+                    mbar_arrive(&sm.u_empty[us]);
+                }
+                // the stream that finishes the row tile's last partition joins them, always
+                // in the order of the partitions
+                __threadfence();
+                named_bar_sync(kBarStream + si, 128);
+                if (row == 0)
+                    sm.last_part[si] =
+                        atomicAdd(&p.arrive[((size_t)u.split * Hkv + u.kvh) * 2 + si], 1) == u.nparts - 1;
+                named_bar_sync(kBarStream + si, 128);
+                if (sm.last_part[si]) {
+                    __threadfence();
+                    float M = -INFINITY;
+                    for (int q = 0; q < u.nparts; ++q) M = fmaxf(M, __ldcg(&p.part_ml[place(q) + row]).x);
+                    float den = 0.f;
+                    for (int q = 0; q < u.nparts; ++q) {
+                        const float2 ml = __ldcg(&p.part_ml[place(q) + row]);
+                        den += state_weight(ml.x, M) * ml.y;
+                    }
+                    const float f = den == 0.f ? 0.f : p.out_scale / den;
+                    for (int h = 0; h < D / 32; ++h) {
+                        float o[32];
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] = 0.f;
+                        for (int q = 0; q < u.nparts; ++q) {
+                            const size_t pr = place(q);
+                            const float wq = state_weight(__ldcg(&p.part_ml[pr + row]).x, M);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                o[c] = fmaf(wq, __ldcg(&p.part_acc[pr * D + (32 * h + c) * kPfRows + row]), o[c]);
+                        }
+                        if (mine) store_row(h, o, f);
+                    }
+                }
+                named_bar_sync(kBarStream + si, 128);   // last_part is reused
+            }
+        }
+    }
+
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tmem_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace pf
+}  // namespace pa
