@@ -46,7 +46,7 @@ constexpr int kBarStream = 1;          // named barriers 1, 2: the warps of a st
 constexpr float kRefSlack = 8.f;       // a reference is left behind by at most this (log2)
 constexpr int32_t kNoToken = 0x7fffffff;
 // Registers per thread: 128 at launch, re-divided among the four warpgroups.
-constexpr int kRegLaunch = 128, kRegSoft = 184, kRegAux = 64, kRegFix = 80;
+constexpr int kRegLaunch = 128, kRegSoft = 168, kRegAux = 96, kRegFix = 80;
 static_assert(2 * kRegSoft + kRegAux + kRegFix <= 4 * kRegLaunch, "register split");
 
 // BF16: type of the MMA operands (fp16 for fp8 caches); QBF16: type of query and out.
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     u.split = e.split;
                     u.pad[0] = u.pad[1] = 0;
                     // tiles a stream needs: up to the last token its last row sees
+#pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int32_t a = e.tok0 + i * p.tpt, b = min(a + p.tpt, e.q_len);
                         const int32_t n = a < e.q_len ? max(e.len - e.q_len + b, 0) : 0;
@@ -293,10 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t rows = (uint32_t)(p.tpt * G);
                             mbar_arrive_expect_tx(&sm.q_full, ((u.cnt[0] > 0) + (u.cnt[1] > 0)) * rows *
                                                                   C::HALVES * 128u);
+#pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                for (int h = 0; h < C::HALVES && u.cnt[i] > 0; ++h)
-                                    tma_load_3d(sm.q[i] + h * C::HALF, &qmap, h * 64, u.kvh * G,
-                                                u.q_start + u.tok0 + i * p.tpt, &sm.q_full);
+                                if (u.cnt[i] > 0)
+                                    for (int h = 0; h < C::HALVES; ++h)
+                                        tma_load_3d(sm.q[i] + h * C::HALF, &qmap, h * 64, u.kvh * G,
+                                                    u.q_start + u.tok0 + i * p.tpt, &sm.q_full);
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -639,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Unit u = {};
             u.seq = -1;
             if (ok) u = sm.unit[us];
-            const int32_t cnt = ok ? u.cnt[si] : 0;
+            const int32_t cnt = ok ? (si ? u.cnt[1] : u.cnt[0]) : 0;
             const int32_t tok = ok ? u.tok0 + si * p.tpt + qtok : 0;
             // tokens this row sees, and the fewest any row of the stream sees
             const int32_t limit = min(u.len - u.q_len + tok + 1, u.len);
@@ -652,19 +655,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++ns;
                     tmem_fence_after_sync();
                     float x[kPfTok];
-#pragma unroll
-                    for (int c = 0; c < kPfTok / 32; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
-                    tmem_wait_ld();
-                    if (p.negate) {
-#pragma unroll
-                        for (int c = 0; c < kPfTok; ++c) x[c] = -x[c];
-                    }
                     const int32_t t0 = (u.tile0 + j) * kPfTok;
-                    if (t0 + kPfTok > whole) {
-                        const int32_t seen = limit - t0;
+                    // this row's scores of the tile, masked
+                    auto scores = [&]() {
 #pragma unroll
-                        for (int c = 0; c < kPfTok; ++c) x[c] = c < seen ? x[c] : -INFINITY;
-                    }
+                        for (int c = 0; c < kPfTok / 32; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
+                        tmem_wait_ld();
+                        if (p.negate) {
+#pragma unroll
+                            for (int c = 0; c < kPfTok; ++c) x[c] = -x[c];
+                        }
+                        if (t0 + kPfTok > whole) {
+                            const int32_t seen = limit - t0;
+#pragma unroll
+                            for (int c = 0; c < kPfTok; ++c) x[c] = c < seen ? x[c] : -INFINITY;
+                        }
+                    };
+                    scores();
                     float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                     for (int c = 4; c < kPfTok; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
@@ -688,6 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st32(to + 32 * h, reinterpret_cast<const uint32_t*>(o));
                             }
                         }
+                        scores();   // (read again: they need not stay in registers meanwhile)
                     }
                     const float nref = ref == -INFINITY ? 0.f : -ref;
                     float s4[4] = {0.f, 0.f, 0.f, 0.f};
