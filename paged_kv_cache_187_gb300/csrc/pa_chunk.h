@@ -52,8 +52,7 @@ struct PrefillParams {
     int32_t num_tokens, num_seqs, num_q_heads, num_kv_heads, group;
     int32_t num_blocks, block_size, head_size, max_context_len;
     int32_t tpt;               // new tokens per stream: 128 / group
-    float scale_log2;          // |softmax scale| (x k_scale) * log2(e)
-    int32_t negate;            // the softmax scale is negative: scores are negated first
+    float scale_log2;          // softmax scale (x k_scale) * log2(e), never 0
     float out_scale;           // v_scale for fp8 caches, else 1
     int32_t grid;              // CTAs of the attention launch
     int32_t max_row_tiles;     // what the workspace has room for

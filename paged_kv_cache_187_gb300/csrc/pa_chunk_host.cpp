@@ -118,6 +118,7 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
         return fail(PA_ERR_INVALID_ARG, "prefill: k_scale and v_scale must be positive");
     if (a.block_size != 16 && a.block_size != 32)
         return fail(PA_ERR_UNSUPPORTED, "prefill: block_size %d (16 or 32)", a.block_size);
+    if (!std::isfinite(a.scale)) return fail(PA_ERR_INVALID_ARG, "prefill: scale must be finite");
     if (a.num_q_heads % a.num_kv_heads)
         return fail(PA_ERR_INVALID_ARG, "prefill: num_q_heads %% num_kv_heads != 0");
     const int32_t group = a.num_q_heads / a.num_kv_heads;
@@ -161,8 +162,9 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
     p.max_context_len = a.max_context_len;
     p.tpt = pa::kPfRows / group;
     const float scale = a.scale * (a.kv8 ? a.k_scale : 1.f);
-    p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
-    p.negate = std::signbit(scale) ? 1 : 0;
+    // never 0: a masked score is infinite, and stays so times any other scale
+    p.scale_log2 = scale * 1.4426950408889634f;
+    if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = std::copysign(1e-30f, scale);
     p.out_scale = a.kv8 ? a.v_scale : 1.f;
     p.max_row_tiles = L.max_row_tiles;
     p.max_entries = L.max_entries;

@@ -103,14 +103,64 @@ constexpr size_t smem_bytes() {
     return sizeof(Smem<C>) + 1024;
 }
 
-// D (TMEM) (+)= A (TMEM) x B (shared); one thread issues it.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, bool accumulate) {
+// The lower and upper words of a shared-memory descriptor of 128-byte swizzled rows.  The
+// upper one is a constant and the steps of a product change only the lower one, which keeps
+// the issue loop short: the tensor pipe takes a product step every 64 cycles.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// D (TMEM) (+)= A (shared) x B (shared); one thread issues it.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
         : "memory");
+}
+// D (TMEM) (+)= A (TMEM) x B (shared).
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+        : "memory");
+}
+
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
+// Two fp32 values per instruction (the .x2 forms of sm_100 and later).
+__device__ __forceinline__ uint64_t pack_f32(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack_f32(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // 32 consecutive 32-bit tensor-memory columns of this thread's lane (no wait).
@@ -139,6 +189,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+    tmem_wait_ld();
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v))
+                 : "memory");
+    tmem_wait_st();
 }
 
 // 3-D tiled TMA load (Q: head dims, heads, tokens).
@@ -379,102 +441,118 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == kWarpMma) {
             // ------------------------------------------------------------ MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t kIdQK = mma_idesc_f16(C::kBf16, 0, 0, kPfRows, kPfTok);
-                constexpr uint32_t kIdPV = mma_idesc_f16(C::kBf16, 0, 1, kPfRows, D);
-                uint32_t kt = 0, nq = 0, np[2] = {0, 0}, no[2] = {0, 0};
-                uint32_t full_phase = 0, fix_phase = 0;   // bit s: parity of stage s's next such tile
-                bool ok = true;
-                for (uint32_t it = 0; ok; ++it) {
-                    const uint32_t us = it & 1;
-                    ok = mbar_wait(&sm.u_full[us], (it >> 1) & 1);
-                    if (!ok) break;
-                    const int32_t seq = sm.unit[us].seq, fix0 = sm.unit[us].fix0;
-                    const int32_t cnt[2] = {sm.unit[us].cnt[0], sm.unit[us].cnt[1]};
-                    mbar_arrive(&sm.u_empty[us]);
-                    if (seq < 0) break;
-                    const int32_t nt = max(cnt[0], cnt[1]);
-                    if (nt == 0) continue;
-                    ok = mbar_wait(C::kKv8 && C::kQBf16 ? &sm.q_ready : &sm.q_full, nq & 1);
-                    if (!ok) break;
-                    ++nq;
-                    auto wait_kv = [&](uint32_t n, bool fixed) {
-                        const uint32_t st = n % C::NST;
-                        uint32_t& phase = fixed ? fix_phase : full_phase;
-                        const bool here = mbar_wait(fixed ? &sm.kv_fixed[st] : &sm.kv_full[st], (phase >> st) & 1);
-                        phase ^= 1u << st;
-                        return here;
-                    };
-                    // S of stream i = Q K^T with the K tile of ring place n
-                    auto qk = [&](int i, uint32_t n) {
-                        const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[i]), 16, 1024);
-                        const uint64_t kd = smem_desc_sw128(smem_u32(sm.kv[n % C::NST]), 16, 1024);
+            // The whole warp runs the loop and one elected lane issues: with every value the
+            // same in all lanes, descriptors stay in uniform registers, and a product step
+            // issues faster than the tensor pipe takes it (64 cycles).
+            constexpr uint32_t kIdQK = mma_idesc_f16(C::kBf16, 0, 0, kPfRows, kPfTok);
+            constexpr uint32_t kIdPV = mma_idesc_f16(C::kBf16, 0, 1, kPfRows, D);
+            const uint32_t q_lo = desc_lo(smem_u32(sm.q[0]), 16);
+            const uint32_t k_lo = desc_lo(smem_u32(sm.kv[0]), 16);
+            const uint32_t v_lo = desc_lo(smem_u32(sm.kv[0]), C::HALF);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            uint32_t st = 0, q_phase = 0;             // next stage of the ring; parity of q
+            uint32_t full_phase = 0, fix_phase = 0;   // bit s: parity of stage s's next such tile
+            uint32_t p_phase = 0, o_phase = 0;        // bit i: parities of stream i
+            bool ok = true;
+            auto next = [](uint32_t x) { return x + 1 == C::NST ? 0u : x + 1; };
+            auto wait_kv = [&](uint32_t x, bool fixed) {
+                const uint32_t phase = fixed ? fix_phase : full_phase;
+                const bool here = mbar_wait_warp(fixed ? &sm.kv_fixed[x] : &sm.kv_full[x], (phase >> x) & 1);
+                if (fixed) fix_phase ^= 1u << x;
+                else full_phase ^= 1u << x;
+                return here;
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) mma_commit(bar);
+            };
+            // S of stream i = Q K^T with the K tile of stage x
+            auto qk = [&](uint32_t i, uint32_t x) {
+                const uint32_t a = q_lo + i * (C::TILE >> 4), b = k_lo + x * (C::TILE >> 4);
+                const uint32_t d = tm + C::COL_S + i * kPfTok;
+                if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t off = (uint64_t)(((k >> 2) * C::HALF + (k & 3) * 32) >> 4);
-                            mma_f16_ss(tmem + C::COL_S + i * kPfTok, qd + off, kd + off, kIdQK, k > 0);
-                        }
-                        mma_commit(&sm.s_full[i]);
-                    };
-                    const uint32_t base = kt;   // tile j: K at base + 2 j, V at base + 2 j + 1
-                    ok = wait_kv(base, false);
-                    if (!ok) break;
-                    tmem_fence_after_sync();
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * C::HALF + (k & 3) * 32) >> 4;
+                        mma_ss(d, a + off, b + off, kIdQK, k > 0);
+                    }
+                    mma_commit(&sm.s_full[i]);
+                }
+            };
+            // O of stream i += P V with the V tile of stage x
+            auto pv = [&](uint32_t i, uint32_t x, bool first) {
+                const uint32_t a = tm + C::COL_S + i * kPfTok, b = v_lo + x * (C::TILE >> 4);
+                const uint32_t d = tm + C::COL_O + i * D;
+                if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (cnt[i] > 0) qk(i, base);
-                    mma_commit(&sm.kv_empty[base % C::NST]);
-                    if (nt == 1) mma_commit(&sm.q_empty);
-                    for (int32_t j = 0; j < nt && ok; ++j) {
-                        const uint32_t nv = base + 2 * j + 1, nk = base + 2 * j + 2;
-                        const int vlast = j < cnt[1] ? 1 : 0, klast = j + 1 < cnt[1] ? 1 : 0;
-                        bool v_here = false, k_here = false;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (!ok || j >= cnt[i]) continue;
-                            if (!v_here) {
-                                ok = wait_kv(nv, !C::kKv8 && j >= fix0);
-                                v_here = true;
+                    for (int k = 0; k < kPfTok / 16; ++k)
+                        mma_ts(d, a + 8 * k, b + k * (2048 >> 4), kIdPV, k > 0 ? 1u : (first ? 0u : 1u));
+                }
+            };
+#pragma unroll 1
+            for (uint32_t it = 0; ok; ++it) {
+                const uint32_t us = it & 1;
+                ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
+                if (!ok) break;
+                const int32_t seq = __shfl_sync(0xffffffffu, sm.unit[us].seq, 0);
+                const int32_t fix0 = __shfl_sync(0xffffffffu, sm.unit[us].fix0, 0);
+                const int32_t cnt0 = __shfl_sync(0xffffffffu, sm.unit[us].cnt[0], 0);
+                const int32_t cnt1 = __shfl_sync(0xffffffffu, sm.unit[us].cnt[1], 0);
+                if (lane == 0) mbar_arrive(&sm.u_empty[us]);
+                if (seq < 0) break;
+                const int32_t nt = max(cnt0, cnt1);
+                if (nt == 0) continue;
+                ok = mbar_wait_warp(C::kKv8 && C::kQBf16 ? &sm.q_ready : &sm.q_full, q_phase);
+                q_phase ^= 1;
+                if (ok) ok = wait_kv(st, false);
+                if (!ok) break;
+                // tile j's K sits in stage ks, its V in the next one
+                uint32_t ks = st;
+                tmem_fence_after_sync();
+                if (cnt0 > 0) qk(0, ks);
+                if (cnt1 > 0) qk(1, ks);
+                commit(&sm.kv_empty[ks]);
+                if (nt == 1) commit(&sm.q_empty);
+#pragma unroll 1
+                for (int32_t j = 0; j < nt && ok; ++j) {
+                    const uint32_t vs = next(ks), kn = next(vs);
+                    // the streams that take this tile: from i0, up to i1
+                    const uint32_t i0 = j < cnt0 ? 0 : 1, i1 = j < cnt1 ? 1 : 0;
+                    ok = wait_kv(vs, !C::kKv8 && j >= fix0);
+                    bool k_here = false;
+#pragma unroll 1
+                    for (uint32_t i = i0; i <= i1 && ok; ++i) {
+                        ok = mbar_wait_warp(&sm.p_full[i], (p_phase >> i) & 1);
+                        if (ok && j == 0) ok = mbar_wait_warp(&sm.o_free[i], ((o_phase >> i) & 1) ^ 1);
+                        if (!ok) break;
+                        p_phase ^= 1u << i;
+                        tmem_fence_after_sync();
+                        pv(i, vs, j == 0);
+                        if (i == i1) commit(&sm.kv_empty[vs]);
+                        if (j + 1 < (i ? cnt1 : cnt0)) {
+                            if (!k_here) {
+                                ok = wait_kv(kn, false);
+                                k_here = true;
+                                if (!ok) break;
+                                tmem_fence_after_sync();
                             }
-                            if (ok) ok = mbar_wait(&sm.p_full[i], np[i] & 1);
-                            if (ok && j == 0) ok = mbar_wait(&sm.o_free[i], (no[i] & 1) ^ 1);
-                            if (!ok) continue;
-                            ++np[i];
-                            tmem_fence_after_sync();
-                            {
-                                const uint64_t vd =
-                                    smem_desc_sw128(smem_u32(sm.kv[nv % C::NST]), C::HALF, 1024);
-#pragma unroll
-                                for (int k = 0; k < kPfTok / 16; ++k)
-                                    mma_f16_ts(tmem + C::COL_O + i * D, tmem + C::COL_S + i * kPfTok + 8 * k,
-                                               vd + (uint64_t)(k * (2048 >> 4)), kIdPV, j > 0 || k > 0);
+                            qk(i, kn);
+                            if (i == (j + 1 < cnt1 ? 1u : 0u)) {
+                                commit(&sm.kv_empty[kn]);
+                                if (j + 2 == nt) commit(&sm.q_empty);
                             }
-                            if (i == vlast) mma_commit(&sm.kv_empty[nv % C::NST]);
-                            if (j + 1 < cnt[i]) {
-                                if (!k_here) {
-                                    ok = wait_kv(nk, false);
-                                    k_here = true;
-                                    if (!ok) continue;
-                                    tmem_fence_after_sync();
-                                }
-                                qk(i, nk);
-                                if (i == klast) {
-                                    mma_commit(&sm.kv_empty[nk % C::NST]);
-                                    if (j + 2 == nt) mma_commit(&sm.q_empty);
-                                }
-                            } else {
-                                mma_commit(&sm.o_full[i]);
-                                ++no[i];
-                            }
+                        } else {
+                            commit(&sm.o_full[i]);
+                            o_phase ^= 1u << i;
                         }
                     }
-                    kt = base + 2 * nt;
+                    ks = kn;
                 }
-                if (!ok) fail();
-                // every MMA this thread issued has completed before tensor memory is freed
-                mma_commit(&sm.drain);
-                (void)mbar_wait(&sm.drain, 0);
+                st = ks;
             }
+            if (!ok && lane == 0) fail();
+            // every MMA of this warp has completed before tensor memory is freed
+            commit(&sm.drain);
+            (void)mbar_wait_warp(&sm.drain, 0);
             __syncwarp();
         }
     } else if (warp >= kWarpFix0) {
@@ -528,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 constexpr uint32_t kExp = C::kBf16 ? 0x7F80u : 0x7C00u;
                 if ((acc & kExp) != kExp && ((acc >> 16) & kExp) != kExp) return;
+#pragma unroll 1
                 for (int d = 0; d < D; ++d) {
                     uint16_t* x = reinterpret_cast<uint16_t*>(
                         buf + (d >> 6) * C::HALF + row * 128 + ((((d >> 3) & 7) ^ (row & 7)) << 4) + (d & 7) * 2);
@@ -639,53 +718,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t it = 0;; ++it) {
             const uint32_t us = it & 1;
             bool ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
-            Unit u = {};
-            u.seq = -1;
-            if (ok) u = sm.unit[us];
-            const int32_t cnt = ok ? (si ? u.cnt[1] : u.cnt[0]) : 0;
-            const int32_t tok = ok ? u.tok0 + si * p.tpt + qtok : 0;
+            // (the slot stays this item's until these warps release it, so what only the
+            // epilogue needs is read there)
+            const Unit& un = sm.unit[us];
+            const int32_t seq = ok ? un.seq : -1;
+            const int32_t cnt = seq >= 0 ? un.cnt[si] : 0;
             // tokens this row sees, and the fewest any row of the stream sees
-            const int32_t limit = min(u.len - u.q_len + tok + 1, u.len);
-            const int32_t whole = u.len - u.q_len + u.tok0 + si * p.tpt + 1;
+            const int32_t whole = un.len - un.q_len + un.tok0 + si * p.tpt + 1;
+            const int32_t limit = min(whole + qtok, un.len);
+            int32_t t0 = un.tile0 * kPfTok;   // first token of the tile
             float ref = -INFINITY, sum = 0.f;
-            if (ok && u.seq >= 0) {
-                for (int32_t j = 0; j < cnt; ++j) {
+            const uint64_t scale2 = pack_f32(p.scale_log2, p.scale_log2);
+            const float hidden = p.scale_log2 < 0.f ? INFINITY : -INFINITY;   // -inf once scaled
+            if (seq >= 0) {
+#pragma unroll 1
+                for (int32_t j = 0; j < cnt; ++j, t0 += kPfTok) {
                     ok = mbar_wait_warp(&sm.s_full[si], ns & 1);
                     if (!ok) break;
                     ++ns;
                     tmem_fence_after_sync();
-                    float x[kPfTok];
-                    const int32_t t0 = (u.tile0 + j) * kPfTok;
-                    // this row's scores of the tile, masked
-                    auto scores = [&]() {
+                    const bool masked = t0 + kPfTok > whole;
+                    // z = score - reference in log2 units, in pairs; once more, with O
+                    // rescaled, when a row's reference moves (the scores stay in tensor
+                    // memory until P overwrites them)
+                    uint64_t z[kPfTok / 2];
+#pragma unroll 1
+                    for (int pass = 0;; ++pass) {
+                        const float nref = ref == -INFINITY ? 0.f : -ref;
+                        const uint64_t nref2 = pack_f32(nref, nref);
+                        {
+                            float x[kPfTok];
 #pragma unroll
-                        for (int c = 0; c < kPfTok / 32; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
-                        tmem_wait_ld();
-                        if (p.negate) {
+                            for (int c = 0; c < kPfTok / 32; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
+                            tmem_wait_ld();
+                            if (masked) {
+                                const int32_t seen = limit - t0;
 #pragma unroll
-                            for (int c = 0; c < kPfTok; ++c) x[c] = -x[c];
+                                for (int c = 0; c < kPfTok; ++c) x[c] = c < seen ? x[c] : hidden;
+                            }
+#pragma unroll
+                            for (int c = 0; c < kPfTok / 2; ++c)
+                                z[c] = fma_x2(pack_f32(x[2 * c], x[2 * c + 1]), scale2, nref2);
                         }
-                        if (t0 + kPfTok > whole) {
-                            const int32_t seen = limit - t0;
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int c = 0; c < kPfTok; ++c) x[c] = c < seen ? x[c] : -INFINITY;
+                        for (int c = 0; c < kPfTok / 2; ++c) {
+                            float a, b;
+                            unpack_f32(z[c], a, b);
+                            mx[c & 3] = max3(mx[c & 3], a, b);
                         }
-                    };
-                    scores();
-                    float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                    for (int c = 4; c < kPfTok; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-                    const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                    // (m is NaN for an infinite score times a zero scale: the reference stays)
-                    const bool move = m > ref + kRefSlack || (ref == -INFINITY && m > -INFINITY);
-                    if (__any_sync(0xffffffffu, move)) {
-                        const float next = move ? m : ref;
+                        const float m = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                        const bool move = m > kRefSlack || (ref == -INFINITY && m > -INFINITY);
+                        if (!__any_sync(0xffffffffu, move) || pass == 1) break;
+                        const float next = move ? m - nref : ref;
                         const float a = move ? fast_exp2(ref - next) : 1.f;
                         sum *= a;
                         ref = next;
                         if (j > 0) {
                             // (the wait for S has also seen the previous tile's PV complete)
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < D / 32; ++h) {
                                 float o[32];
                                 tmem_ld32(to + 32 * h, o);
@@ -695,22 +786,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st32(to + 32 * h, reinterpret_cast<const uint32_t*>(o));
                             }
                         }
-                        scores();   // (read again: they need not stay in registers meanwhile)
                     }
-                    const float nref = ref == -INFINITY ? 0.f : -ref;
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t w[kPfTok / 2];
+                    uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int c = 0; c < kPfTok; c += 2) {
-                        const float a = fast_exp2(fmaf(x[c], p.scale_log2, nref));
-                        const float b = fast_exp2(fmaf(x[c + 1], p.scale_log2, nref));
-                        s4[c & 2] += a;
-                        s4[(c & 2) + 1] += b;
-                        w[c / 2] = pack2<C::kBf16>(a, b);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[kPfTok / 4];
+#pragma unroll
+                        for (int c = 0; c < kPfTok / 4; ++c) {
+                            float a, b;
+                            unpack_f32(z[h * (kPfTok / 4) + c], a, b);
+                            a = fast_exp2(a);
+                            b = fast_exp2(b);
+                            s2[c & 1] = add_x2(s2[c & 1], pack_f32(a, b));
+                            w[c] = pack2<C::kBf16>(a, b);
+                        }
+                        tmem_st32(ts + h * 32, w);
                     }
-                    tmem_st32(ts, w);
-                    tmem_st32(ts + 32, w + 32);
-                    sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    {
+                        float a, b;
+                        unpack_f32(add_x2(s2[0], s2[1]), a, b);
+                        sum += a + b;
+                    }
                     tmem_wait_st();
                     tmem_fence_before_sync();
                     __syncwarp();
@@ -730,12 +826,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) fail();
                 break;
             }
-            if (u.seq < 0) break;
+            if (seq < 0) break;
+            const Unit u = un;
+            const int32_t tok = u.tok0 + si * p.tpt + qtok;
             const bool mine = qtok < p.tpt && tok < u.q_len;
             const bool nonfinite = sm.any_nonfinite[us] != 0;
             const size_t orow = ((size_t)(u.q_start + tok) * p.num_q_heads + (size_t)u.kvh * G + row % G) * D;
-            // 32 head dims of O (0 where the stream had no tile), with the infinite and NaN
-            // values this row sees
+            // infinite and NaN values that were kept out of the products, for the rows that
+            // see them
+            if (nonfinite && cnt > 0) {
+#pragma unroll 1
+                for (int d = 0; d < D; ++d) {
+                    float o = tmem_ld1(to + d);
+                    if (sm.nonfinite[us][0][d] < limit) o += INFINITY;
+                    if (sm.nonfinite[us][1][d] < limit) o -= INFINITY;
+                    if (sm.nonfinite[us][2][d] < limit) o = __int_as_float(0x7fc00000);
+                    tmem_st1(to + d, o);
+                }
+            }
+            // 32 head dims of O (0 where the stream had no tile)
             auto load_o = [&](int h, float (&o)[32]) {
                 if (cnt > 0) {
                     tmem_ld32(to + 32 * h, o);
@@ -743,15 +852,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) o[c] = 0.f;
-                }
-                if (nonfinite) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int d = 32 * h + c;
-                        if (sm.nonfinite[us][0][d] < limit) o[c] += INFINITY;
-                        if (sm.nonfinite[us][1][d] < limit) o[c] -= INFINITY;
-                        if (sm.nonfinite[us][2][d] < limit) o[c] = __int_as_float(0x7fc00000);
-                    }
                 }
             };
             auto store_row = [&](int h, const float (&o)[32], float f) {
@@ -765,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (u.nparts == 1) {
                 const float f = sum == 0.f ? 0.f : p.out_scale / sum;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < D / 32; ++h) {
                     float o[32];
                     load_o(h, o);
@@ -783,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return (((size_t)(u.slot0 + part) * Hkv + u.kvh) * 2 + si) * kPfRows;
                 };
                 const size_t at = place(u.part);
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < D / 32; ++h) {
                     float o[32];
                     load_o(h, o);
@@ -808,17 +908,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (sm.last_part[si]) {
                     __threadfence();
                     float M = -INFINITY;
+#pragma unroll 1
                     for (int q = 0; q < u.nparts; ++q) M = fmaxf(M, __ldcg(&p.part_ml[place(q) + row]).x);
                     float den = 0.f;
+#pragma unroll 1
                     for (int q = 0; q < u.nparts; ++q) {
                         const float2 ml = __ldcg(&p.part_ml[place(q) + row]);
                         den += state_weight(ml.x, M) * ml.y;
                     }
                     const float f = den == 0.f ? 0.f : p.out_scale / den;
+#pragma unroll 1
                     for (int h = 0; h < D / 32; ++h) {
                         float o[32];
 #pragma unroll
                         for (int c = 0; c < 32; ++c) o[c] = 0.f;
+#pragma unroll 1
                         for (int q = 0; q < u.nparts; ++q) {
                             const size_t pr = place(q);
                             const float wq = state_weight(__ldcg(&p.part_ml[pr + row]).x, M);
