@@ -11,7 +11,7 @@
 // kvh * group + r % group, so that the heads of a group share every K/V tile.  Per tile of
 // 128 tokens and stream:
 //     S = Q K^T   M = 128 rows, N = 128 tokens, Q and K in shared memory, S in tensor memory
-//     P = 2^(S scale - ref)  one thread per row, written back over S as 16-bit pairs
+//     P = 2^(S scale - ref)  two threads per row, written back over S as 16-bit pairs
 //     O += P V    M = 128 rows, N = head dims, P read from tensor memory, V MN-major
 // The MMA thread issues PV of one stream and its next QK^T back to back, stream by stream,
 // so the tensor pipe works on one stream while the other's softmax runs.  A row's
@@ -28,10 +28,10 @@
 // and note for each head dim the first token with +inf, -inf and NaN; the rows that do see
 // that token get the value added at the end.
 //
-// Warps: 0-3 and 4-7 softmax and epilogue of streams 0 and 1; 8 producer (claims items,
-// TMA of Q, K and V); 9 MMA issuer; 12-15 fix V tiles (16-bit caches), or widen the fp8
-// K/V tiles to fp16 and fix them.  Every wait is bounded; the four warps of a stream
-// decide together after each item whether to stop.
+// Warps: 0-7 and 8-15 softmax and epilogue of streams 0 and 1, two threads per row; 16
+// producer (claims items, TMA of Q, K and V); 17 MMA issuer; 20-23 fix V tiles (16-bit
+// caches), or widen the fp8 K/V tiles to fp16 and fix them.  Every wait is bounded; the
+// warps of a stream decide together whether to stop.
 #pragma once
 
 #include "pa_chunk.h"
@@ -40,14 +40,15 @@
 namespace pa {
 namespace pf {
 
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix0 = 12;
-constexpr int kThreads = 512;
+constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpFix0 = 20;
+constexpr int kThreads = 768;
+constexpr int kStreamThreads = 256;    // two warpgroups of softmax per stream
 constexpr int kBarStream = 1;          // named barriers 1, 2: the warps of a stream
 constexpr float kRefSlack = 8.f;       // a reference is left behind by at most this (log2)
 constexpr int32_t kNoToken = 0x7fffffff;
-// Registers per thread: 128 at launch, re-divided among the four warpgroups.
-constexpr int kRegLaunch = 128, kRegSoft = 168, kRegAux = 96, kRegFix = 80;
-static_assert(2 * kRegSoft + kRegAux + kRegFix <= 4 * kRegLaunch, "register split");
+// Registers per thread: 80 at launch, re-divided among the six warpgroups.
+constexpr int kRegLaunch = 80, kRegSoft = 88, kRegAux = 72, kRegFix = 56;
+static_assert(4 * kRegSoft + kRegAux + kRegFix <= 6 * kRegLaunch, "register split");
 
 // BF16: type of the MMA operands (fp16 for fp8 caches); QBF16: type of query and out.
 template <bool BF16_, bool QBF16_, int D_, int BS_, bool KV8_>
@@ -87,7 +88,8 @@ struct alignas(1024) Smem {
     uint64_t kv_full[C::NST], kv_raw[C::NST], kv_fixed[C::NST], kv_empty[C::NST];
     uint64_t kv8_full[C::N8 ? C::N8 : 1], kv8_empty[C::N8 ? C::N8 : 1];
     uint64_t q_full, q_ready, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];
+    float red[2][2][kPfRows];          // [stream][half][row]: maxima, or weight sums
     uint64_t u_full[2], u_empty[2], drain;
     Unit unit[2];
     // first token with +inf / -inf / NaN of each head dim among an item's fixed tiles
@@ -258,11 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.p_full[i][0], 4);
+            mbar_init(&sm.p_full[i][1], 4);
             mbar_init(&sm.o_full[i], 1);
-            mbar_init(&sm.o_free[i], 4);
+            mbar_init(&sm.o_free[i], 8);
             mbar_init(&sm.u_full[i], 1);
-            mbar_init(&sm.u_empty[i], 13);   // MMA thread, 8 softmax warps, 4 fixing warps
+            mbar_init(&sm.u_empty[i], 21);   // MMA warp, 16 softmax warps, 4 fixing warps
             sm.any_nonfinite[i] = 1;         // the producer clears the tables first
         }
         mbar_init(&sm.drain, 1);
@@ -478,13 +481,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&sm.s_full[i]);
                 }
             };
-            // O of stream i += P V with the V tile of stage x
-            auto pv = [&](uint32_t i, uint32_t x, bool first) {
-                const uint32_t a = tm + C::COL_S + i * kPfTok, b = v_lo + x * (C::TILE >> 4);
+            // O of stream i += P V, half h of the V tile of stage x (P of half h sits where
+            // that half's scores were)
+            auto pv = [&](uint32_t i, uint32_t x, uint32_t h, bool first) {
+                const uint32_t a = tm + C::COL_S + i * kPfTok + h * (kPfTok / 2);
+                const uint32_t b = v_lo + x * (C::TILE >> 4) + h * (8192 >> 4);
                 const uint32_t d = tm + C::COL_O + i * D;
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kPfTok / 16; ++k)
+                    for (int k = 0; k < kPfTok / 32; ++k)
                         mma_ts(d, a + 8 * k, b + k * (2048 >> 4), kIdPV, k > 0 ? 1u : (first ? 0u : 1u));
                 }
             };
@@ -521,12 +526,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bool k_here = false;
 #pragma unroll 1
                     for (uint32_t i = i0; i <= i1 && ok; ++i) {
-                        ok = mbar_wait_warp(&sm.p_full[i], (p_phase >> i) & 1);
+                        ok = mbar_wait_warp(&sm.p_full[i][0], (p_phase >> i) & 1);
                         if (ok && j == 0) ok = mbar_wait_warp(&sm.o_free[i], ((o_phase >> i) & 1) ^ 1);
+                        if (!ok) break;
+                        tmem_fence_after_sync();
+                        pv(i, vs, 0, j == 0);
+                        ok = mbar_wait_warp(&sm.p_full[i][1], (p_phase >> i) & 1);
                         if (!ok) break;
                         p_phase ^= 1u << i;
                         tmem_fence_after_sync();
-                        pv(i, vs, j == 0);
+                        pv(i, vs, 1, false);
                         if (i == i1) commit(&sm.kv_empty[vs]);
                         if (j + 1 < (i ? cnt1 : cnt0)) {
                             if (!k_here) {
@@ -708,139 +717,153 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0) fail();
     } else {
         // ---------------------------------------------------------- softmax and epilogue
+        // Two threads per query row: thread `row` of warpgroup `half` takes tokens 64 half ..
+        // of every tile and the same half of the head dims of O.
         warpgroup_reg_alloc<kRegSoft>();
-        const int si = warp >> 2, sw = warp & 3;
+        constexpr int kCols = kPfTok / 2, kDims = D / 2;
+        const int si = warp >> 3, half = (warp >> 2) & 1, sw = warp & 3;
         const int row = sw * 32 + lane;                 // query row of the stream = TMEM lane
         const uint32_t taddr = tmem + ((uint32_t)(sw * 32) << 16);
-        const uint32_t ts = taddr + C::COL_S + si * kPfTok, to = taddr + C::COL_O + si * D;
+        const uint32_t ts = taddr + C::COL_S + si * kPfTok + half * kCols;
+        const uint32_t to = taddr + C::COL_O + si * D + half * kDims;
+        const int bar = kBarStream + si;
         const int32_t qtok = row / G;                   // new token of this row, within the stream
+        const uint64_t scale2 = pack_f32(p.scale_log2, p.scale_log2);
+        const float hidden = p.scale_log2 < 0.f ? INFINITY : -INFINITY;   // -inf once scaled
         uint32_t ns = 0, no = 0;                        // scores seen, outputs taken
+        bool failed = false;
+#pragma unroll 1
         for (uint32_t it = 0;; ++it) {
             const uint32_t us = it & 1;
             bool ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
+            // the warps of a stream stop together
+            if (consumers_any(!ok, kStreamThreads, bar)) {
+                failed = true;
+                break;
+            }
             // (the slot stays this item's until these warps release it, so what only the
             // epilogue needs is read there)
             const Unit& un = sm.unit[us];
-            const int32_t seq = ok ? un.seq : -1;
-            const int32_t cnt = seq >= 0 ? un.cnt[si] : 0;
+            if (un.seq < 0) break;
+            const int32_t cnt = un.cnt[si];
             // tokens this row sees, and the fewest any row of the stream sees
             const int32_t whole = un.len - un.q_len + un.tok0 + si * p.tpt + 1;
             const int32_t limit = min(whole + qtok, un.len);
-            int32_t t0 = un.tile0 * kPfTok;   // first token of the tile
+            int32_t t0 = un.tile0 * kPfTok + half * kCols;   // first token of the half tile
             float ref = -INFINITY, sum = 0.f;
-            const uint64_t scale2 = pack_f32(p.scale_log2, p.scale_log2);
-            const float hidden = p.scale_log2 < 0.f ? INFINITY : -INFINITY;   // -inf once scaled
-            if (seq >= 0) {
 #pragma unroll 1
-                for (int32_t j = 0; j < cnt; ++j, t0 += kPfTok) {
-                    ok = mbar_wait_warp(&sm.s_full[si], ns & 1);
-                    if (!ok) break;
-                    ++ns;
-                    tmem_fence_after_sync();
-                    const bool masked = t0 + kPfTok > whole;
-                    // z = score - reference in log2 units, in pairs; once more, with O
-                    // rescaled, when a row's reference moves (the scores stay in tensor
-                    // memory until P overwrites them)
-                    uint64_t z[kPfTok / 2];
+            for (int32_t j = 0; j < cnt; ++j, t0 += kPfTok) {
+                ok = mbar_wait_warp(&sm.s_full[si], ns & 1);
+                ++ns;
+                tmem_fence_after_sync();
+                const bool masked = t0 + kCols > whole;
+                // z = score - reference in log2 units, in pairs; once more, with O rescaled,
+                // when a row's reference moves (the scores stay in tensor memory until P
+                // overwrites them)
+                uint64_t z[kCols / 2];
 #pragma unroll 1
-                    for (int pass = 0;; ++pass) {
-                        const float nref = ref == -INFINITY ? 0.f : -ref;
-                        const uint64_t nref2 = pack_f32(nref, nref);
-                        {
-                            float x[kPfTok];
-#pragma unroll
-                            for (int c = 0; c < kPfTok / 32; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
-                            tmem_wait_ld();
-                            if (masked) {
-                                const int32_t seen = limit - t0;
-#pragma unroll
-                                for (int c = 0; c < kPfTok; ++c) x[c] = c < seen ? x[c] : hidden;
-                            }
-#pragma unroll
-                            for (int c = 0; c < kPfTok / 2; ++c)
-                                z[c] = fma_x2(pack_f32(x[2 * c], x[2 * c + 1]), scale2, nref2);
-                        }
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int c = 0; c < kPfTok / 2; ++c) {
-                            float a, b;
-                            unpack_f32(z[c], a, b);
-                            mx[c & 3] = max3(mx[c & 3], a, b);
-                        }
-                        const float m = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                        const bool move = m > kRefSlack || (ref == -INFINITY && m > -INFINITY);
-                        if (!__any_sync(0xffffffffu, move) || pass == 1) break;
-                        const float next = move ? m - nref : ref;
-                        const float a = move ? fast_exp2(ref - next) : 1.f;
-                        sum *= a;
-                        ref = next;
-                        if (j > 0) {
-                            // (the wait for S has also seen the previous tile's PV complete)
-#pragma unroll 1
-                            for (int h = 0; h < D / 32; ++h) {
-                                float o[32];
-                                tmem_ld32(to + 32 * h, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) o[c] *= a;
-                                tmem_st32(to + 32 * h, reinterpret_cast<const uint32_t*>(o));
-                            }
-                        }
-                    }
-                    uint64_t s2[2] = {0ull, 0ull};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[kPfTok / 4];
-#pragma unroll
-                        for (int c = 0; c < kPfTok / 4; ++c) {
-                            float a, b;
-                            unpack_f32(z[h * (kPfTok / 4) + c], a, b);
-                            a = fast_exp2(a);
-                            b = fast_exp2(b);
-                            s2[c & 1] = add_x2(s2[c & 1], pack_f32(a, b));
-                            w[c] = pack2<C::kBf16>(a, b);
-                        }
-                        tmem_st32(ts + h * 32, w);
-                    }
+                for (int pass = 0;; ++pass) {
+                    const float nref = ref == -INFINITY ? 0.f : -ref;
+                    const uint64_t nref2 = pack_f32(nref, nref);
                     {
+                        float x[kCols];
+#pragma unroll
+                        for (int c = 0; c < kCols / 32; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
+                        tmem_wait_ld();
+                        if (masked) {
+                            const int32_t seen = limit - t0;
+#pragma unroll
+                            for (int c = 0; c < kCols; ++c) x[c] = c < seen ? x[c] : hidden;
+                        }
+#pragma unroll
+                        for (int c = 0; c < kCols / 2; ++c)
+                            z[c] = fma_x2(pack_f32(x[2 * c], x[2 * c + 1]), scale2, nref2);
+                    }
+                    if (pass == 1) break;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < kCols / 2; ++c) {
                         float a, b;
-                        unpack_f32(add_x2(s2[0], s2[1]), a, b);
-                        sum += a + b;
+                        unpack_f32(z[c], a, b);
+                        mx[c & 3] = max3(mx[c & 3], a, b);
                     }
-                    tmem_wait_st();
-                    tmem_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_full[si]);
-                }
-                // ---- the item's rows
-                if (ok && cnt > 0) {
-                    ok = mbar_wait_warp(&sm.o_full[si], no & 1);
-                    if (ok) {
-                        ++no;
-                        tmem_fence_after_sync();
+                    float m = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    auto moves = [&](float x) { return x > kRefSlack || (ref == -INFINITY && x > -INFINITY); };
+                    if (!consumers_any(!ok || moves(m), kStreamThreads, bar)) break;
+                    // rare: some row's reference moves, or a wait gave up
+                    sm.red[si][half][row] = m;
+                    failed = consumers_any(!ok, kStreamThreads, bar);
+                    if (failed) break;
+                    m = fmaxf(m, sm.red[si][half ^ 1][row]);
+                    const bool move = moves(m);
+                    const float next = move ? m - nref : ref;
+                    const float a = move ? fast_exp2(ref - next) : 1.f;
+                    sum *= a;
+                    ref = next;
+                    if (j > 0 && __any_sync(0xffffffffu, move)) {
+                        // (the wait for S has also seen the previous tile's PV complete)
+#pragma unroll 1
+                        for (int h = 0; h < kDims / 32; ++h) {
+                            float o[32];
+                            tmem_ld32(to + 32 * h, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] *= a;
+                            tmem_st32(to + 32 * h, reinterpret_cast<const uint32_t*>(o));
+                        }
                     }
                 }
+                if (failed) break;
+                uint64_t s2[2] = {0ull, 0ull};
+                {
+                    uint32_t w[kCols / 2];
+#pragma unroll
+                    for (int c = 0; c < kCols / 2; ++c) {
+                        float a, b;
+                        unpack_f32(z[c], a, b);
+                        a = fast_exp2(a);
+                        b = fast_exp2(b);
+                        s2[c & 1] = add_x2(s2[c & 1], pack_f32(a, b));
+                        w[c] = pack2<C::kBf16>(a, b);
+                    }
+                    tmem_st32(ts, w);
+                }
+                {
+                    float a, b;
+                    unpack_f32(add_x2(s2[0], s2[1]), a, b);
+                    sum += a + b;
+                }
+                tmem_wait_st();
+                tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[si][half]);
             }
-            // the four warps of the stream stop together
-            if (consumers_any(!ok, 128, kBarStream + si)) {
-                if (lane == 0) fail();
+            if (failed) break;
+            // ---- the item's rows
+            if (cnt > 0) {
+                ok = mbar_wait_warp(&sm.o_full[si], no & 1);
+                ++no;
+                tmem_fence_after_sync();
+            }
+            sm.red[si][half][row] = sum;
+            if (consumers_any(!ok, kStreamThreads, bar)) {
+                failed = true;
                 break;
             }
-            if (seq < 0) break;
+            sum += sm.red[si][half ^ 1][row];   // (two terms: the same sum in both halves)
             const Unit u = un;
             const int32_t tok = u.tok0 + si * p.tpt + qtok;
             const bool mine = qtok < p.tpt && tok < u.q_len;
-            const bool nonfinite = sm.any_nonfinite[us] != 0;
-            const size_t orow = ((size_t)(u.q_start + tok) * p.num_q_heads + (size_t)u.kvh * G + row % G) * D;
             // infinite and NaN values that were kept out of the products, for the rows that
             // see them
-            if (nonfinite && cnt > 0) {
+            if (sm.any_nonfinite[us] && cnt > 0) {
 #pragma unroll 1
-                for (int d = 0; d < D; ++d) {
+                for (int d = 0; d < kDims; ++d) {
                     float o = tmem_ld1(to + d);
-                    if (sm.nonfinite[us][0][d] < limit) o += INFINITY;
-                    if (sm.nonfinite[us][1][d] < limit) o -= INFINITY;
-                    if (sm.nonfinite[us][2][d] < limit) o = __int_as_float(0x7fc00000);
+                    const int32_t* const first = &sm.nonfinite[us][0][half * kDims + d];
+                    if (first[0] < limit) o += INFINITY;
+                    if (first[D] < limit) o -= INFINITY;
+                    if (first[2 * D] < limit) o = __int_as_float(0x7fc00000);
                     tmem_st1(to + d, o);
                 }
             }
@@ -855,7 +878,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto store_row = [&](int h, const float (&o)[32], float f) {
-                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow + 32 * h);
+                const size_t orow =
+                    ((size_t)(u.q_start + tok) * p.num_q_heads + (size_t)u.kvh * G + row % G) * D;
+                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow +
+                                                      half * kDims + 32 * h);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     dst[k] = make_uint4(pack2<C::kQBf16>(o[8 * k] * f, o[8 * k + 1] * f),
@@ -863,48 +889,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         pack2<C::kQBf16>(o[8 * k + 4] * f, o[8 * k + 5] * f),
                                         pack2<C::kQBf16>(o[8 * k + 6] * f, o[8 * k + 7] * f));
             };
-            if (u.nparts == 1) {
-                const float f = sum == 0.f ? 0.f : p.out_scale / sum;
-#pragma unroll 1
-                for (int h = 0; h < D / 32; ++h) {
-                    float o[32];
-                    load_o(h, o);
-                    if (mine) store_row(h, o, f);
-                }
+            // these warps are done with the item's O and its slot
+            auto release = [&]() {
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
                     if (cnt > 0) mbar_arrive(&sm.o_free[si]);
                     mbar_arrive(&sm.u_empty[us]);
                 }
+            };
+            if (u.nparts == 1) {
+                const float f = sum == 0.f ? 0.f : p.out_scale / sum;
+#pragma unroll 1
+                for (int h = 0; h < kDims / 32; ++h) {
+                    float o[32];
+                    load_o(h, o);
+                    if (mine) store_row(h, o, f);
+                }
+                release();
             } else {
                 // partial rows, [dim][row] so that a warp's accesses are contiguous
                 auto place = [&](int part) {
                     return (((size_t)(u.slot0 + part) * Hkv + u.kvh) * 2 + si) * kPfRows;
                 };
+                auto cell = [&](size_t at, int d) { return at * D + (size_t)(half * kDims + d) * kPfRows + row; };
                 const size_t at = place(u.part);
 #pragma unroll 1
-                for (int h = 0; h < D / 32; ++h) {
+                for (int h = 0; h < kDims / 32; ++h) {
                     float o[32];
                     load_o(h, o);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) p.part_acc[at * D + (32 * h + c) * kPfRows + row] = o[c];
+                    for (int c = 0; c < 32; ++c) p.part_acc[cell(at, 32 * h + c)] = o[c];
                 }
-                p.part_ml[at + row] = make_float2(ref, sum);
-                tmem_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if (cnt > 0) mbar_arrive(&sm.o_free[si]);
-                    mbar_arrive(&sm.u_empty[us]);
-                }
+                if (half == 0) p.part_ml[at + row] = make_float2(ref, sum);
+                release();
                 // the stream that finishes the row tile's last partition joins them, always
                 // in the order of the partitions
                 __threadfence();
-                named_bar_sync(kBarStream + si, 128);
-                if (row == 0)
+                named_bar_sync(bar, kStreamThreads);
+                if (row == 0 && half == 0)
                     sm.last_part[si] =
                         atomicAdd(&p.arrive[((size_t)u.split * Hkv + u.kvh) * 2 + si], 1) == u.nparts - 1;
-                named_bar_sync(kBarStream + si, 128);
+                named_bar_sync(bar, kStreamThreads);
                 if (sm.last_part[si]) {
                     __threadfence();
                     float M = -INFINITY;
@@ -918,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float f = den == 0.f ? 0.f : p.out_scale / den;
 #pragma unroll 1
-                    for (int h = 0; h < D / 32; ++h) {
+                    for (int h = 0; h < kDims / 32; ++h) {
                         float o[32];
 #pragma unroll
                         for (int c = 0; c < 32; ++c) o[c] = 0.f;
@@ -928,14 +954,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float wq = state_weight(__ldcg(&p.part_ml[pr + row]).x, M);
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                o[c] = fmaf(wq, __ldcg(&p.part_acc[pr * D + (32 * h + c) * kPfRows + row]), o[c]);
+                                o[c] = fmaf(wq, __ldcg(&p.part_acc[cell(pr, 32 * h + c)]), o[c]);
                         }
                         if (mine) store_row(h, o, f);
                     }
                 }
-                named_bar_sync(kBarStream + si, 128);   // last_part is reused
             }
         }
+        if (failed && lane == 0) fail();
     }
 
     __syncthreads();
