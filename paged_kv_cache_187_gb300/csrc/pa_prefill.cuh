@@ -757,50 +757,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ns;
                 tmem_fence_after_sync();
                 const bool masked = t0 + kCols > whole;
-                // z = score - reference in log2 units, in pairs; once more, with O rescaled,
-                // when a row's reference moves (the scores stay in tensor memory until P
-                // overwrites them)
-                uint64_t z[kCols / 2];
-#pragma unroll 1
-                for (int pass = 0;; ++pass) {
-                    const float nref = ref == -INFINITY ? 0.f : -ref;
-                    const uint64_t nref2 = pack_f32(nref, nref);
-                    {
-                        float x[kCols];
+                const int32_t seen = limit - t0;
+                // 32 of the row's 64 scores, masked
+                auto scores = [&](int h, float (&x)[32]) {
+                    tmem_ld32(ts + 32 * h, x);
+                    tmem_wait_ld();
+                    if (masked) {
 #pragma unroll
-                        for (int c = 0; c < kCols / 32; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
-                        tmem_wait_ld();
-                        if (masked) {
-                            const int32_t seen = limit - t0;
-#pragma unroll
-                            for (int c = 0; c < kCols; ++c) x[c] = c < seen ? x[c] : hidden;
-                        }
-#pragma unroll
-                        for (int c = 0; c < kCols / 2; ++c)
-                            z[c] = fma_x2(pack_f32(x[2 * c], x[2 * c + 1]), scale2, nref2);
+                        for (int c = 0; c < 32; ++c) x[c] = 32 * h + c < seen ? x[c] : hidden;
                     }
-                    if (pass == 1) break;
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < kCols / 2; ++c) {
-                        float a, b;
-                        unpack_f32(z[c], a, b);
-                        mx[c & 3] = max3(mx[c & 3], a, b);
-                    }
-                    float m = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                    auto moves = [&](float x) { return x > kRefSlack || (ref == -INFINITY && x > -INFINITY); };
-                    if (!consumers_any(!ok || moves(m), kStreamThreads, bar)) break;
-                    // rare: some row's reference moves, or a wait gave up
+                };
+                // Moves the references that a score passes by too much (m: this thread's
+                // largest exponent), in both threads of a row, and rescales O.
+                auto settle = [&](float m) {
                     sm.red[si][half][row] = m;
                     failed = consumers_any(!ok, kStreamThreads, bar);
-                    if (failed) break;
                     m = fmaxf(m, sm.red[si][half ^ 1][row]);
-                    const bool move = moves(m);
-                    const float next = move ? m - nref : ref;
+                    const bool move = m > kRefSlack || (ref == -INFINITY && m > -INFINITY);
+                    const float next = move ? (ref == -INFINITY ? m : m + ref) : ref;
                     const float a = move ? fast_exp2(ref - next) : 1.f;
                     sum *= a;
                     ref = next;
-                    if (j > 0 && __any_sync(0xffffffffu, move)) {
+                    if (j > 0 && __any_sync(0xffffffffu, move) && !failed) {
                         // (the wait for S has also seen the previous tile's PV complete)
 #pragma unroll 1
                         for (int h = 0; h < kDims / 32; ++h) {
@@ -812,27 +790,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st32(to + 32 * h, reinterpret_cast<const uint32_t*>(o));
                         }
                     }
-                }
-                if (failed) break;
-                uint64_t s2[2] = {0ull, 0ull};
-                {
-                    uint32_t w[kCols / 2];
+                };
+                if (j == 0) {
+                    // an item's first tile: the references are the rows' largest scores
+                    float m = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < kCols / 32; ++h) {
+                        float x[32];
+                        scores(h, x);
 #pragma unroll
-                    for (int c = 0; c < kCols / 2; ++c) {
-                        float a, b;
-                        unpack_f32(z[c], a, b);
-                        a = fast_exp2(a);
-                        b = fast_exp2(b);
-                        s2[c & 1] = add_x2(s2[c & 1], pack_f32(a, b));
-                        w[c] = pack2<C::kBf16>(a, b);
+                        for (int c = 0; c < 32; ++c) m = fmaxf(m, x[c] * p.scale_log2);
                     }
-                    tmem_st32(ts, w);
+                    settle(m);
+                    if (failed) break;
                 }
-                {
+                // Weights against the present reference, and their largest exponent, in one
+                // go; should a row's reference have to move, they are thrown away and taken
+                // once more (the scores stay in tensor memory until P overwrites them).
+                uint32_t w[kCols / 2];
+                float tile_sum;
+#pragma unroll 1
+                for (bool again = j == 0;; again = true) {
+                    const float nref = ref == -INFINITY ? 0.f : -ref;
+                    const uint64_t nref2 = pack_f32(nref, nref);
+                    float mx[2] = {-INFINITY, -INFINITY};
+                    uint64_t s2[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int h = 0; h < kCols / 32; ++h) {
+                        float x[32];
+                        scores(h, x);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            float a, b;
+                            unpack_f32(fma_x2(pack_f32(x[2 * c], x[2 * c + 1]), scale2, nref2), a, b);
+                            mx[c & 1] = max3(mx[c & 1], a, b);
+                            a = fast_exp2(a);
+                            b = fast_exp2(b);
+                            s2[c & 1] = add_x2(s2[c & 1], pack_f32(a, b));
+                            w[16 * h + c] = pack2<C::kBf16>(a, b);
+                        }
+                    }
                     float a, b;
                     unpack_f32(add_x2(s2[0], s2[1]), a, b);
-                    sum += a + b;
+                    tile_sum = a + b;
+                    if (again) break;
+                    const float m = fmaxf(mx[0], mx[1]);
+                    const bool move = m > kRefSlack || (ref == -INFINITY && m > -INFINITY);
+                    if (!consumers_any(!ok || move, kStreamThreads, bar)) break;
+                    settle(m);   // rare
+                    if (failed) break;
                 }
+                if (failed) break;
+                sum += tile_sum;
+                tmem_st32(ts, w);
                 tmem_wait_st();
                 tmem_fence_before_sync();
                 __syncwarp();
