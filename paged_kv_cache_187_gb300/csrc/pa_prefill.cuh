@@ -29,7 +29,7 @@
 // that token get the value added at the end.
 //
 // Warps: 0-7 and 8-15 softmax and epilogue of streams 0 and 1, two threads per row; 16
-// producer (claims items, TMA of Q, K and V); 17 MMA issuer; 20-23 fix V tiles (16-bit
+// producer (claims items, TMA of Q and K); 17 MMA issuer; 18 TMA of V; 19 waits for tiles; 20-23 fix V tiles (16-bit
 // caches), or widen the fp8 K/V tiles to fp16 and fix them.  Every wait is bounded; the
 // warps of a stream decide together whether to stop.
 #pragma once
@@ -40,7 +40,7 @@
 namespace pa {
 namespace pf {
 
-constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpFix0 = 20;
+constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpLoadV = 18, kWarpReady = 19, kWarpFix0 = 20;
 constexpr int kThreads = 768;
 constexpr int kStreamThreads = 256;    // two warpgroups of softmax per stream
 constexpr int kBarStream = 1;          // named barriers 1, 2: the warps of a stream
@@ -87,8 +87,8 @@ struct alignas(1024) Smem {
     // behind from one that is ready.
     uint64_t kv_full[C::NST], kv_raw[C::NST], kv_fixed[C::NST], kv_empty[C::NST];
     uint64_t kv8_full[C::N8 ? C::N8 : 1], kv8_empty[C::N8 ? C::N8 : 1];
-    uint64_t q_full, q_ready, q_empty;
-    uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];
+    uint64_t q_full, q_ready, q_empty, item_ready;
+    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
     float red[2][2][kPfRows];          // [stream][half][row]: maxima, or weight sums
     uint64_t u_full[2], u_empty[2], drain;
     Unit unit[2];
@@ -258,14 +258,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_ready, 4);
         mbar_init(&sm.q_empty, 1);
+        mbar_init(&sm.item_ready, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i][0], 4);
-            mbar_init(&sm.p_full[i][1], 4);
+            mbar_init(&sm.p_full[i], 9);     // 8 softmax warps and the readiness warp
             mbar_init(&sm.o_full[i], 1);
             mbar_init(&sm.o_free[i], 8);
             mbar_init(&sm.u_full[i], 1);
-            mbar_init(&sm.u_empty[i], 21);   // MMA warp, 16 softmax warps, 4 fixing warps
+            mbar_init(&sm.u_empty[i], 23);   // V, MMA, readiness, 16 softmax warps, 4 fixing warps
             sm.any_nonfinite[i] = 1;         // the producer clears the tables first
         }
         mbar_init(&sm.drain, 1);
@@ -293,12 +293,85 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kWarpLoad && warp < kWarpFix0) {
         warpgroup_reg_release<kRegAux>();
+        // ---------------------------------------------------------------- loads
+        // Block-table entries of an item, 32 at a time, one per lane; an entry outside the
+        // pool becomes a row past the tensor map (TMA reads zeros).
+        auto entries = [&](int32_t seq, int32_t first, int32_t end) {
+            int32_t phys = p.num_blocks;
+            if (first + lane < end) {
+                phys = p.block_tables[(size_t)seq * p.max_blocks_per_seq + first + lane];
+                if (phys < 0 || phys >= p.num_blocks) {
+                    flag_error(p.status, PA_DEVERR_BAD_BLOCK_);
+                    phys = p.num_blocks;
+                }
+            }
+            return phys;
+        };
+        // The K (V) tiles of an item, ring places n0, n0 + 2, ..; one lane issues the copies,
+        // all from values the whole warp agrees on (copies issued lane by lane took 90 cycles
+        // each, and bounded the kernel).  `phase`: bit s, parity of this warp's next copy on
+        // stage s; V tiles from fix0 on land on kv_raw (16-bit caches).
+        constexpr uint32_t kRing = C::kKv8 ? C::N8 : C::NST;
+        auto load_tiles = [&](const CUtensorMap* map, uint32_t n0, int32_t nt, int32_t seq, int32_t kvh,
+                              int32_t tile0, int32_t len, int32_t fix0, uint32_t& full_phase,
+                              uint32_t& raw_phase) {
+            const int32_t nb0 = tile0 * C::BLOCKS;
+            const int32_t nb1 = min(nb0 + nt * C::BLOCKS, (len + C::BS - 1) / C::BS);
+            int32_t chunk = 0, cur = entries(seq, nb0, nb1), nxt = entries(seq, nb0 + 32, nb1);
+            uint32_t n = n0;
+#pragma unroll 1
+            for (int32_t j = 0; j < nt; ++j, n += 2) {
+                const int32_t tb = j * C::BLOCKS;
+                if ((tb >> 5) != chunk) {
+                    chunk = tb >> 5;
+                    cur = nxt;
+                    nxt = entries(seq, nb0 + 32 * (chunk + 1), nb1);
+                }
+                const uint32_t st = n % kRing;
+                const bool raw = !C::kKv8 && j >= fix0;
+                uint64_t* const full = C::kKv8 ? &sm.kv8_full[st] : raw ? &sm.kv_raw[st] : &sm.kv_full[st];
+                if (!mbar_wait_warp(C::kKv8 ? &sm.kv8_empty[st] : &sm.kv_empty[st], ((n / kRing) & 1) ^ 1))
+                    return false;
+                int32_t y[C::BLOCKS];
+#pragma unroll
+                for (int b = 0; b < C::BLOCKS; ++b)
+                    y[b] = (__shfl_sync(0xffffffffu, cur, (tb & 31) + b) * Hkv + kvh) * C::BS;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full, C::kKv8 ? C::TILE8 : C::TILE);
+                    uint8_t* const dst = C::kKv8 ? sm.kv8[st] : sm.kv[st];
+#pragma unroll
+                    for (int b = 0; b < C::BLOCKS; ++b)
+#pragma unroll
+                        for (int h = 0; h < (C::kKv8 ? 1 : C::HALVES); ++h)
+                            tma_load_2d_keep(dst + h * C::HALF + b * C::BS * 128, map, h * 64, y[b], full);
+                }
+                __syncwarp();
+                if (raw) raw_phase ^= 1u << st;
+                else full_phase ^= 1u << st;
+            }
+            return true;
+        };
+        // After an abort, copies may still be landing: waits (bounded) for this warp's last
+        // ones, at ring places before `end`.  (The fp8 ring is odd, so its stages change
+        // hands, and a wait there may run to its limit.)
+        auto settle_copies = [&](uint32_t full_phase, uint32_t raw_phase, uint32_t end) {
+            if (lane != 0 || !sm.abort) return;
+            for (uint32_t k = 2; k <= 2 * kRing && k <= end; k += 2) {
+                const uint32_t n = end - k, st = n % kRing;
+                if (C::kKv8) {
+                    (void)mbar_wait(&sm.kv8_full[st], (n / kRing) & 1);
+                } else {
+                    (void)mbar_wait(&sm.kv_full[st], ((full_phase >> st) & 1) ^ 1);
+                    (void)mbar_wait(&sm.kv_raw[st], ((raw_phase >> st) & 1) ^ 1);
+                }
+            }
+        };
         if (warp == kWarpLoad) {
-            // ------------------------------------------------------------ producer
+            // ---------------------------------------- items, Q and K tiles
             const int32_t total = (int32_t)p.hdr->total_items;
             int32_t w = (int32_t)blockIdx.x;
-            uint32_t kt = 0, nq = 0;   // K/V tiles and Q loads issued
-            uint32_t full_phase = 0, raw_phase = 0;   // bit s: parity of stage s's next such tile
+            uint32_t kt = 0, nq = 0;   // ring places and Q loads used
+            uint32_t full_phase = 0, raw_phase = 0;
             bool ok = true;
             for (uint32_t it = 0; ok; ++it) {
                 const uint32_t us = it & 1;
@@ -370,79 +443,96 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                     if (ok) ++nq;
                 }
-                // block-table entries, 32 at a time, one per lane, the next 32 in flight; an
-                // entry outside the pool becomes a row past the tensor map (TMA reads zeros)
-                const int32_t nb0 = u.tile0 * C::BLOCKS;
-                const int32_t nb1 = min(nb0 + nt * C::BLOCKS, (u.len + C::BS - 1) / C::BS);
-                auto entries = [&](int32_t first) {
-                    int32_t phys = p.num_blocks;
-                    if (first + lane < nb1) {
-                        phys = p.block_tables[(size_t)u.seq * p.max_blocks_per_seq + first + lane];
-                        if (phys < 0 || phys >= p.num_blocks) {
-                            flag_error(p.status, PA_DEVERR_BAD_BLOCK_);
-                            phys = p.num_blocks;
-                        }
-                    }
-                    return phys;
-                };
-                int32_t chunk = 0, cur = p.num_blocks, nxt = p.num_blocks;
-                if (nt > 0) {
-                    cur = entries(nb0);
-                    nxt = entries(nb0 + 32);
-                }
-                for (int32_t j = 0; j < nt && ok; ++j) {
-                    const int32_t tb = j * C::BLOCKS;
-                    if ((tb >> 5) != chunk) {
-                        chunk = tb >> 5;
-                        cur = nxt;
-                        nxt = entries(nb0 + 32 * (chunk + 1));
-                    }
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (!ok) break;
-                        const uint32_t ns = C::kKv8 ? C::N8 : C::NST;
-                        const uint32_t st = kt % ns, ph = ((kt / ns) & 1) ^ 1;
-                        const bool raw = !C::kKv8 && kv == 1 && j >= u.fix0;
-                        uint64_t* const full =
-                            C::kKv8 ? &sm.kv8_full[st] : raw ? &sm.kv_raw[st] : &sm.kv_full[st];
-                        uint64_t* const empty = C::kKv8 ? &sm.kv8_empty[st] : &sm.kv_empty[st];
-                        if (lane == 0) {
-                            ok = mbar_wait(empty, ph);
-                            if (ok) mbar_arrive_expect_tx(full, C::kKv8 ? C::TILE8 : C::TILE);
-                        }
-                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                        if (!ok) break;
-                        __syncwarp();   // the expected bytes are posted before any copy
-                        constexpr int kCopies = C::kKv8 ? C::BLOCKS : C::BLOCKS * C::HALVES;
-                        const int b = C::kKv8 ? lane % C::BLOCKS : (lane / C::HALVES) % C::BLOCKS;
-                        const int h = C::kKv8 ? 0 : lane % C::HALVES;
-                        const int32_t pb = __shfl_sync(0xffffffffu, cur, (tb & 31) + b);
-                        if (lane < kCopies) {
-                            const int32_t y = (pb * Hkv + u.kvh) * C::BS;
-                            uint8_t* const dst = C::kKv8 ? sm.kv8[st] + b * C::BS * 128
-                                                         : sm.kv[st] + h * C::HALF + b * C::BS * 128;
-                            tma_load_2d_keep(dst, kv == 0 ? &kmap : &vmap, h * 64, y, full);
-                        }
-                        ++kt;
-                        if (raw) raw_phase ^= 1u << st;
-                        else full_phase ^= 1u << st;
-                    }
-                }
+                if (ok && nt > 0)
+                    ok = load_tiles(&kmap, kt, nt, u.seq, u.kvh, u.tile0, u.len, nt, full_phase, raw_phase);
+                kt += 2 * nt;
                 w = __shfl_sync(0xffffffffu, claimed, 0);
             }
             if (!ok && lane == 0) fail();
-            // after an abort, copies may still be landing: wait (bounded) for all of them
-            if (lane == 0 && sm.abort) {
-                // (the last copy on each barrier has the parity before its next)
-                for (uint32_t st = 0; st < (uint32_t)(C::kKv8 ? C::N8 : C::NST); ++st) {
-                    (void)mbar_wait(C::kKv8 ? &sm.kv8_full[st] : &sm.kv_full[st],
-                                    ((full_phase >> st) & 1) ^ 1);
-                    if (!C::kKv8) (void)mbar_wait(&sm.kv_raw[st], ((raw_phase >> st) & 1) ^ 1);
-                }
-                if (nq > 0) (void)mbar_wait(&sm.q_full, (nq - 1) & 1);
-            }
+            settle_copies(full_phase, raw_phase, kt);
+            if (lane == 0 && sm.abort && nq > 0) (void)mbar_wait(&sm.q_full, (nq - 1) & 1);
             __syncwarp();
-        } else if (warp == kWarpMma) {
+        } else if (warp == kWarpLoadV) {
+            // ---------------------------------------- V tiles
+            uint32_t kt = 0, full_phase = 0, raw_phase = 0;
+            bool ok = true;
+            for (uint32_t it = 0; ok; ++it) {
+                const uint32_t us = it & 1;
+                ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
+                if (!ok) break;
+                const int32_t seq = __shfl_sync(0xffffffffu, sm.unit[us].seq, 0);
+                const int32_t kvh = __shfl_sync(0xffffffffu, sm.unit[us].kvh, 0);
+                const int32_t tile0 = __shfl_sync(0xffffffffu, sm.unit[us].tile0, 0);
+                const int32_t len = __shfl_sync(0xffffffffu, sm.unit[us].len, 0);
+                const int32_t fix0 = __shfl_sync(0xffffffffu, sm.unit[us].fix0, 0);
+                const int32_t nt = __shfl_sync(0xffffffffu, max(sm.unit[us].cnt[0], sm.unit[us].cnt[1]), 0);
+                if (lane == 0) mbar_arrive(&sm.u_empty[us]);
+                if (seq < 0) break;
+                if (nt > 0)
+                    ok = load_tiles(&vmap, kt + 1, nt, seq, kvh, tile0, len, fix0, full_phase, raw_phase);
+                kt += 2 * nt;
+            }
+            if (!ok && lane == 0) fail();
+            settle_copies(full_phase, raw_phase, kt + 1);
+            __syncwarp();
+        } else if (warp == kWarpReady) {
+            // ------------------------------------------------------------ readiness
+            // Waits in the MMA warp's stead for everything but the weights: for Q, the first
+            // K tile, then per tile its V, the next K and (first tile) the stream's O, and
+            // adds its arrival to the weights'.  A wait costs the MMA warp 130-200 cycles even
+            // when it is over; now it has one per stream and tile.
+            uint32_t st = 0, q_phase = 0;             // next stage of the ring; parity of q
+            uint32_t full_phase = 0, fix_phase = 0;   // bit s: parity of stage s's next such tile
+            uint32_t p_phase = 0x3, o_phase = 0;      // bit i: parities of stream i (P: the last one)
+            bool ok = true;
+            auto next = [](uint32_t x) { return x + 1 == C::NST ? 0u : x + 1; };
+            auto wait_kv = [&](uint32_t x, bool fixed) {
+                const uint32_t phase = fixed ? fix_phase : full_phase;
+                const bool here = mbar_wait_warp(fixed ? &sm.kv_fixed[x] : &sm.kv_full[x], (phase >> x) & 1);
+                if (fixed) fix_phase ^= 1u << x;
+                else full_phase ^= 1u << x;
+                return here;
+            };
+#pragma unroll 1
+            for (uint32_t it = 0; ok; ++it) {
+                const uint32_t us = it & 1;
+                ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
+                if (!ok) break;
+                const int32_t seq = sm.unit[us].seq, fix0 = sm.unit[us].fix0;
+                const int32_t cnt0 = sm.unit[us].cnt[0], cnt1 = sm.unit[us].cnt[1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.u_empty[us]);
+                if (seq < 0) break;
+                const int32_t nt = max(cnt0, cnt1);
+                if (nt == 0) continue;
+                ok = mbar_wait_warp(C::kKv8 && C::kQBf16 ? &sm.q_ready : &sm.q_full, q_phase);
+                q_phase ^= 1;
+                if (ok) ok = wait_kv(st, false);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&sm.item_ready);
+#pragma unroll 1
+                for (int32_t j = 0; j < nt && ok; ++j) {
+                    const uint32_t vs = next(st), kn = next(vs);
+                    ok = wait_kv(vs, !C::kKv8 && j >= fix0);
+                    if (ok && j + 1 < nt) ok = wait_kv(kn, false);
+#pragma unroll 1
+                    for (uint32_t i = 0; i < 2 && ok; ++i) {
+                        if (j >= (i ? cnt1 : cnt0)) continue;
+                        if (j == 0) {
+                            ok = mbar_wait_warp(&sm.o_free[i], ((o_phase >> i) & 1) ^ 1);
+                            o_phase ^= 1u << i;
+                        }
+                        // (the arrival belongs to this tile's phase: the last one is over)
+                        if (ok) ok = mbar_wait_warp(&sm.p_full[i], (p_phase >> i) & 1);
+                        p_phase ^= 1u << i;
+                        if (ok && lane == 0) mbar_arrive(&sm.p_full[i]);
+                    }
+                    st = kn;
+                }
+            }
+            if (!ok && lane == 0) fail();
+            __syncwarp();
+        } else {
             // ------------------------------------------------------------ MMA issuer
             // The whole warp runs the loop and one elected lane issues: with every value the
             // same in all lanes, descriptors stay in uniform registers, and a product step
@@ -453,45 +543,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t k_lo = desc_lo(smem_u32(sm.kv[0]), 16);
             const uint32_t v_lo = desc_lo(smem_u32(sm.kv[0]), C::HALF);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            uint32_t st = 0, q_phase = 0;             // next stage of the ring; parity of q
-            uint32_t full_phase = 0, fix_phase = 0;   // bit s: parity of stage s's next such tile
-            uint32_t p_phase = 0, o_phase = 0;        // bit i: parities of stream i
+            uint32_t st = 0, i_phase = 0;             // next stage of the ring; items begun
+            uint32_t p_phase = 0;                     // bit i: parity of stream i
             bool ok = true;
             auto next = [](uint32_t x) { return x + 1 == C::NST ? 0u : x + 1; };
-            auto wait_kv = [&](uint32_t x, bool fixed) {
-                const uint32_t phase = fixed ? fix_phase : full_phase;
-                const bool here = mbar_wait_warp(fixed ? &sm.kv_fixed[x] : &sm.kv_full[x], (phase >> x) & 1);
-                if (fixed) fix_phase ^= 1u << x;
-                else full_phase ^= 1u << x;
-                return here;
-            };
-            auto commit = [&](uint64_t* bar) {
-                if (elect_one()) mma_commit(bar);
-            };
-            // S of stream i = Q K^T with the K tile of stage x
+            // (one lane) S of stream i = Q K^T with the K tile of stage x
             auto qk = [&](uint32_t i, uint32_t x) {
                 const uint32_t a = q_lo + i * (C::TILE >> 4), b = k_lo + x * (C::TILE >> 4);
                 const uint32_t d = tm + C::COL_S + i * kPfTok;
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k >> 2) * C::HALF + (k & 3) * 32) >> 4;
-                        mma_ss(d, a + off, b + off, kIdQK, k > 0);
-                    }
-                    mma_commit(&sm.s_full[i]);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * C::HALF + (k & 3) * 32) >> 4;
+                    mma_ss(d, a + off, b + off, kIdQK, k > 0);
                 }
+                mma_commit(&sm.s_full[i]);
             };
-            // O of stream i += P V, half h of the V tile of stage x (P of half h sits where
-            // that half's scores were)
-            auto pv = [&](uint32_t i, uint32_t x, uint32_t h, bool first) {
-                const uint32_t a = tm + C::COL_S + i * kPfTok + h * (kPfTok / 2);
-                const uint32_t b = v_lo + x * (C::TILE >> 4) + h * (8192 >> 4);
+            // (one lane) O of stream i += P V with the V tile of stage x; P of either half of
+            // the tokens sits where that half's scores were
+            auto pv = [&](uint32_t i, uint32_t x, uint32_t more) {
+                const uint32_t a = tm + C::COL_S + i * kPfTok, b = v_lo + x * (C::TILE >> 4);
                 const uint32_t d = tm + C::COL_O + i * D;
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kPfTok / 32; ++k)
-                        mma_ts(d, a + 8 * k, b + k * (2048 >> 4), kIdPV, k > 0 ? 1u : (first ? 0u : 1u));
-                }
+                for (int k = 0; k < kPfTok / 16; ++k)
+                    mma_ts(d, a + 8 * (k & 3) + (k >> 2) * (kPfTok / 2), b + k * (2048 >> 4), kIdPV,
+                           k > 0 ? 1u : more);
             };
 #pragma unroll 1
             for (uint32_t it = 0; ok; ++it) {
@@ -499,68 +574,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
                 if (!ok) break;
                 const int32_t seq = __shfl_sync(0xffffffffu, sm.unit[us].seq, 0);
-                const int32_t fix0 = __shfl_sync(0xffffffffu, sm.unit[us].fix0, 0);
                 const int32_t cnt0 = __shfl_sync(0xffffffffu, sm.unit[us].cnt[0], 0);
                 const int32_t cnt1 = __shfl_sync(0xffffffffu, sm.unit[us].cnt[1], 0);
                 if (lane == 0) mbar_arrive(&sm.u_empty[us]);
                 if (seq < 0) break;
                 const int32_t nt = max(cnt0, cnt1);
                 if (nt == 0) continue;
-                ok = mbar_wait_warp(C::kKv8 && C::kQBf16 ? &sm.q_ready : &sm.q_full, q_phase);
-                q_phase ^= 1;
-                if (ok) ok = wait_kv(st, false);
+                ok = mbar_wait_warp(&sm.item_ready, i_phase);
+                i_phase ^= 1;
                 if (!ok) break;
                 // tile j's K sits in stage ks, its V in the next one
                 uint32_t ks = st;
                 tmem_fence_after_sync();
-                if (cnt0 > 0) qk(0, ks);
-                if (cnt1 > 0) qk(1, ks);
-                commit(&sm.kv_empty[ks]);
-                if (nt == 1) commit(&sm.q_empty);
+                if (elect_one()) {
+                    if (cnt0 > 0) qk(0, ks);
+                    if (cnt1 > 0) qk(1, ks);
+                    mma_commit(&sm.kv_empty[ks]);
+                    if (nt == 1) mma_commit(&sm.q_empty);
+                }
+                // per tile: PV of each stream and its next QK^T, with nothing to wait for in
+                // between
 #pragma unroll 1
-                for (int32_t j = 0; j < nt && ok; ++j) {
+                for (int32_t j = 0; j < nt; ++j) {
                     const uint32_t vs = next(ks), kn = next(vs);
-                    // the streams that take this tile: from i0, up to i1
-                    const uint32_t i0 = j < cnt0 ? 0 : 1, i1 = j < cnt1 ? 1 : 0;
-                    ok = wait_kv(vs, !C::kKv8 && j >= fix0);
-                    bool k_here = false;
+                    const uint32_t last = j < cnt1 ? 1 : 0;
 #pragma unroll 1
-                    for (uint32_t i = i0; i <= i1 && ok; ++i) {
-                        ok = mbar_wait_warp(&sm.p_full[i][0], (p_phase >> i) & 1);
-                        if (ok && j == 0) ok = mbar_wait_warp(&sm.o_free[i], ((o_phase >> i) & 1) ^ 1);
+                    for (uint32_t i = j < cnt0 ? 0 : 1; i <= last; ++i) {
+                        const bool more = j + 1 < (i ? cnt1 : cnt0);
+                        ok = mbar_wait_warp(&sm.p_full[i], (p_phase >> i) & 1);
                         if (!ok) break;
                         tmem_fence_after_sync();
-                        pv(i, vs, 0, j == 0);
-                        ok = mbar_wait_warp(&sm.p_full[i][1], (p_phase >> i) & 1);
-                        if (!ok) break;
-                        p_phase ^= 1u << i;
-                        tmem_fence_after_sync();
-                        pv(i, vs, 1, false);
-                        if (i == i1) commit(&sm.kv_empty[vs]);
-                        if (j + 1 < (i ? cnt1 : cnt0)) {
-                            if (!k_here) {
-                                ok = wait_kv(kn, false);
-                                k_here = true;
-                                if (!ok) break;
-                                tmem_fence_after_sync();
+                        if (elect_one()) {
+                            pv(i, vs, (uint32_t)j);
+                            if (i == last) mma_commit(&sm.kv_empty[vs]);
+                            if (more) qk(i, kn);
+                            else mma_commit(&sm.o_full[i]);
+                            if (i == last) {
+                                if (j + 1 < nt) mma_commit(&sm.kv_empty[kn]);
+                                if (j + 2 == nt) mma_commit(&sm.q_empty);
                             }
-                            qk(i, kn);
-                            if (i == (j + 1 < cnt1 ? 1u : 0u)) {
-                                commit(&sm.kv_empty[kn]);
-                                if (j + 2 == nt) commit(&sm.q_empty);
-                            }
-                        } else {
-                            commit(&sm.o_full[i]);
-                            o_phase ^= 1u << i;
                         }
+                        p_phase ^= 1u << i;
                     }
+                    if (!ok) break;
                     ks = kn;
                 }
                 st = ks;
             }
             if (!ok && lane == 0) fail();
             // every MMA of this warp has completed before tensor memory is freed
-            commit(&sm.drain);
+            if (elect_one()) mma_commit(&sm.drain);
             (void)mbar_wait_warp(&sm.drain, 0);
             __syncwarp();
         }
@@ -846,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tmem_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[si][half]);
+                if (lane == 0) mbar_arrive(&sm.p_full[si]);
             }
             if (failed) break;
             // ---- the item's rows
