@@ -16,31 +16,26 @@ constexpr int32_t kPfRows = 128;
 constexpr int32_t kPfTok = 128;
 // The grid never has more CTAs than this (one per SM); the workspace is sized for it.
 constexpr int32_t kPfMaxGrid = 160;
-// Shortest partition of a context, in 128-token tiles.
-constexpr int32_t kPfMinPart = 2;
+// What an item costs beside its tiles (Q, the first scores, the rows' output), in tiles.
+constexpr int32_t kPfItemCost = 2;
+// Shortest share of the work, in tiles, worth a CTA of its own when contexts are cut.
+constexpr int32_t kPfMinShare = 6;
 
-// Head of the prefill workspace, written by the plan kernel.
+// Head of the prefill workspace, written by the plan kernel.  A row tile is a run of up to
+// 2 * tpt new tokens of a sequence; a unit is a row tile with one kv head, of as many
+// 128-token tiles as its last row sees; its cost is its tiles + kPfItemCost.
+//   cut 0: whole units, claimed one by one, longest row tiles first (`order`).
+//   cut 1: the units' costs laid end to end (row tile by row tile, kv heads innermost) are
+//          cut into `shares` equal stretches, one per CTA, so that all finish together.
+//          Share b starts at floor(b * cost / shares); a unit belongs to the share in which
+//          its cost for beginning ends, and goes on into the next ones.
 struct PfHeader {
-    uint32_t counter;       // items claimed past the first gridDim.x
-    uint32_t total_items;   // list entries * num_kv_heads
-    uint32_t pad[62];
-};
-
-// One entry of the work list: a partition of the context of one row tile (the query rows
-// of up to 2 * tokens_per_stream new tokens of a sequence), for every kv head.
-struct alignas(16) PfEntry {
-    int32_t seq;       // sequence (block-table row)
-    int32_t len;       // context length, clamped
-    int32_t q_start;   // first row of the sequence's chunk in query / out
-    int32_t q_len;     // new tokens of the sequence
-    int32_t tok0;      // first new token of the row tile, counted within the chunk
-    int32_t tile0;     // first 128-token tile of the partition
-    int32_t tile1;     // one past its last tile
-    int32_t nparts;    // partitions of this row tile
-    int32_t part;      // which of them
-    int32_t slot0;     // first partial-result slot of the row tile (nparts > 1)
-    int32_t split;     // index among the row tiles with several partitions
-    int32_t pad;
+    uint32_t counter;       // units claimed past the first gridDim.x (cut 0)
+    uint32_t total_units;   // row tiles * num_kv_heads
+    uint32_t cut;
+    uint32_t shares;
+    int64_t cost;           // all units'
+    uint32_t pad[58];
 };
 
 struct PrefillParams {
@@ -56,20 +51,23 @@ struct PrefillParams {
     float out_scale;           // v_scale for fp8 caches, else 1
     int32_t grid;              // CTAs of the attention launch
     int32_t max_row_tiles;     // what the workspace has room for
-    int32_t max_entries;
-    int32_t max_slots;
     PfHeader* hdr;
     int4* seqs;                // [num_seqs] (q_start, q_len, len, first row tile)
-    PfEntry* list;             // [max_entries]
-    int32_t* arrive;           // [split row tiles][num_kv_heads][2 streams]
-    float2* part_ml;           // [slot][kv head][stream][128] (reference, weight sum)
-    float* part_acc;           // [slot][kv head][stream][head_size][128]
+    int32_t* seq_of;           // [row tiles] the sequence
+    int32_t* order;            // [row tiles] longest first
+    int64_t* before;           // [row tiles + 1] cost of the row tiles before, one kv head
+    int32_t* arrive;           // [CTAs][2 streams] finished partitions of the unit that a
+                               // share leaves unfinished
+    float2* part_ml;           // [CTAs][2][2 streams][128] (reference, weight sum): a share
+                               // holds the end of a unit begun before it, and the beginning
+                               // of one that goes on
+    float* part_acc;           // [CTAs][2][2 streams][head_size][128]
     int32_t* status;
 };
 
 struct PfWorkspace {
-    size_t hdr, seqs, list, arrive, part_ml, part_acc, total;
-    int32_t max_row_tiles, max_entries, max_slots;
+    size_t hdr, seqs, seq_of, order, before, arrive, part_ml, part_acc, total;
+    int32_t max_row_tiles;
 };
 PfWorkspace prefill_workspace(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
                               int32_t num_kv_heads, int32_t head_size, int32_t max_context_len);

@@ -45,24 +45,19 @@ __device__ __forceinline__ int32_t block_scan(int32_t x, int32_t* buf, int32_t* 
 constexpr int kPlanThreads = 512;
 constexpr int kBuckets = 256;
 
-// Cuts a ragged batch into the work list of the attention kernel.  Row tiles are the runs
-// of up to 2 * tpt new tokens of a sequence; a row tile needs the 128-token tiles up to the
-// last token its last row sees.  When there are too few row tiles to fill the CTAs, long
-// ones are cut into equal partitions of the context, none longer than the mean work per
-// CTA.  Longest items first, so that the last ones handed out are the cheapest.
+// Lists the row tiles of a ragged batch and settles how the attention kernel shares them
+// out (see PfHeader).  Whole units are claimed longest first, which leaves the shortest for
+// the end; where the longest unit is more than half of a CTA's share of the work (few or
+// long units), the work is cut into equal shares instead, whatever the units' ends.
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillParams p) {
     __shared__ int32_t buf[32];
     __shared__ int32_t hist[kBuckets], first[kBuckets];
-    __shared__ unsigned long long work;
     __shared__ int32_t longest;
     allow_dependent_launch();
     grid_dependency_wait();
     const int32_t tid = threadIdx.x, span = 2 * p.tpt;
     if (tid < kBuckets) hist[tid] = 0;
-    if (tid == 0) {
-        work = 0;
-        longest = 0;
-    }
+    if (tid == 0) longest = 0;
     // the sequences: chunk, context, first row tile; bad metadata is clamped and reported
     int32_t row_tiles = 0;
     const int64_t row_cap = (int64_t)p.max_blocks_per_seq * p.block_size;
@@ -90,91 +85,63 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
         row_tiles = p.max_row_tiles;
     }
     __syncthreads();
-    // row tile i: its sequence (the last whose first row tile is at or before i) and tiles
-    auto locate = [&](int32_t i, int4& q, int32_t& s, int32_t& tok0) {
-        int32_t a = 0, b = p.num_seqs;
-        while (b - a > 1) {
-            const int32_t m = (a + b) >> 1;
-            if (p.seqs[m].w <= i) a = m;
-            else b = m;
-        }
-        s = a;
-        q = p.seqs[a];
-        tok0 = (i - q.w) * span;
-        const int32_t last = min(tok0 + span, q.y);
+    // row tile i: its sequence (the last whose first row tile is at or before i), and the
+    // tiles it needs, up to the last token its last row sees
+    auto tiles_of = [&](int32_t i, int32_t s) {
+        const int4 q = p.seqs[s];
+        const int32_t last = min((i - q.w + 1) * span, q.y);
         return (max(q.z - q.y + last, 0) + kPfTok - 1) / kPfTok;
     };
-    int4 q;
-    int32_t s, tok0;
-    {
-        unsigned long long mine = 0;
-        int32_t most = 0;
-        for (int32_t i = tid; i < row_tiles; i += kPlanThreads) {
-            const int32_t n = locate(i, q, s, tok0);
-            mine += (unsigned)n;
-            most = max(most, n);
+    long long cost = 0;
+    for (int32_t base = 0; base < row_tiles; base += kPlanThreads) {
+        const int32_t i = base + tid;
+        int32_t n = 0;
+        if (i < row_tiles) {
+            int32_t a = 0, b = p.num_seqs;
+            while (b - a > 1) {
+                const int32_t m = (a + b) >> 1;
+                if (p.seqs[m].w <= i) a = m;
+                else b = m;
+            }
+            p.seq_of[i] = a;
+            n = tiles_of(i, a);
+            if (n > 0) atomicMax(&longest, n);
+            n += kPfItemCost;
         }
-        if (mine) atomicAdd(&work, mine);
-        if (most) atomicMax(&longest, most);
+        int32_t sum;      // (512 row tiles of at most 2^24 tiles each: below 2^31 by far in use,
+                          // and a context of 2^31 tokens is 2^24 tiles)
+        const int32_t at = block_scan(min(n, 1 << 21), buf, &sum);
+        if (i < row_tiles) p.before[i] = cost + at;
+        cost += sum;
     }
+    if (tid == 0) p.before[row_tiles] = cost;
     __syncthreads();
-    const unsigned long long all = work * (unsigned long long)p.num_kv_heads;
-    const int32_t P =
-        (int32_t)max((unsigned long long)kPfMinPart, min((all + p.grid - 1) / p.grid, 1ull << 28));
-    auto parts_of = [&](int32_t n) { return n <= P ? 1 : (n + P - 1) / P; };
-    const int32_t scale = min(longest, P) + 1;
-    auto bucket = [&](int32_t n, int32_t np) {
-        return kBuckets - 1 - min(kBuckets - 1, (int32_t)((int64_t)((n + np - 1) / np) * kBuckets / scale));
-    };
-    for (int32_t i = tid; i < row_tiles; i += kPlanThreads) {
-        const int32_t n = locate(i, q, s, tok0), np = parts_of(n);
-        atomicAdd(&hist[bucket(n, np)], np);
-    }
-    __syncthreads();
-    {
+    const long long units = (long long)row_tiles * p.num_kv_heads, all = cost * p.num_kv_heads;
+    // shares: all CTAs, unless that makes them too short to be worth it
+    const long long shares = max(1ll, min((long long)p.grid, max(units, all / kPfMinShare)));
+    const bool cut = longest > 1 && 2 * (longest + kPfItemCost) * shares > all && units > 0;
+    if (!cut) {
+        const int32_t scale = longest + 1;
+        auto bucket = [&](int32_t n) {
+            return kBuckets - 1 - min(kBuckets - 1, (int32_t)((int64_t)n * kBuckets / scale));
+        };
+        for (int32_t i = tid; i < row_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(tiles_of(i, p.seq_of[i]))], 1);
+        __syncthreads();
         int32_t sum;
         const int32_t at = block_scan(tid < kBuckets ? hist[tid] : 0, buf, &sum);
         if (tid < kBuckets) first[tid] = at;
         __syncthreads();
+        for (int32_t i = tid; i < row_tiles; i += kPlanThreads)
+            p.order[atomicAdd(&first[bucket(tiles_of(i, p.seq_of[i]))], 1)] = i;
+    } else {
+        for (int32_t i = tid; i < 2 * p.grid; i += kPlanThreads) p.arrive[i] = 0;
     }
-    int32_t slots = 0, splits = 0;
-    for (int32_t base = 0; base < row_tiles; base += kPlanThreads) {
-        const int32_t i = base + tid;
-        int32_t n = 0, np = 0;
-        if (i < row_tiles) {
-            n = locate(i, q, s, tok0);
-            np = parts_of(n);
-        }
-        int32_t ss, us;
-        const int32_t slot0 = slots + block_scan(np > 1 ? np : 0, buf, &ss);
-        const int32_t split = splits + block_scan(np > 1 ? 1 : 0, buf, &us);
-        if (i < row_tiles) {
-            const int32_t pos = atomicAdd(&first[bucket(n, np)], np);
-            for (int32_t k = 0; k < np; ++k) {
-                PfEntry e;
-                e.seq = s;
-                e.len = q.z;
-                e.q_start = q.x;
-                e.q_len = q.y;
-                e.tok0 = tok0;
-                e.tile0 = (int32_t)((int64_t)n * k / np);
-                e.tile1 = (int32_t)((int64_t)n * (k + 1) / np);
-                e.nparts = np;
-                e.part = k;
-                e.slot0 = slot0;
-                e.split = split;
-                e.pad = 0;
-                p.list[pos + k] = e;
-            }
-        }
-        slots += ss;
-        splits += us;
-    }
-    const int32_t counters = splits * p.num_kv_heads * 2;
-    for (int32_t i = tid; i < counters; i += kPlanThreads) p.arrive[i] = 0;
     if (tid == 0) {
         p.hdr->counter = 0;
-        p.hdr->total_items = (uint32_t)((row_tiles - splits + slots) * p.num_kv_heads);
+        p.hdr->total_units = (uint32_t)units;
+        p.hdr->cut = cut ? 1 : 0;
+        p.hdr->shares = (uint32_t)shares;
+        p.hdr->cost = all;
     }
 }
 

@@ -134,7 +134,7 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
         return fail(PA_ERR_INVALID_ARG, "prefill: device buffers must be 16-byte aligned");
     const pa::PfWorkspace L = pa::prefill_workspace(a.num_tokens, a.num_seqs, a.num_q_heads,
                                                     a.num_kv_heads, a.head_size, a.max_context_len);
-    if ((int64_t)L.max_entries * a.num_kv_heads > INT32_MAX)
+    if ((int64_t)L.max_row_tiles * a.num_kv_heads > INT32_MAX)
         return fail(PA_ERR_UNSUPPORTED, "prefill: too many work items");
     if (!ws || ws_bytes < L.total)
         return fail(PA_ERR_WORKSPACE, "prefill: workspace of %zu bytes, need %zu", ws_bytes, L.total);
@@ -167,14 +167,16 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
     if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = std::copysign(1e-30f, scale);
     p.out_scale = a.kv8 ? a.v_scale : 1.f;
     p.max_row_tiles = L.max_row_tiles;
-    p.max_entries = L.max_entries;
-    p.max_slots = L.max_slots;
-    p.grid = (int32_t)std::min<int64_t>(std::min(sms, pa::kPfMaxGrid),
-                                        (int64_t)L.max_entries * a.num_kv_heads);
+    // one CTA per SM, but never more than tiles
+    const int64_t tiles = (int64_t)L.max_row_tiles * a.num_kv_heads *
+                          std::max(1, (a.max_context_len + pa::kPfTok - 1) / pa::kPfTok);
+    p.grid = (int32_t)std::min<int64_t>(std::min(sms, pa::kPfMaxGrid), tiles);
     uint8_t* w = static_cast<uint8_t*>(ws);
     p.hdr = reinterpret_cast<pa::PfHeader*>(w + L.hdr);
     p.seqs = reinterpret_cast<int4*>(w + L.seqs);
-    p.list = reinterpret_cast<pa::PfEntry*>(w + L.list);
+    p.seq_of = reinterpret_cast<int32_t*>(w + L.seq_of);
+    p.order = reinterpret_cast<int32_t*>(w + L.order);
+    p.before = reinterpret_cast<int64_t*>(w + L.before);
     p.arrive = reinterpret_cast<int32_t*>(w + L.arrive);
     p.part_ml = reinterpret_cast<float2*>(w + L.part_ml);
     p.part_acc = reinterpret_cast<float*>(w + L.part_acc);
@@ -287,30 +289,29 @@ pa::RopeParams rope_params(void* query_out, const void* query, const void* key, 
 
 namespace pa {
 
-// Row tiles: at most one more than full ones per sequence that has tokens.  Partitions are
-// never shorter than the mean work per CTA, so the partial slots of all kv heads are fewer
-// than twice the CTAs (see prefill_plan_kernel).
+// Row tiles: at most one more than full ones per sequence that has tokens.
 PfWorkspace prefill_workspace(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
                               int32_t num_kv_heads, int32_t head_size, int32_t max_context_len) {
     PfWorkspace L;
     const int32_t group = std::max(1, num_q_heads / num_kv_heads);
     const int32_t span = 2 * std::max(1, kPfRows / group);
     L.max_row_tiles = num_tokens / span + std::min(num_seqs, num_tokens);
-    L.max_slots = max_context_len > kPfMinPart * kPfTok ? 2 * kPfMaxGrid / num_kv_heads + 1 : 0;
-    L.max_entries = L.max_row_tiles + L.max_slots;
+    // no unit is cut whose context is a single tile
+    const size_t parts = max_context_len > kPfTok ? (size_t)kPfMaxGrid * 2 * 2 * kPfRows : 0;
     size_t off = 0;
-    L.hdr = off;
-    off = align256(off + sizeof(PfHeader));
-    L.seqs = off;
-    off = align256(off + sizeof(int4) * (size_t)num_seqs);
-    L.list = off;
-    off = align256(off + sizeof(PfEntry) * (size_t)L.max_entries);
-    L.arrive = off;
-    off = align256(off + sizeof(int32_t) * 2 * (size_t)L.max_slots * num_kv_heads);
-    L.part_ml = off;
-    off = align256(off + sizeof(float2) * 2 * kPfRows * (size_t)L.max_slots * num_kv_heads);
-    L.part_acc = off;
-    off = align256(off + sizeof(float) * 2 * kPfRows * (size_t)L.max_slots * num_kv_heads * head_size);
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align256(off + bytes);
+        return at;
+    };
+    L.hdr = take(sizeof(PfHeader));
+    L.seqs = take(sizeof(int4) * (size_t)num_seqs);
+    L.seq_of = take(sizeof(int32_t) * (size_t)L.max_row_tiles);
+    L.order = take(sizeof(int32_t) * (size_t)L.max_row_tiles);
+    L.before = take(sizeof(int64_t) * ((size_t)L.max_row_tiles + 1));
+    L.arrive = take(sizeof(int32_t) * 2 * kPfMaxGrid);
+    L.part_ml = take(sizeof(float2) * parts);
+    L.part_acc = take(sizeof(float) * parts * head_size);
     L.total = off;
     return L;
 }

@@ -72,8 +72,9 @@ struct Unit {
     int32_t kvh, len, q_start, q_len, tok0, tile0;
     int32_t cnt[2];       // tiles each stream needs
     int32_t fix0;         // tiles at or past this one (within the item) are fixed
-    int32_t nparts, part, slot0, split;
-    int32_t pad[2];
+    int32_t nparts, part; // the unit's partitions, and which of them this is
+    int32_t first;        // the share (CTA) that holds partition 0
+    int32_t pad[3];
 };
 
 template <class C>
@@ -87,7 +88,7 @@ struct alignas(1024) Smem {
     // behind from one that is ready.
     uint64_t kv_full[C::NST], kv_raw[C::NST], kv_fixed[C::NST], kv_empty[C::NST];
     uint64_t kv8_full[C::N8 ? C::N8 : 1], kv8_empty[C::N8 ? C::N8 : 1];
-    uint64_t q_full, q_ready, q_empty, item_ready;
+    uint64_t q_full, q_ready, q_empty, item_ready, k_ready;
     uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
     float red[2][2][kPfRows];          // [stream][half][row]: maxima, or weight sums
     uint64_t u_full[2], u_empty[2], drain;
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.q_ready, 4);
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.item_ready, 1);
+        mbar_init(&sm.k_ready, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 9);     // 8 softmax warps and the readiness warp
@@ -368,46 +370,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (warp == kWarpLoad) {
             // ---------------------------------------- items, Q and K tiles
-            const int32_t total = (int32_t)p.hdr->total_items;
+            const PfHeader hdr = *p.hdr;
+            const int64_t shares = hdr.shares;
+            // cut 0: the unit to take next; cut 1: the cost at which this share goes on, and
+            // where it ends
             int32_t w = (int32_t)blockIdx.x;
+            auto share_at = [&](int64_t b) { return b * hdr.cost / shares; };
+            int64_t at = 0, end = 0;
+            int32_t here = 0;
+            if (hdr.cut && w < (int32_t)hdr.shares) {
+                at = share_at(w);
+                end = share_at(w + 1);
+            }
             uint32_t kt = 0, nq = 0;   // ring places and Q loads used
             uint32_t full_phase = 0, raw_phase = 0;
             bool ok = true;
             for (uint32_t it = 0; ok; ++it) {
                 const uint32_t us = it & 1;
-                if (lane == 0) ok = mbar_wait(&sm.u_empty[us], ((it >> 1) & 1) ^ 1);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                ok = mbar_wait_warp(&sm.u_empty[us], ((it >> 1) & 1) ^ 1);
                 if (!ok) break;
-                const bool done = w >= total || warp_sees_abort(sm.abort);
-                int32_t claimed = total;
-                if (!done && lane == 0)
-                    claimed = (int32_t)(gridDim.x + atomicAdd(&p.hdr->counter, 1u));
+                // the next unit: row tile and kv head, and (cut 1) the tiles of this share
                 Unit u;
                 u.seq = -1;
                 u.cnt[0] = u.cnt[1] = 0;
-                if (!done) {
-                    const PfEntry e = p.list[w / Hkv];
-                    u.seq = e.seq;
-                    u.kvh = w % Hkv;
-                    u.len = e.len;
-                    u.q_start = e.q_start;
-                    u.q_len = e.q_len;
-                    u.tok0 = e.tok0;
-                    u.tile0 = e.tile0;
-                    u.nparts = e.nparts;
-                    u.part = e.part;
-                    u.slot0 = e.slot0;
-                    u.split = e.split;
-                    u.pad[0] = u.pad[1] = 0;
+                u.nparts = 1;
+                u.part = u.first = 0;
+                u.pad[0] = u.pad[1] = u.pad[2] = 0;
+                int32_t claimed = 0, rt = -1, tile0 = 0, tile1 = kNoToken;
+                if (warp_sees_abort(sm.abort)) {
+                } else if (!hdr.cut) {
+                    if (w < (int32_t)hdr.total_units) {
+                        if (lane == 0) claimed = (int32_t)(gridDim.x + atomicAdd(&p.hdr->counter, 1u));
+                        rt = p.order[w / Hkv];
+                        u.kvh = w % Hkv;
+                    }
+                } else {
+                    // (a share may be used up by the beginning of a unit that belongs to the
+                    // next one)
+                    if (at < end) do {
+                        // row tile: the last one whose units begin at or before `at`
+                        int32_t a = here;
+                        if (it == 0) {
+                            int32_t b = (int32_t)(hdr.total_units / (uint32_t)Hkv);
+                            while (b - a > 1) {
+                                const int32_t m = (a + b) >> 1;
+                                if (p.before[m] * Hkv <= at) a = m;
+                                else b = m;
+                            }
+                        } else if (p.before[a + 1] * Hkv <= at) {
+                            ++a;
+                        }
+                        here = a;
+                        const int64_t len = p.before[a + 1] - p.before[a];   // a unit's cost
+                        const int64_t in = at - p.before[a] * Hkv;
+                        const int32_t kvh = (int32_t)(in / len);
+                        const int64_t begin = p.before[a] * Hkv + kvh * len;
+                        const int64_t body = begin + kPfItemCost;            // its first tile
+                        if (end <= body && end < begin + len) {
+                            at = end;                                        // the next share's
+                            break;
+                        }
+                        // shares that begin inside the unit's tiles: lo, lo + 1, .. hi
+                        const int64_t lo = ((body + 1) * shares + hdr.cost - 1) / hdr.cost;
+                        const int64_t hi = ((begin + len) * shares - 1) / hdr.cost;
+                        rt = a;
+                        u.kvh = kvh;
+                        u.nparts = (int32_t)max(hi - lo + 1, (int64_t)0) + 1;
+                        u.first = (int32_t)(u.nparts > 1 ? lo - 1 : w);
+                        u.part = w - u.first;
+                        tile0 = at > body ? (int32_t)(at - body) : 0;
+                        tile1 = end < begin + len ? (int32_t)(end - body) : kNoToken;
+                        at = min(begin + len, end);
+                    } while (false);
+                }
+                if (rt >= 0) {
+                    u.seq = p.seq_of[rt];
+                    const int4 q = p.seqs[u.seq];
+                    u.q_start = q.x;
+                    u.q_len = q.y;
+                    u.len = q.z;
+                    u.tok0 = (rt - q.w) * 2 * p.tpt;
+                    u.tile0 = tile0;
                     // tiles a stream needs: up to the last token its last row sees
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int32_t a = e.tok0 + i * p.tpt, b = min(a + p.tpt, e.q_len);
-                        const int32_t n = a < e.q_len ? max(e.len - e.q_len + b, 0) : 0;
-                        u.cnt[i] = max(min((n + kPfTok - 1) / kPfTok, e.tile1) - e.tile0, 0);
+                        const int32_t a = u.tok0 + i * p.tpt, b = min(a + p.tpt, u.q_len);
+                        const int32_t n = a < u.q_len ? max(u.len - u.q_len + b, 0) : 0;
+                        u.cnt[i] = max(min((n + kPfTok - 1) / kPfTok, tile1) - tile0, 0);
                     }
                     // first tile that some row does not see whole
-                    u.fix0 = max(e.len - e.q_len + e.tok0 + 1, 0) / kPfTok - e.tile0;
+                    u.fix0 = max(u.len - u.q_len + u.tok0 + 1, 0) / kPfTok - tile0;
                 }
                 // no one reads the table of two items ago any more
                 if (sm.any_nonfinite[us]) {
@@ -446,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && nt > 0)
                     ok = load_tiles(&kmap, kt, nt, u.seq, u.kvh, u.tile0, u.len, nt, full_phase, raw_phase);
                 kt += 2 * nt;
-                w = __shfl_sync(0xffffffffu, claimed, 0);
+                if (!hdr.cut) w = __shfl_sync(0xffffffffu, claimed, 0);
             }
             if (!ok && lane == 0) fail();
             settle_copies(full_phase, raw_phase, kt);
@@ -514,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int32_t j = 0; j < nt && ok; ++j) {
                     const uint32_t vs = next(st), kn = next(vs);
                     ok = wait_kv(vs, !C::kKv8 && j >= fix0);
-                    if (ok && j + 1 < nt) ok = wait_kv(kn, false);
+                    if (!C::kKv8 && ok && j + 1 < nt) ok = wait_kv(kn, false);
 #pragma unroll 1
                     for (uint32_t i = 0; i < 2 && ok; ++i) {
                         if (j >= (i ? cnt1 : cnt0)) continue;
@@ -526,6 +578,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (ok) ok = mbar_wait_warp(&sm.p_full[i], (p_phase >> i) & 1);
                         p_phase ^= 1u << i;
                         if (ok && lane == 0) mbar_arrive(&sm.p_full[i]);
+                    }
+                    // (a widened K tile comes later: its stage is the last V tile's)
+                    if (C::kKv8 && ok && j + 1 < nt) {
+                        ok = wait_kv(kn, false);
+                        if (ok && lane == 0) mbar_arrive(&sm.k_ready);
                     }
                     st = kn;
                 }
@@ -543,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t k_lo = desc_lo(smem_u32(sm.kv[0]), 16);
             const uint32_t v_lo = desc_lo(smem_u32(sm.kv[0]), C::HALF);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            uint32_t st = 0, i_phase = 0;             // next stage of the ring; items begun
+            uint32_t st = 0, i_phase = 0, k_phase = 0;   // next stage of the ring; parities
             uint32_t p_phase = 0;                     // bit i: parity of stream i
             bool ok = true;
             auto next = [](uint32_t x) { return x + 1 == C::NST ? 0u : x + 1; };
@@ -598,21 +655,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int32_t j = 0; j < nt; ++j) {
                     const uint32_t vs = next(ks), kn = next(vs);
                     const uint32_t last = j < cnt1 ? 1 : 0;
+                    bool k_here = false;
 #pragma unroll 1
                     for (uint32_t i = j < cnt0 ? 0 : 1; i <= last; ++i) {
                         const bool more = j + 1 < (i ? cnt1 : cnt0);
                         ok = mbar_wait_warp(&sm.p_full[i], (p_phase >> i) & 1);
                         if (!ok) break;
                         tmem_fence_after_sync();
-                        if (elect_one()) {
-                            pv(i, vs, (uint32_t)j);
+                        // (one lane) what follows PV: the stages given back, the next scores
+                        auto go_on = [&]() {
                             if (i == last) mma_commit(&sm.kv_empty[vs]);
                             if (more) qk(i, kn);
-                            else mma_commit(&sm.o_full[i]);
                             if (i == last) {
                                 if (j + 1 < nt) mma_commit(&sm.kv_empty[kn]);
                                 if (j + 2 == nt) mma_commit(&sm.q_empty);
                             }
+                        };
+                        if (elect_one()) {
+                            pv(i, vs, (uint32_t)j);
+                            if (!more) mma_commit(&sm.o_full[i]);
+                            if (!C::kKv8) go_on();
+                        }
+                        if (C::kKv8) {
+                            // (the V stage is given back after the wait for K: a K tile that
+                            // needs the stage cannot become ready, and complete the barrier's
+                            // next phase, while this one is still waited for)
+                            if (more && !k_here) {
+                                ok = mbar_wait_warp(&sm.k_ready, k_phase);
+                                k_phase ^= 1;
+                                k_here = true;
+                                if (!ok) break;
+                                tmem_fence_after_sync();
+                            }
+                            if (elect_one()) go_on();
                         }
                         p_phase ^= 1u << i;
                     }
@@ -734,39 +809,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const bool fix = (t & 1) && (t >> 1) >= fix0;
                     uint8_t* const dst = sm.kv[st];
-                    // 16 elements per step: lanes 0..7 of a row take its eight 16-byte pieces
-#pragma unroll 4
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = i * 16 + (tid >> 3), c = tid & 7;
-                        uint4 x = *reinterpret_cast<const uint4*>(sm.kv8[s8] + row * 128 + ((c ^ (row & 7)) << 4));
-                        if (fix) {
-                            const int32_t tok = (tile0 + (t >> 1)) * kPfTok + row;
-                            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+                    // 16 elements per step: lanes 0..7 of a row take its eight 16-byte pieces;
+                    // four steps' reads go ahead of their writes, which the compiler could not
+                    // move past one another
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (tok >= len) w[k] = 0;
-                                // a byte of E4M3 is NaN when its low seven bits are all set
-                                const uint32_t nan = ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                                if (nan) {
-                                    for (int b = 0; b < 4; ++b)
-                                        if ((nan >> (8 * b)) & 0x80u) {
-                                            note(16 * c + 4 * k + b, tok, 2);
-                                            w[k] &= ~(0xFFu << (8 * b));
-                                        }
+                    for (int g = 0; g < 2; ++g) {
+                        uint4 x4[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = (4 * g + i) * 16 + (tid >> 3), c = tid & 7;
+                            x4[i] = *reinterpret_cast<const uint4*>(sm.kv8[s8] + row * 128 + ((c ^ (row & 7)) << 4));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = (4 * g + i) * 16 + (tid >> 3), c = tid & 7;
+                            uint4 x = x4[i];
+                            if (fix) {
+                                const int32_t tok = (tile0 + (t >> 1)) * kPfTok + row;
+                                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    if (tok >= len) w[k] = 0;
+                                    // a byte of E4M3 is NaN when its low seven bits are all set
+                                    const uint32_t nan = ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                                    if (nan) {
+#pragma unroll 1
+                                        for (int b = 0; b < 4; ++b)
+                                            if ((nan >> (8 * b)) & 0x80u) {
+                                                note(16 * c + 4 * k + b, tok, 2);
+                                                w[k] &= ~(0xFFu << (8 * b));
+                                            }
+                                    }
                                 }
                             }
+                            uint4 lo, hi;
+                            e4m3x4_to_f16x2x2(x.x, lo.x, lo.y);
+                            e4m3x4_to_f16x2x2(x.y, lo.z, lo.w);
+                            e4m3x4_to_f16x2x2(x.z, hi.x, hi.y);
+                            e4m3x4_to_f16x2x2(x.w, hi.z, hi.w);
+                            // pieces of the second half go out in the other order, so that
+                            // eight lanes always write to eight different bank groups
+                            uint8_t* const r = dst + (c >> 2) * C::HALF + row * 128;
+                            const int c0 = (2 * c) & 7, odd = c >> 2;
+                            *reinterpret_cast<uint4*>(r + (((c0 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+                            *reinterpret_cast<uint4*>(r + (((c0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
                         }
-                        uint4 lo, hi;
-                        e4m3x4_to_f16x2x2(x.x, lo.x, lo.y);
-                        e4m3x4_to_f16x2x2(x.y, lo.z, lo.w);
-                        e4m3x4_to_f16x2x2(x.z, hi.x, hi.y);
-                        e4m3x4_to_f16x2x2(x.w, hi.z, hi.w);
-                        // pieces of the second half go out in the other order, so that eight
-                        // lanes always write to eight different bank groups
-                        uint8_t* const r = dst + (c >> 2) * C::HALF + row * 128;
-                        const int c0 = (2 * c) & 7, odd = c >> 2;
-                        *reinterpret_cast<uint4*>(r + (((c0 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4*>(r + (((c0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -982,8 +1069,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 release();
             } else {
                 // partial rows, [dim][row] so that a warp's accesses are contiguous
+                // (a share's place 1 is for a unit that goes on, 0 for one that came to it)
                 auto place = [&](int part) {
-                    return (((size_t)(u.slot0 + part) * Hkv + u.kvh) * 2 + si) * kPfRows;
+                    return ((size_t)(2 * (u.first + part) + (part == 0)) * 2 + si) * kPfRows;
                 };
                 auto cell = [&](size_t at, int d) { return at * D + (size_t)(half * kDims + d) * kPfRows + row; };
                 const size_t at = place(u.part);
@@ -1002,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 named_bar_sync(bar, kStreamThreads);
                 if (row == 0 && half == 0)
                     sm.last_part[si] =
-                        atomicAdd(&p.arrive[((size_t)u.split * Hkv + u.kvh) * 2 + si], 1) == u.nparts - 1;
+                        atomicAdd(&p.arrive[2 * u.first + si], 1) == u.nparts - 1;
                 named_bar_sync(bar, kStreamThreads);
                 if (sm.last_part[si]) {
                     __threadfence();
