@@ -8,6 +8,7 @@ without the built library raises immediately.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -521,85 +522,112 @@ def pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, h
                                               head_size, max_context_len))
 
 
-def _prefill_sizes(out, query, key_cache, value_cache, block_tables, context_lens, query_starts):
+class _Call:
+    """The device and stream of one call, and its tensors' addresses.  The library launches on
+    the current device, so every tensor has to live there."""
+
+    __slots__ = ("dev",)
+
+    def __init__(self):
+        import torch
+        self.dev = torch._C._cuda_getDevice()
+
+    def stream(self, stream):
+        if stream is None:
+            import torch
+            return torch._C._cuda_getCurrentRawStream(self.dev)
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def here(self, t, name):
+        if t.get_device() != self.dev:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} is on device {t.get_device()}, the current device is "
+                             f"{self.dev}")
+
+    def ptr(self, t, name, dtype):
+        if t.get_device() != self.dev:
+            self.here(t, name)
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def pool8(self, t, name):
+        """An fp8 E4M3 pool: a uint8 or float8_e4m3fn tensor."""
+        import torch
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError(f"{name} must be uint8 / float8_e4m3fn (fp8 E4M3 bytes), got {t.dtype}")
+        return self.ptr(t, name, t.dtype)
+
+    def rows(self, t, name, dtype):
+        """Address and token stride of a [T, H, D] tensor whose rows of one token are dense
+        (a slice of a fused projection, for example)."""
+        if t.get_device() != self.dev:
+            self.here(t, name)
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        T, H, D = t.shape
+        s0, s1, s2 = t.stride()
+        if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
+            raise ValueError(f"{name}: the rows of one token must be dense")
+        return t.data_ptr(), (s0 if T > 1 else H * D)
+
+
+def _prefill(fn, pool, scales, out, query, key_cache, value_cache, block_tables, context_lens,
+             query_starts, max_context_len, scale, workspace, status, stream):
+    import torch
+    i32 = torch.int32
+    c = _Call()
     T, Hq, D = query.shape
     NB, Hkv, bs, D2 = key_cache.shape
+    S = context_lens.shape[0]
     if out.shape != query.shape or value_cache.shape != key_cache.shape or D2 != D:
         raise ValueError("prefill: inconsistent shapes")
-    S = context_lens.shape[0]
     if (context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S
-            or query_starts.shape != (S + 1,)):
+            or query_starts.dim() != 1 or query_starts.shape[0] != S + 1):
         raise ValueError("prefill: block_tables [S, max_blocks], context_lens [S] and "
                          "query_starts [S + 1] expected")
-    if out.dtype != query.dtype:
-        raise TypeError("out dtype differs from query")
-    return T, S, Hq, Hkv, D, bs, NB
+    wp, wb = None, 0
+    if workspace is not None:
+        wp, wb = c.ptr(workspace, "workspace", workspace.dtype), workspace.nbytes
+    qt = query.dtype
+    dt = _dt(query)
+    if pool is None:
+        k, v = c.ptr(key_cache, "key_cache", qt), c.ptr(value_cache, "value_cache", qt)
+    else:
+        k, v = c.pool8(key_cache, "key_cache"), c.pool8(value_cache, "value_cache")
+    _check(fn(
+        c.ptr(out, "out", qt), c.ptr(query, "query", qt), k, v,
+        c.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
+        c.ptr(context_lens, "context_lens", i32), c.ptr(query_starts, "query_starts", i32), T, S, Hq,
+        Hkv, D, bs, NB, max_context_len, scale, *scales, dt, wp, wb,
+        None if status is None else c.ptr(status, "status", i32), c.stream(stream)))
 
 
 def pa_prefill(out, query, key_cache, value_cache, block_tables, context_lens, query_starts,
                max_context_len: int, scale: float, workspace=None, status=None, stream=None):
     """Attention of a ragged chunk of new tokens over the paged cache: query/out [T, Hq, D],
     rows query_starts[s] .. query_starts[s+1]-1 belonging to sequence s's last tokens."""
-    import torch
-    sizes = _prefill_sizes(out, query, key_cache, value_cache, block_tables, context_lens,
-                           query_starts)
-    for t, n in ((key_cache, "key_cache"), (value_cache, "value_cache")):
-        if t.dtype != query.dtype:
-            raise TypeError(f"{n} dtype differs from query")
-    wp, wb = _ws(workspace)
-    _check(_lib.pa_prefill(
-        _dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"),
-        _dev(value_cache, "value_cache"), _dev(block_tables, "block_tables", torch.int32),
-        int(block_tables.shape[1]), _dev(context_lens, "context_lens", torch.int32),
-        _dev(query_starts, "query_starts", torch.int32), *sizes, int(max_context_len), float(scale),
-        _dt(query), wp, wb, _opt_dev(status, "status"), _stream(stream)))
+    _prefill(_lib.pa_prefill, None, (), out, query, key_cache, value_cache, block_tables,
+             context_lens, query_starts, int(max_context_len), float(scale), workspace, status,
+             stream)
 
 
 def pa_prefill_fp8(out, query, key_cache, value_cache, block_tables, context_lens, query_starts,
                    max_context_len: int, scale: float, k_scale: float, v_scale: float,
                    workspace=None, status=None, stream=None):
     """pa_prefill over fp8 E4M3 pools (uint8 or float8_e4m3fn), head_size 128."""
+    _prefill(_lib.pa_prefill_fp8, True, (float(k_scale), float(v_scale)), out, query, key_cache,
+             value_cache, block_tables, context_lens, query_starts, int(max_context_len),
+             float(scale), workspace, status, stream)
+
+
+def _rope(fn, fp8, scales, query_out, query, key, value, key_cache, value_cache, slot_mapping,
+          positions, inv_freq, pair_axes, interleaved, status, stream):
     import torch
-    sizes = _prefill_sizes(out, query, key_cache, value_cache, block_tables, context_lens,
-                           query_starts)
-    wp, wb = _ws(workspace)
-    _check(_lib.pa_prefill_fp8(
-        _dev(out, "out"), _dev(query, "query"), _u8(key_cache, "key_cache"),
-        _u8(value_cache, "value_cache"), _dev(block_tables, "block_tables", torch.int32),
-        int(block_tables.shape[1]), _dev(context_lens, "context_lens", torch.int32),
-        _dev(query_starts, "query_starts", torch.int32), *sizes, int(max_context_len), float(scale),
-        float(k_scale), float(v_scale), _dt(query), wp, wb, _opt_dev(status, "status"),
-        _stream(stream)))
-
-
-def _rows(t, name):
-    """Pointer and token stride of a [T, H, D] CUDA tensor whose rows of one token are dense
-    (a slice of a fused projection, for example)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    T, H, D = t.shape
-    s0, s1, s2 = t.stride()
-    if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
-        raise ValueError(f"{name}: the rows of one token must be dense")
-    return ctypes.c_void_p(t.data_ptr()), (s0 if T > 1 else H * D)
-
-
-_AXES = {}     # pair_axes as the host arrays the C call reads, by their values
-
-
-def _pair_axes(pair_axes):
-    key = tuple(pair_axes)
-    a = _AXES.get(key)
-    if a is None:
-        if len(_AXES) >= 64:
-            _AXES.clear()
-        a = _AXES[key] = _np_i32(key)
-    return a
-
-
-def _rope(fn, query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
-          inv_freq, pair_axes, interleaved, status, stream, pool, scales=()):
-    import torch
+    c = _Call()
     T, Hq, D = query.shape
     Hkv = key.shape[1]
     NB, Hkv2, bs, D2 = key_cache.shape
@@ -610,44 +638,46 @@ def _rope(fn, query_out, query, key, value, key_cache, value_cache, slot_mapping
         raise ValueError("rope_and_cache: slot_mapping [T] and positions [axes, T] expected")
     if inv_freq.dim() != 1:
         raise ValueError("rope_and_cache: inv_freq [rot_dim / 2] expected")
-    for t, n in ((key, "key"), (value, "value"), (query_out, "query_out")):
-        if t.dtype != query.dtype:
-            raise TypeError(f"{n} dtype differs from query")
+    half = inv_freq.shape[0]
     axes = None
     if pair_axes is not None:
-        axes = _pair_axes(pair_axes)
-        if axes.shape != inv_freq.shape:
+        axes = array.array("i", pair_axes)
+        if len(axes) != half:
             raise ValueError("rope_and_cache: pair_axes must name one axis per pair")
-    (qp, qs), (kp, ks), (vp, vs) = _rows(query, "query"), _rows(key, "key"), _rows(value, "value")
+    dt, qt = _dt(query), query.dtype
+    qp, qs = c.rows(query, "query", qt)
+    kp, ks = c.rows(key, "key", qt)
+    vp, vs = c.rows(value, "value", qt)
+    if fp8:
+        kc, vc = c.pool8(key_cache, "key_cache"), c.pool8(value_cache, "value_cache")
+    else:
+        kc, vc = c.ptr(key_cache, "key_cache", qt), c.ptr(value_cache, "value_cache", qt)
     _check(fn(
-        _dev(query_out, "query_out"), qp, kp, vp, qs, ks, vs, pool(key_cache, "key_cache"),
-        pool(value_cache, "value_cache"), _dev(slot_mapping, "slot_mapping", torch.int32),
-        _dev(positions, "positions", torch.int64), int(positions.shape[0]),
-        None if axes is None else _nptr(axes), _dev(inv_freq, "inv_freq", torch.float32),
-        2 * int(inv_freq.shape[0]), 1 if interleaved else 0, T, Hq, Hkv, D, bs, NB, _dt(query),
-        *scales, _opt_dev(status, "status"), _stream(stream)))
+        c.ptr(query_out, "query_out", qt), qp, kp, vp, qs, ks, vs, kc, vc,
+        c.ptr(slot_mapping, "slot_mapping", torch.int32), c.ptr(positions, "positions", torch.int64),
+        positions.shape[0], None if axes is None else axes.buffer_info()[0],
+        c.ptr(inv_freq, "inv_freq", torch.float32), 2 * half, 1 if interleaved else 0, T, Hq, Hkv, D,
+        bs, NB, dt, *scales, None if status is None else c.ptr(status, "status", torch.int32),
+        c.stream(stream)))
 
 
 def pa_rope_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
                       inv_freq, pair_axes=None, interleaved: bool = False, status=None, stream=None):
     """Rotary positions on query/key [T, H, D] and the K/V rows into the pools.  positions
-    int64 [axes, T]; inv_freq fp32 [rot_dim / 2]; pair_axes (a sequence of ints on the host)
-    names the axis of each rotated pair, needed for more than one axis.  query/key/value may
-    be slices of a fused projection; query_out is dense."""
-    for t, n in ((key_cache, "key_cache"), (value_cache, "value_cache")):
-        if t.dtype != query.dtype:
-            raise TypeError(f"{n} dtype differs from query")
-    _rope(_lib.pa_rope_and_cache, query_out, query, key, value, key_cache, value_cache,
-          slot_mapping, positions, inv_freq, pair_axes, interleaved, status, stream, _dev)
+    int64 [axes, T]; inv_freq fp32 [rot_dim / 2]; pair_axes (a sequence of ints on the
+    host) names the axis of each rotated pair, needed for more than
+    one axis.  query/key/value may be slices of a fused projection; query_out is dense."""
+    _rope(_lib.pa_rope_and_cache, False, (), query_out, query, key, value, key_cache, value_cache,
+          slot_mapping, positions, inv_freq, pair_axes, interleaved, status, stream)
 
 
 def pa_rope_and_cache_fp8(query_out, query, key, value, key_cache, value_cache, slot_mapping,
                           positions, inv_freq, k_scale: float, v_scale: float, pair_axes=None,
                           interleaved: bool = False, status=None, stream=None):
     """pa_rope_and_cache into fp8 E4M3 pools (uint8 or float8_e4m3fn)."""
-    _rope(_lib.pa_rope_and_cache_fp8, query_out, query, key, value, key_cache, value_cache,
-          slot_mapping, positions, inv_freq, pair_axes, interleaved, status, stream, _u8,
-          (float(k_scale), float(v_scale)))
+    _rope(_lib.pa_rope_and_cache_fp8, True, (float(k_scale), float(v_scale)), query_out, query, key,
+          value, key_cache, value_cache, slot_mapping, positions, inv_freq, pair_axes, interleaved,
+          status, stream)
 
 
 def pa_move_blocks(key_caches, value_caches, block_pairs, block_tables=None, status=None,
@@ -656,30 +686,35 @@ def pa_move_blocks(key_caches, value_caches, block_pairs, block_tables=None, sta
     on the device, ascending `from`) in every layer's pools (lists of [NB, Hkv, bs, D]
     tensors), and rewrites block_tables (int32 [rows, max_blocks] on the device)."""
     import torch
+    c = _Call()
     L = len(key_caches)
     if L == 0 or len(value_caches) != L:
         raise ValueError("move_blocks: key_caches and value_caches of at least one layer expected")
     if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
         raise ValueError("move_blocks: pairs [n, 2] expected")
     k0 = key_caches[0]
-    NB, Hkv, bs, D = k0.shape
-    pools = (ctypes.c_void_p * (2 * L))()
-    for i, t in enumerate((*key_caches, *value_caches)):
-        if t.shape != k0.shape or t.dtype != k0.dtype:
+    NB, Hkv, bs, D = shape = k0.shape
+    pt = k0.dtype
+    dt = PA_FP8_E4M3 if k0.element_size() == 1 else _dt(k0)
+    if dt == PA_FP8_E4M3:
+        c.pool8(k0, "pool")
+    pools = []
+    for t in (*key_caches, *value_caches):
+        if t.shape != shape:
             raise ValueError("move_blocks: the pools must have one shape and type")
-        pools[i] = _dev(t, "pool").value
-    rows, width = 0, 1
+        pools.append(c.ptr(t, "pool", pt))
+    pools = np.array(pools, dtype=np.uint64)
+    rows, width, tables = 0, 1, None
     if block_tables is not None:
         if block_tables.dim() != 2:
             raise ValueError("move_blocks: block_tables [rows, max_blocks] expected")
         rows, width = block_tables.shape
-    dt = PA_FP8_E4M3 if k0.element_size() == 1 else _dt(k0)
-    base = ctypes.addressof(pools)
+        tables = c.ptr(block_tables, "block_tables", torch.int32)
+    base = pools.ctypes.data
     _check(_lib.pa_move_blocks(
-        ctypes.c_void_p(base), ctypes.c_void_p(base + L * ctypes.sizeof(ctypes.c_void_p)), L,
-        _dev(block_pairs, "block_pairs", torch.int32), int(block_pairs.shape[0]),
-        None if block_tables is None else _dev(block_tables, "block_tables", torch.int32), rows,
-        width, Hkv, D, bs, NB, dt, _opt_dev(status, "status"), _stream(stream)))
+        base, base + 8 * L, L, c.ptr(block_pairs, "block_pairs", torch.int32), block_pairs.shape[0],
+        tables, rows, width, Hkv, D, bs, NB, dt,
+        None if status is None else c.ptr(status, "status", torch.int32), c.stream(stream)))
 
 
 def pa_selftest_wait_timeout(status, limit_us: int, stream=None):

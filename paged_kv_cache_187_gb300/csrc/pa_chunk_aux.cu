@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
 }
 
 // ------------------------------------------------------------------ rotary + cache write
-constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;     // tokens per CTA
+constexpr int kRopeThreads = 128;
+constexpr int kRopeUnits = 4;      // 32-byte units a thread has in flight
 
 // Rotates the query and key rows of new tokens and writes K and V into the pools.
 //
@@ -157,115 +157,140 @@ constexpr int kRopeTokens = 4;     // tokens per CTA
 // left is rounded once, to fp32, so that far positions lose nothing: the fraction is
 // within 2^-53 of itself, 2^-22 radians at position 2^31.
 //
-// A CTA takes kRopeTokens tokens: first the cosines and sines of their pairs, one thread
-// per pair, into shared memory, then 32 bytes of a row per thread and step.
+// A CTA takes a token.  Its rows are cut into 32-byte units (two 16-byte pieces: 8 pairs,
+// or 16 dimensions that do not turn); the first units are on their way while the pairs'
+// cosines and sines are computed, one thread per pair, into shared memory.
 template <bool BF16, bool KV8>
 __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const RopeParams p) {
-    __shared__ float2 turn[kRopeTokens][kMaxRopePairs];
-    __shared__ int32_t slots[kRopeTokens];
+    __shared__ float2 turn[kMaxRopePairs];
     allow_dependent_launch();   // what follows waits for this kernel before it reads the pools
     grid_dependency_wait();
-    const int32_t i0 = blockIdx.x * kRopeTokens;
-    const int32_t n = min(kRopeTokens, p.num_tokens - i0);
-    const int32_t half = p.rot_dim / 2;
-    for (int32_t e = threadIdx.x; e < n * half; e += kRopeThreads) {
-        const int32_t t = e / half, i = e - t * half;
-        double f = (double)p.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+    const int64_t i = blockIdx.x;
+    const int32_t half = p.rot_dim / 2, tid = threadIdx.x;
+    int32_t slot = p.slot_mapping[i];
+    if ((int64_t)slot >= (int64_t)p.num_blocks * p.block_size) {
+        if (tid == 0 && p.status) atomicOr(p.status, kBadSlot);
+        slot = -1;
+    }
+    const int64_t block = slot / p.block_size, offset = slot - block * p.block_size;
+    const uint32_t units = (uint32_t)p.head_size / 16, rot_units = (uint32_t)p.rot_dim / 16;
+    const uint32_t hq = (uint32_t)p.num_q_heads, hk = (uint32_t)p.num_kv_heads;
+    // a padding token's K and V are not written
+    const uint32_t all = (slot < 0 ? hq : hq + 2 * hk) * units;
+    struct Unit {
+        uint32_t kind, head, c;      // 0 query, 1 key, 2 value; head; unit within the row
+        bool rot;
+        uint32_t d0, d1;             // first dimensions of its two pieces
+    };
+    auto unit = [&](uint32_t e) {
+        Unit u;
+        const uint32_t h = units == 1 ? e : __umulhi(e, p.unit_div);
+        u.c = e - h * units;
+        u.kind = h < hq ? 0 : h < hq + hk ? 1 : 2;
+        u.head = u.kind == 0 ? h : u.kind == 1 ? h - hq : h - hq - hk;
+        u.rot = u.kind != 2 && u.c < rot_units;
+        const bool apart = u.rot && !p.interleaved;
+        u.d0 = apart ? 8 * u.c : 16 * u.c;
+        u.d1 = apart ? half + 8 * u.c : 16 * u.c + 8;
+        return u;
+    };
+    uint4 xa[kRopeUnits], xb[kRopeUnits];
+    auto load = [&](uint32_t base) {
+#pragma unroll
+        for (int k = 0; k < kRopeUnits; ++k) {
+            const uint32_t e = base + k * kRopeThreads;
+            if (e >= all) break;
+            const Unit u = unit(e);
+            const uint16_t* src = u.kind == 0   ? static_cast<const uint16_t*>(p.query) + i * p.q_stride
+                                  : u.kind == 1 ? static_cast<const uint16_t*>(p.key) + i * p.k_stride
+                                                : static_cast<const uint16_t*>(p.value) + i * p.v_stride;
+            src += (size_t)u.head * p.head_size;
+            xa[k] = *reinterpret_cast<const uint4*>(src + u.d0);
+            xb[k] = *reinterpret_cast<const uint4*>(src + u.d1);
+        }
+    };
+    load(tid);
+    for (int32_t e = tid; e < half; e += kRopeThreads) {
+        double f = (double)p.inv_freq[e] * 0.15915494309189533577;   // 1 / (2 pi)
         f -= floor(f);
         const unsigned long long step = (unsigned long long)(f * 18446744073709551616.0);
-        const unsigned long long pos =
-            (unsigned long long)p.positions[(int64_t)p.axis[i] * p.num_tokens + i0 + t];
+        const unsigned long long pos = (unsigned long long)p.positions[(int64_t)p.axis[e] * p.num_tokens + i];
         // the upper half, as a signed number of half turns in [-1, 1)
         const float x = (float)(int32_t)((step * pos) >> 32) * 4.656612873077392578125e-10f;
         float sn, cs;
         sincospif(x, &sn, &cs);
-        turn[t][i] = make_float2(cs, sn);
-    }
-    if (threadIdx.x < n) {
-        const int32_t slot = p.slot_mapping[i0 + threadIdx.x];
-        const bool bad = (int64_t)slot >= (int64_t)p.num_blocks * p.block_size;
-        if (bad && p.status) atomicOr(p.status, kBadSlot);
-        slots[threadIdx.x] = bad ? -1 : slot;
+        turn[e] = make_float2(cs, sn);
     }
     __syncthreads();
-    const int32_t units = p.head_size / 16;                        // 32-byte units of a row
-    const int32_t rot_units = p.rot_dim / 16;
-    const int32_t heads = p.num_q_heads + 2 * p.num_kv_heads, per = heads * units;
-    for (int32_t e = threadIdx.x; e < n * per; e += kRopeThreads) {
-        const int32_t t = e / per, r = e - t * per, h = r / units, c = r - h * units;
-        const int32_t kind = h < p.num_q_heads ? 0 : h < p.num_q_heads + p.num_kv_heads ? 1 : 2;
-        const int32_t head = kind == 0 ? h : kind == 1 ? h - p.num_q_heads : h - p.num_q_heads - p.num_kv_heads;
-        const int32_t slot = slots[t];
-        if (kind != 0 && slot < 0) continue;                        // a padding token's K and V
-        const bool rot = kind != 2 && c < rot_units;
-        // the unit's two 16-byte pieces: pairs (d, d + half) or adjacent elements
-        const int32_t d0 = rot && !p.interleaved ? 8 * c : 16 * c;
-        const int32_t d1 = rot && !p.interleaved ? half + 8 * c : 16 * c + 8;
-        const int64_t i = i0 + t;
-        const uint16_t* src = kind == 0 ? static_cast<const uint16_t*>(p.query) + i * p.q_stride
-                              : kind == 1 ? static_cast<const uint16_t*>(p.key) + i * p.k_stride
-                                          : static_cast<const uint16_t*>(p.value) + i * p.v_stride;
-        src += (int64_t)head * p.head_size;
-        const uint4 xa = *reinterpret_cast<const uint4*>(src + d0), xb = *reinterpret_cast<const uint4*>(src + d1);
-        float a[8], b[8];
-        unpack2<BF16>(xa.x, a[0], a[1]);
-        unpack2<BF16>(xa.y, a[2], a[3]);
-        unpack2<BF16>(xa.z, a[4], a[5]);
-        unpack2<BF16>(xa.w, a[6], a[7]);
-        unpack2<BF16>(xb.x, b[0], b[1]);
-        unpack2<BF16>(xb.y, b[2], b[3]);
-        unpack2<BF16>(xb.z, b[4], b[5]);
-        unpack2<BF16>(xb.w, b[6], b[7]);
-        if (rot) {
-            if (!p.interleaved) {
+    for (uint32_t base = tid; base < all; base += kRopeUnits * kRopeThreads) {
+        if (base != (uint32_t)tid) load(base);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 w = turn[t][8 * c + k];
-                    const float x = a[k], y = b[k];
-                    a[k] = x * w.x - y * w.y;
-                    b[k] = x * w.y + y * w.x;
+        for (int k = 0; k < kRopeUnits; ++k) {
+            const uint32_t e = base + k * kRopeThreads;
+            if (e >= all) break;
+            const Unit u = unit(e);
+            float a[8], b[8];
+            const uint32_t wa[4] = {xa[k].x, xa[k].y, xa[k].z, xa[k].w};
+            const uint32_t wb[4] = {xb[k].x, xb[k].y, xb[k].z, xb[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                unpack2<BF16>(wa[j], a[2 * j], a[2 * j + 1]);
+                unpack2<BF16>(wb[j], b[2 * j], b[2 * j + 1]);
+            }
+            if (u.rot) {
+                const float4* t4 = reinterpret_cast<const float4*>(&turn[8 * u.c]);
+                if (!p.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 w = t4[j];       // (cos, sin) of two pairs
+                        const float x = a[2 * j], y = b[2 * j], z = a[2 * j + 1], v = b[2 * j + 1];
+                        a[2 * j] = x * w.x - y * w.y;
+                        b[2 * j] = x * w.y + y * w.x;
+                        a[2 * j + 1] = z * w.z - v * w.w;
+                        b[2 * j + 1] = z * w.w + v * w.z;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 w = t4[j];
+                        float* r = j < 2 ? a + 4 * j : b + 4 * (j - 2);
+                        const float x = r[0], y = r[1], z = r[2], v = r[3];
+                        r[0] = x * w.x - y * w.y;
+                        r[1] = x * w.y + y * w.x;
+                        r[2] = z * w.z - v * w.w;
+                        r[3] = z * w.w + v * w.z;
+                    }
                 }
+            }
+            const int64_t row = u.kind == 0 ? i * hq + u.head
+                                            : (block * hk + u.head) * p.block_size + offset;
+            if (KV8 && u.kind != 0) {
+                // e4m3(x * (1 / scale)): fp32 product, nearest-even, saturated
+                uint8_t* dst = static_cast<uint8_t*>(u.kind == 1 ? p.key_cache : p.value_cache) + row * p.head_size;
+                const float inv = u.kind == 1 ? p.k_inv : p.v_inv;
+                uint32_t qa[4], qb[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    qa[j] = f32x2_to_e4m3x2(__fmul_rn(a[2 * j], inv), __fmul_rn(a[2 * j + 1], inv));
+                    qb[j] = f32x2_to_e4m3x2(__fmul_rn(b[2 * j], inv), __fmul_rn(b[2 * j + 1], inv));
+                }
+                *reinterpret_cast<uint2*>(dst + u.d0) = make_uint2(qa[0] | (qa[1] << 16), qa[2] | (qa[3] << 16));
+                *reinterpret_cast<uint2*>(dst + u.d1) = make_uint2(qb[0] | (qb[1] << 16), qb[2] | (qb[3] << 16));
             } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 w = turn[t][8 * c + k], v = turn[t][8 * c + 4 + k];
-                    const float x = a[2 * k], y = a[2 * k + 1], z = b[2 * k], u = b[2 * k + 1];
-                    a[2 * k] = x * w.x - y * w.y;
-                    a[2 * k + 1] = x * w.y + y * w.x;
-                    b[2 * k] = z * v.x - u * v.y;
-                    b[2 * k + 1] = z * v.y + u * v.x;
+                uint16_t* dst =
+                    static_cast<uint16_t*>(u.kind == 0 ? p.query_out : u.kind == 1 ? p.key_cache : p.value_cache) +
+                    row * p.head_size;
+                // a unit that does not turn goes out as it came in
+                uint4 ya = xa[k], yb = xb[k];
+                if (u.rot) {
+                    ya = make_uint4(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]), pack2<BF16>(a[4], a[5]),
+                                    pack2<BF16>(a[6], a[7]));
+                    yb = make_uint4(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]), pack2<BF16>(b[4], b[5]),
+                                    pack2<BF16>(b[6], b[7]));
                 }
+                *reinterpret_cast<uint4*>(dst + u.d0) = ya;
+                *reinterpret_cast<uint4*>(dst + u.d1) = yb;
             }
-        }
-        const int64_t row = kind == 0
-                                ? i * p.num_q_heads + head
-                                : ((int64_t)(slot / p.block_size) * p.num_kv_heads + head) * p.block_size +
-                                      slot % p.block_size;
-        if (KV8 && kind != 0) {
-            // e4m3(x * (1 / scale)): fp32 product, nearest-even, saturated
-            uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? p.key_cache : p.value_cache) + row * p.head_size;
-            const float inv = kind == 1 ? p.k_inv : p.v_inv;
-            uint32_t qa[4], qb[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                qa[k] = f32x2_to_e4m3x2(__fmul_rn(a[2 * k], inv), __fmul_rn(a[2 * k + 1], inv));
-                qb[k] = f32x2_to_e4m3x2(__fmul_rn(b[2 * k], inv), __fmul_rn(b[2 * k + 1], inv));
-            }
-            *reinterpret_cast<uint2*>(dst + d0) = make_uint2(qa[0] | (qa[1] << 16), qa[2] | (qa[3] << 16));
-            *reinterpret_cast<uint2*>(dst + d1) = make_uint2(qb[0] | (qb[1] << 16), qb[2] | (qb[3] << 16));
-        } else {
-            uint16_t* dst = static_cast<uint16_t*>(kind == 0 ? p.query_out : kind == 1 ? p.key_cache : p.value_cache) +
-                            row * p.head_size;
-            // a piece that is not rotated goes out as it came in
-            uint4 ya = xa, yb = xb;
-            if (rot) {
-                ya = make_uint4(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]), pack2<BF16>(a[4], a[5]),
-                                pack2<BF16>(a[6], a[7]));
-                yb = make_uint4(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]), pack2<BF16>(b[4], b[5]),
-                                pack2<BF16>(b[6], b[7]));
-            }
-            *reinterpret_cast<uint4*>(dst + d0) = ya;
-            *reinterpret_cast<uint4*>(dst + d1) = yb;
         }
     }
 }
@@ -349,8 +374,7 @@ cudaError_t launch_rope_and_cache(const RopeParams& p, bool bf16, bool kv8, cuda
     using Kern = void (*)(RopeParams);
     const Kern kern = kv8 ? (bf16 ? (Kern)rope_and_cache_kernel<true, true> : (Kern)rope_and_cache_kernel<false, true>)
                           : (bf16 ? (Kern)rope_and_cache_kernel<true, false> : (Kern)rope_and_cache_kernel<false, false>);
-    return launch_pdl<RopeParams>(dim3((unsigned)((p.num_tokens + kRopeTokens - 1) / kRopeTokens)),
-                                  dim3(kRopeThreads), stream, kern, p);
+    return launch_pdl<RopeParams>(dim3((unsigned)p.num_tokens), dim3(kRopeThreads), stream, kern, p);
 }
 
 cudaError_t launch_move_blocks(const MoveParams& p, cudaStream_t stream) {

@@ -232,7 +232,7 @@ pa_status run_rope(pa::RopeParams& p, const int32_t* pair_axes, int32_t num_axes
         return fail(PA_ERR_INVALID_ARG, "rope_and_cache: a token stride is shorter than a token's rows");
     if (p.q_stride % 8 || p.k_stride % 8 || p.v_stride % 8)
         return fail(PA_ERR_INVALID_ARG, "rope_and_cache: token strides must be multiples of 8 elements");
-    if ((int64_t)4 * (qrow + 2 * krow) > INT32_MAX)
+    if (qrow + 2 * krow > (1 << 26))
         return fail(PA_ERR_UNSUPPORTED, "rope_and_cache: too many heads");
     if (kv8 && !(k_scale > 0.f && v_scale > 0.f))
         return fail(PA_ERR_INVALID_ARG, "rope_and_cache: scales must be positive");
@@ -245,6 +245,8 @@ pa_status run_rope(pa::RopeParams& p, const int32_t* pair_axes, int32_t num_axes
         return fail(PA_ERR_INVALID_ARG, "rope_and_cache: buffers must be 16-byte aligned");
     if (p.query_out == p.query && p.q_stride != qrow)
         return fail(PA_ERR_INVALID_ARG, "rope_and_cache: query may be rotated in place only when dense");
+    const uint32_t units = (uint32_t)p.head_size / 16;
+    p.unit_div = units == 1 ? 0u : (uint32_t)(((1ull << 32) + units - 1) / units);
     p.k_inv = kv8 ? 1.0f / k_scale : 1.f;
     p.v_inv = kv8 ? 1.0f / v_scale : 1.f;
     cudaError_t e = pa::launch_rope_and_cache(p, dtype == PA_BF16, kv8, stream);
