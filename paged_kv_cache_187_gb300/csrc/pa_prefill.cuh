@@ -70,11 +70,13 @@ struct Cfg {
 struct Unit {
     int32_t seq;          // -1: no more items
     int32_t kvh, len, q_start, q_len, tok0, tile0;
-    int32_t cnt[2];       // tiles each stream needs
+    int32_t cnt[2];       // tiles each stream takes
+    int32_t nt;           // tiles of the item
+    int32_t both;         // the streams share the first one's rows and take turns at the tiles
+    int32_t single;       // the unit has rows for one stream only
     int32_t fix0;         // tiles at or past this one (within the item) are fixed
     int32_t nparts, part; // the unit's partitions, and which of them this is
     int32_t first;        // the share (CTA) that holds partition 0
-    int32_t pad[3];
 };
 
 template <class C>
@@ -90,7 +92,10 @@ struct alignas(1024) Smem {
     uint64_t kv8_full[C::N8 ? C::N8 : 1], kv8_empty[C::N8 ? C::N8 : 1];
     uint64_t q_full, q_ready, q_empty, item_ready, k_ready;
     uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
-    float red[2][2][kPfRows];          // [stream][half][row]: maxima, or weight sums
+    uint64_t x_full[2], x_again[2];    // by item parity: streams that share rows meet
+    float red[2][2][kPfRows];          // [stream][half][row]: maxima
+    // by item parity: weight sums [stream][half][row] and references
+    float xsum[2][2][2][kPfRows], xref[2][2][kPfRows];
     uint64_t u_full[2], u_empty[2], drain;
     Unit unit[2];
     // first token with +inf / -inf / NaN of each head dim among an item's fixed tiles
@@ -265,7 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 9);     // 8 softmax warps and the readiness warp
             mbar_init(&sm.o_full[i], 1);
-            mbar_init(&sm.o_free[i], 8);
+            mbar_init(&sm.o_free[i], 16);    // 8 warps twice, or 16
+            mbar_init(&sm.x_full[i], 16);
+            mbar_init(&sm.x_again[i], 16);
             mbar_init(&sm.u_full[i], 1);
             mbar_init(&sm.u_empty[i], 23);   // V, MMA, readiness, 16 softmax warps, 4 fixing warps
             sm.any_nonfinite[i] = 1;         // the producer clears the tables first
@@ -392,10 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the next unit: row tile and kv head, and (cut 1) the tiles of this share
                 Unit u;
                 u.seq = -1;
-                u.cnt[0] = u.cnt[1] = 0;
+                u.cnt[0] = u.cnt[1] = u.nt = u.both = u.single = 0;
                 u.nparts = 1;
                 u.part = u.first = 0;
-                u.pad[0] = u.pad[1] = u.pad[2] = 0;
                 int32_t claimed = 0, rt = -1, tile0 = 0, tile1 = kNoToken;
                 if (warp_sees_abort(sm.abort)) {
                 } else if (!hdr.cut) {
@@ -458,6 +464,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int32_t n = a < u.q_len ? max(u.len - u.q_len + b, 0) : 0;
                         u.cnt[i] = max(min((n + kPfTok - 1) / kPfTok, tile1) - tile0, 0);
                     }
+                    u.nt = max(u.cnt[0], u.cnt[1]);
+                    u.single = u.tok0 + p.tpt >= u.q_len;
+                    // rows for one stream only: both take them, and every other tile each
+                    // (not with the fp8 ring, whose three stages hold too few tiles ahead)
+                    if (!C::kKv8 && u.single && u.nt > 1) {
+                        u.both = 1;
+                        u.cnt[0] = (u.nt + 1) / 2;
+                        u.cnt[1] = u.nt / 2;
+                    }
                     // first tile that some row does not see whole
                     u.fix0 = max(u.len - u.q_len + u.tok0 + 1, 0) / kPfTok - tile0;
                 }
@@ -476,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) allow_dependent_launch();
                     break;
                 }
-                const int32_t nt = max(u.cnt[0], u.cnt[1]);
+                const int32_t nt = u.nt;
                 if (nt > 0) {
                     if (lane == 0) {
                         ok = mbar_wait(&sm.q_empty, (nq & 1) ^ 1);
@@ -489,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (u.cnt[i] > 0)
                                     for (int h = 0; h < C::HALVES; ++h)
                                         tma_load_3d(sm.q[i] + h * C::HALF, &qmap, h * 64, u.kvh * G,
-                                                    u.q_start + u.tok0 + i * p.tpt, &sm.q_full);
+                                                    u.q_start + u.tok0 + (u.both ? 0 : i * p.tpt),
+                                                    &sm.q_full);
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -517,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t tile0 = __shfl_sync(0xffffffffu, sm.unit[us].tile0, 0);
                 const int32_t len = __shfl_sync(0xffffffffu, sm.unit[us].len, 0);
                 const int32_t fix0 = __shfl_sync(0xffffffffu, sm.unit[us].fix0, 0);
-                const int32_t nt = __shfl_sync(0xffffffffu, max(sm.unit[us].cnt[0], sm.unit[us].cnt[1]), 0);
+                const int32_t nt = __shfl_sync(0xffffffffu, sm.unit[us].nt, 0);
                 if (lane == 0) mbar_arrive(&sm.u_empty[us]);
                 if (seq < 0) break;
                 if (nt > 0)
@@ -550,27 +566,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t us = it & 1;
                 ok = mbar_wait_warp(&sm.u_full[us], (it >> 1) & 1);
                 if (!ok) break;
-                const int32_t seq = sm.unit[us].seq, fix0 = sm.unit[us].fix0;
+                const int32_t seq = sm.unit[us].seq, fix0 = sm.unit[us].fix0, nt = sm.unit[us].nt;
                 const int32_t cnt0 = sm.unit[us].cnt[0], cnt1 = sm.unit[us].cnt[1];
+                const bool both = sm.unit[us].both;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.u_empty[us]);
                 if (seq < 0) break;
-                const int32_t nt = max(cnt0, cnt1);
                 if (nt == 0) continue;
                 ok = mbar_wait_warp(C::kKv8 && C::kQBf16 ? &sm.q_ready : &sm.q_full, q_phase);
                 q_phase ^= 1;
                 if (ok) ok = wait_kv(st, false);
+                if (ok && both) ok = wait_kv(next(next(st)), false);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive(&sm.item_ready);
+                // a stream's next K tile comes `ahead` tiles after the one it works on
+                const int32_t ahead = both ? 2 : 1;
 #pragma unroll 1
                 for (int32_t j = 0; j < nt && ok; ++j) {
                     const uint32_t vs = next(st), kn = next(vs);
                     ok = wait_kv(vs, !C::kKv8 && j >= fix0);
-                    if (!C::kKv8 && ok && j + 1 < nt) ok = wait_kv(kn, false);
+                    if (!C::kKv8 && ok && j + ahead < nt) ok = wait_kv(both ? next(next(kn)) : kn, false);
 #pragma unroll 1
                     for (uint32_t i = 0; i < 2 && ok; ++i) {
-                        if (j >= (i ? cnt1 : cnt0)) continue;
-                        if (j == 0) {
+                        if (both ? (j & 1) != (int32_t)i : j >= (i ? cnt1 : cnt0)) continue;
+                        if (j < ahead) {
                             ok = mbar_wait_warp(&sm.o_free[i], ((o_phase >> i) & 1) ^ 1);
                             o_phase ^= 1u << i;
                         }
@@ -633,9 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t seq = __shfl_sync(0xffffffffu, sm.unit[us].seq, 0);
                 const int32_t cnt0 = __shfl_sync(0xffffffffu, sm.unit[us].cnt[0], 0);
                 const int32_t cnt1 = __shfl_sync(0xffffffffu, sm.unit[us].cnt[1], 0);
+                const int32_t nt = __shfl_sync(0xffffffffu, sm.unit[us].nt, 0);
+                const int32_t both = __shfl_sync(0xffffffffu, sm.unit[us].both, 0);
                 if (lane == 0) mbar_arrive(&sm.u_empty[us]);
                 if (seq < 0) break;
-                const int32_t nt = max(cnt0, cnt1);
                 if (nt == 0) continue;
                 ok = mbar_wait_warp(&sm.item_ready, i_phase);
                 i_phase ^= 1;
@@ -643,36 +663,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // tile j's K sits in stage ks, its V in the next one
                 uint32_t ks = st;
                 tmem_fence_after_sync();
+                const int32_t ahead = both ? 2 : 1;   // tiles to a stream's next one
                 if (elect_one()) {
+                    const uint32_t k1 = both ? next(next(ks)) : ks;
                     if (cnt0 > 0) qk(0, ks);
-                    if (cnt1 > 0) qk(1, ks);
+                    if (cnt1 > 0) qk(1, k1);
                     mma_commit(&sm.kv_empty[ks]);
-                    if (nt == 1) mma_commit(&sm.q_empty);
+                    if (both) mma_commit(&sm.kv_empty[k1]);
+                    if (nt <= ahead) mma_commit(&sm.q_empty);
                 }
                 // per tile: PV of each stream and its next QK^T, with nothing to wait for in
                 // between
 #pragma unroll 1
                 for (int32_t j = 0; j < nt; ++j) {
-                    const uint32_t vs = next(ks), kn = next(vs);
-                    const uint32_t last = j < cnt1 ? 1 : 0;
+                    const uint32_t vs = next(ks), kn = next(vs);   // V of tile j, K of the next
+                    const uint32_t kq = both ? next(next(kn)) : kn;   // the next scores' K
+                    const uint32_t last = both ? (uint32_t)j & 1u : j < cnt1 ? 1 : 0;
                     bool k_here = false;
 #pragma unroll 1
-                    for (uint32_t i = j < cnt0 ? 0 : 1; i <= last; ++i) {
-                        const bool more = j + 1 < (i ? cnt1 : cnt0);
+                    for (uint32_t i = both ? last : j < cnt0 ? 0 : 1; i <= last; ++i) {
+                        const bool more = both ? j + 2 < nt : j + 1 < (i ? cnt1 : cnt0);
                         ok = mbar_wait_warp(&sm.p_full[i], (p_phase >> i) & 1);
                         if (!ok) break;
                         tmem_fence_after_sync();
                         // (one lane) what follows PV: the stages given back, the next scores
                         auto go_on = [&]() {
                             if (i == last) mma_commit(&sm.kv_empty[vs]);
-                            if (more) qk(i, kn);
+                            if (more) qk(i, kq);
                             if (i == last) {
-                                if (j + 1 < nt) mma_commit(&sm.kv_empty[kn]);
-                                if (j + 2 == nt) mma_commit(&sm.q_empty);
+                                if (j + ahead < nt) mma_commit(&sm.kv_empty[kq]);
+                                if (j + ahead + 1 == nt) mma_commit(&sm.q_empty);
                             }
                         };
                         if (elect_one()) {
-                            pv(i, vs, (uint32_t)j);
+                            pv(i, vs, j >= ahead ? 1u : 0u);
                             if (!more) mma_commit(&sm.o_full[i]);
                             if (!C::kKv8) go_on();
                         }
@@ -715,8 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const int32_t seq = sm.unit[us].seq, fix0 = sm.unit[us].fix0;
             const int32_t cnt0 = sm.unit[us].cnt[0], cnt1 = sm.unit[us].cnt[1];
-            const int32_t len = sm.unit[us].len, tile0 = sm.unit[us].tile0;
-            const int32_t nt = max(cnt0, cnt1);
+            const int32_t len = sm.unit[us].len, tile0 = sm.unit[us].tile0, nt = sm.unit[us].nt;
             __syncwarp();
             // (the slot is released by the softmax warps at the item's end as well, so the
             // table of non-finite values stays this item's until then)
@@ -881,6 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t scale2 = pack_f32(p.scale_log2, p.scale_log2);
         const float hidden = p.scale_log2 < 0.f ? INFINITY : -INFINITY;   // -inf once scaled
         uint32_t ns = 0, no = 0;                        // scores seen, outputs taken
+        uint32_t x_phase = 0, xa_phase = 0;             // bit us: parities of the streams' meetings
         bool failed = false;
 #pragma unroll 1
         for (uint32_t it = 0;; ++it) {
@@ -896,13 +920,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit& un = sm.unit[us];
             if (un.seq < 0) break;
             const int32_t cnt = un.cnt[si];
+            const bool both = !C::kKv8 && un.both;
             // tokens this row sees, and the fewest any row of the stream sees
-            const int32_t whole = un.len - un.q_len + un.tok0 + si * p.tpt + 1;
+            const int32_t whole = un.len - un.q_len + un.tok0 + (both ? 0 : si * p.tpt) + 1;
             const int32_t limit = min(whole + qtok, un.len);
-            int32_t t0 = un.tile0 * kPfTok + half * kCols;   // first token of the half tile
+            // first token of the half tile
+            int32_t t0 = (un.tile0 + (both ? si : 0)) * kPfTok + half * kCols;
+            const int32_t t_step = both ? 2 * kPfTok : kPfTok;
             float ref = -INFINITY, sum = 0.f;
 #pragma unroll 1
-            for (int32_t j = 0; j < cnt; ++j, t0 += kPfTok) {
+            for (int32_t j = 0; j < cnt; ++j, t0 += t_step) {
                 ok = mbar_wait_warp(&sm.s_full[si], ns & 1);
                 ++ns;
                 tmem_fence_after_sync();
@@ -1005,45 +1032,96 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++no;
                 tmem_fence_after_sync();
             }
-            sm.red[si][half][row] = sum;
+            sm.xsum[us][si][half][row] = sum;
+            if (half == 0) sm.xref[us][si][row] = ref;
+            // (streams that share their rows meet here, with a bounded wait: each may have
+            // given up on its own)
+            auto meet = [&](uint64_t* at, uint32_t& phase) {
+                tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(at);
+                const bool here = mbar_wait_warp(at, (phase >> us) & 1);
+                phase ^= 1u << us;
+                tmem_fence_after_sync();
+                return here;
+            };
+            if (both && ok) ok = meet(&sm.x_full[us], x_phase);
             if (consumers_any(!ok, kStreamThreads, bar)) {
                 failed = true;
                 break;
             }
-            sum += sm.red[si][half ^ 1][row];   // (two terms: the same sum in both halves)
+            sum += sm.xsum[us][si][half ^ 1][row];   // (two terms: the same sum in both halves)
             const Unit u = un;
-            const int32_t tok = u.tok0 + si * p.tpt + qtok;
+            const int32_t tok = u.tok0 + (both ? 0 : si * p.tpt) + qtok;
             const bool mine = qtok < p.tpt && tok < u.q_len;
+            const bool nonfinite = sm.any_nonfinite[us] != 0;
+            // Shared rows: O and the weight sums of the two streams, each against its own
+            // reference, become one, w0 O0 + w1 O1.
+            float w0 = 1.f, w1 = 0.f;
+            bool top_here = true;      // the weight of this stream's O is 1
+            if (both) {
+                const float theirs = sm.xref[us][si ^ 1][row], top = fmaxf(ref, theirs);
+                const float other = sm.xsum[us][si ^ 1][0][row] + sm.xsum[us][si ^ 1][1][row];
+                const float a = state_weight(ref, top), b = state_weight(theirs, top);
+                // (the same order of terms in either stream)
+                sum = si ? fmaf(a, sum, b * other) : fmaf(b, other, a * sum);
+                w0 = si ? b : a;
+                w1 = si ? a : b;
+                top_here = si ? ref > theirs : ref >= theirs;
+                ref = top;
+            }
             // infinite and NaN values that were kept out of the products, for the rows that
             // see them
-            if (sm.any_nonfinite[us] && cnt > 0) {
+            if (nonfinite && cnt > 0) {
 #pragma unroll 1
                 for (int d = 0; d < kDims; ++d) {
                     float o = tmem_ld1(to + d);
                     const int32_t* const first = &sm.nonfinite[us][0][half * kDims + d];
-                    if (first[0] < limit) o += INFINITY;
-                    if (first[D] < limit) o -= INFINITY;
-                    if (first[2 * D] < limit) o = __int_as_float(0x7fc00000);
+                    if (top_here && first[0] < limit) o += INFINITY;
+                    if (top_here && first[D] < limit) o -= INFINITY;
+                    if (top_here && first[2 * D] < limit) o = __int_as_float(0x7fc00000);
                     tmem_st1(to + d, o);
                 }
             }
-            // 32 head dims of O (0 where the stream had no tile)
-            auto load_o = [&](int h, float (&o)[32]) {
+            int dims = kDims, dim0 = half * kDims;
+            uint32_t o_at = to, o_other = 0;
+            if (both) {
+                if (nonfinite) {
+                    ok = meet(&sm.x_again[us], xa_phase);
+                    if (consumers_any(!ok, kStreamThreads, bar)) {
+                        failed = true;
+                        break;
+                    }
+                }
+                // each of the four warpgroups has a quarter of the head dims
+                dims = D / 4;
+                dim0 = (2 * si + half) * (D / 4);
+                o_at = taddr + C::COL_O + dim0;
+                o_other = o_at + D;
+            }
+            // 16 head dims of O (0 where the stream had no tile)
+            auto load_o = [&](int h, float (&o)[16]) {
                 if (cnt > 0) {
-                    tmem_ld32(to + 32 * h, o);
+                    tmem_ld16(o_at + 16 * h, o);
                     tmem_wait_ld();
+                    if (both) {
+                        float o1[16];
+                        tmem_ld16(o_other + 16 * h, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) o[c] = fmaf(w0, o[c], w1 * o1[c]);
+                    }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] = 0.f;
+                    for (int c = 0; c < 16; ++c) o[c] = 0.f;
                 }
             };
-            auto store_row = [&](int h, const float (&o)[32], float f) {
+            auto store_row = [&](int d, const float (&o)[16], float f) {
                 const size_t orow =
                     ((size_t)(u.q_start + tok) * p.num_q_heads + (size_t)u.kvh * G + row % G) * D;
-                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow +
-                                                      half * kDims + 32 * h);
+                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow + d);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 2; ++k)
                     dst[k] = make_uint4(pack2<C::kQBf16>(o[8 * k] * f, o[8 * k + 1] * f),
                                         pack2<C::kQBf16>(o[8 * k + 2] * f, o[8 * k + 3] * f),
                                         pack2<C::kQBf16>(o[8 * k + 4] * f, o[8 * k + 5] * f),
@@ -1054,70 +1132,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if (cnt > 0) mbar_arrive(&sm.o_free[si]);
+                    if (both) {
+                        mbar_arrive(&sm.o_free[0]);
+                        mbar_arrive(&sm.o_free[1]);
+                    } else if (cnt > 0) {
+                        mbar_arrive(&sm.o_free[si]);
+                        mbar_arrive(&sm.o_free[si]);
+                    }
                     mbar_arrive(&sm.u_empty[us]);
                 }
             };
             if (u.nparts == 1) {
                 const float f = sum == 0.f ? 0.f : p.out_scale / sum;
 #pragma unroll 1
-                for (int h = 0; h < kDims / 32; ++h) {
-                    float o[32];
+                for (int h = 0; h < dims / 16; ++h) {
+                    float o[16];
                     load_o(h, o);
-                    if (mine) store_row(h, o, f);
+                    if (mine) store_row(dim0 + 16 * h, o, f);
                 }
                 release();
             } else {
-                // partial rows, [dim][row] so that a warp's accesses are contiguous
-                // (a share's place 1 is for a unit that goes on, 0 for one that came to it)
+                // Partial rows, [dim][row] so that a warp's accesses are contiguous.  (A
+                // share's place 1 is for a unit that goes on, 0 for one that came to it;
+                // rows of one stream only are its first stream's, whoever works on them.)
+                const int sj = u.single ? 0 : si;
+                const bool takes_part = both || !u.single || si == 0;
                 auto place = [&](int part) {
-                    return ((size_t)(2 * (u.first + part) + (part == 0)) * 2 + si) * kPfRows;
+                    return ((size_t)(2 * (u.first + part) + (part == 0)) * 2 + sj) * kPfRows;
                 };
-                auto cell = [&](size_t at, int d) { return at * D + (size_t)(half * kDims + d) * kPfRows + row; };
-                const size_t at = place(u.part);
+                auto cell = [&](size_t at, int d) { return at * D + (size_t)d * kPfRows + row; };
+                if (takes_part) {
+                    const size_t at = place(u.part);
 #pragma unroll 1
-                for (int h = 0; h < kDims / 32; ++h) {
-                    float o[32];
-                    load_o(h, o);
+                    for (int h = 0; h < dims / 16; ++h) {
+                        float o[16];
+                        load_o(h, o);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) p.part_acc[cell(at, 32 * h + c)] = o[c];
-                }
-                if (half == 0) p.part_ml[at + row] = make_float2(ref, sum);
-                release();
-                // the stream that finishes the row tile's last partition joins them, always
-                // in the order of the partitions
-                __threadfence();
-                named_bar_sync(bar, kStreamThreads);
-                if (row == 0 && half == 0)
-                    sm.last_part[si] =
-                        atomicAdd(&p.arrive[2 * u.first + si], 1) == u.nparts - 1;
-                named_bar_sync(bar, kStreamThreads);
-                if (sm.last_part[si]) {
-                    __threadfence();
-                    float M = -INFINITY;
-#pragma unroll 1
-                    for (int q = 0; q < u.nparts; ++q) M = fmaxf(M, __ldcg(&p.part_ml[place(q) + row]).x);
-                    float den = 0.f;
-#pragma unroll 1
-                    for (int q = 0; q < u.nparts; ++q) {
-                        const float2 ml = __ldcg(&p.part_ml[place(q) + row]);
-                        den += state_weight(ml.x, M) * ml.y;
+                        for (int c = 0; c < 16; ++c) p.part_acc[cell(at, dim0 + 16 * h + c)] = o[c];
                     }
-                    const float f = den == 0.f ? 0.f : p.out_scale / den;
+                    if (half == 0 && !(both && si)) p.part_ml[at + row] = make_float2(ref, sum);
+                }
+                release();
+                if (takes_part) {
+                    // The stream that finishes the row tile's last partition joins them,
+                    // always in the order of the partitions.  Shared rows count once for each
+                    // stream, so a partition of a single stream's rows is worth two.
+                    __threadfence();
+                    named_bar_sync(bar, kStreamThreads);
+                    if (row == 0 && half == 0) {
+                        const int32_t worth = u.single && !both ? 2 : 1;
+                        const int32_t full = u.single ? 2 * u.nparts : u.nparts;
+                        sm.last_part[si] = atomicAdd(&p.arrive[2 * u.first + sj], worth) == full - worth;
+                    }
+                    named_bar_sync(bar, kStreamThreads);
+                    if (sm.last_part[si]) {
+                        __threadfence();
+                        float M = -INFINITY;
 #pragma unroll 1
-                    for (int h = 0; h < kDims / 32; ++h) {
-                        float o[32];
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = 0.f;
+                        for (int q = 0; q < u.nparts; ++q) M = fmaxf(M, __ldcg(&p.part_ml[place(q) + row]).x);
+                        float den = 0.f;
 #pragma unroll 1
                         for (int q = 0; q < u.nparts; ++q) {
-                            const size_t pr = place(q);
-                            const float wq = state_weight(__ldcg(&p.part_ml[pr + row]).x, M);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                o[c] = fmaf(wq, __ldcg(&p.part_acc[cell(pr, 32 * h + c)]), o[c]);
+                            const float2 ml = __ldcg(&p.part_ml[place(q) + row]);
+                            den += state_weight(ml.x, M) * ml.y;
                         }
-                        if (mine) store_row(h, o, f);
+                        const float f = den == 0.f ? 0.f : p.out_scale / den;
+#pragma unroll 1
+                        for (int h = 0; h < kDims / 16; ++h) {
+                            const int d = half * kDims + 16 * h;
+                            float o[16];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) o[c] = 0.f;
+#pragma unroll 1
+                            for (int q = 0; q < u.nparts; ++q) {
+                                const size_t pr = place(q);
+                                const float wq = state_weight(__ldcg(&p.part_ml[pr + row]).x, M);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    o[c] = fmaf(wq, __ldcg(&p.part_acc[cell(pr, d + c)]), o[c]);
+                            }
+                            if (mine) store_row(d, o, f);
+                        }
                     }
                 }
             }

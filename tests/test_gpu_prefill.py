@@ -123,3 +123,22 @@ def test_many_items_and_tiles_per_cta(cuda_device, Hq, Hkv, D, bs, dtype, fp8):
     seqs = [(int(n), int(n + p)) for n, p in zip(rng.integers(1, 60, 150), rng.integers(0, 2500, 150))]
     seqs += [(0, 0), (700, 700), (3, 4001), (257, 1500)]
     run(make(seqs, Hq, Hkv, D, bs, dtype, 5, fp8))
+
+
+# Few units, so that the work is cut into shares at places that move with every length: units
+# begun in one share and ended several later, shares that hold the ends of two, rows for one
+# stream only (whose tiles the streams share) and for both, odd and even numbers of tiles.
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,bs,dtype,fp8", [
+    ([(1, 5000)], 8, 1, 128, 16, torch.bfloat16, False),
+    ([(1, 129)], 2, 2, 128, 16, torch.float16, False),
+    ([(2, 9001), (1, 77), (33, 2600)], 4, 2, 128, 32, torch.float16, False),
+    ([(20, 6000), (1, 8191), (70, 4000)], 16, 2, 128, 16, torch.bfloat16, False),
+    ([(100, 3000)], 3, 1, 64, 16, torch.bfloat16, False),
+    ([(1, 20000), (64, 700)], 5, 1, 64, 32, torch.float16, False),
+    ([(1, 5000)], 8, 1, 128, 32, torch.bfloat16, True),
+    ([(20, 6000), (1, 8191), (70, 4000)], 16, 2, 128, 16, torch.float16, True),
+    ([(300, 300)], 16, 1, 128, 16, torch.bfloat16, False),
+    ([(5, 640), (5, 641), (5, 639), (0, 100), (5, 5)], 6, 6, 128, 16, torch.bfloat16, False),
+])
+def test_work_cut_into_shares(cuda_device, seqs, Hq, Hkv, D, bs, dtype, fp8):
+    run(make(seqs, Hq, Hkv, D, bs, dtype, 23 + Hq, fp8))
