@@ -1197,6 +1197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             den += state_weight(ml.x, M) * ml.y;
                         }
                         const float f = den == 0.f ? 0.f : p.out_scale / den;
+                        // (three partitions' values are on their way together: one at a time, joining six of them
+                        // took 20 us)
 #pragma unroll 1
                         for (int h = 0; h < kDims / 16; ++h) {
                             const int d = half * kDims + 16 * h;
@@ -1204,12 +1206,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int c = 0; c < 16; ++c) o[c] = 0.f;
 #pragma unroll 1
-                            for (int q = 0; q < u.nparts; ++q) {
-                                const size_t pr = place(q);
-                                const float wq = state_weight(__ldcg(&p.part_ml[pr + row]).x, M);
+                            for (int q = 0; q < u.nparts; q += 3) {
+                                float v[3][16], wq[3];
 #pragma unroll
-                                for (int c = 0; c < 16; ++c)
-                                    o[c] = fmaf(wq, __ldcg(&p.part_acc[cell(pr, d + c)]), o[c]);
+                                for (int t = 0; t < 3; ++t) {
+                                    const size_t pr = place(min(q + t, u.nparts - 1));
+                                    const bool in = mine && q + t < u.nparts;
+                                    wq[t] = in ? __ldcg(&p.part_ml[pr + row]).x : -INFINITY;
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c)
+                                        v[t][c] = in ? __ldcg(&p.part_acc[cell(pr, d + c)]) : 0.f;
+                                }
+#pragma unroll
+                                for (int t = 0; t < 3; ++t) {
+                                    const float weight = state_weight(wq[t], M);
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c) o[c] = fmaf(weight, v[t][c], o[c]);
+                                }
                             }
                             if (mine) store_row(d, o, f);
                         }
