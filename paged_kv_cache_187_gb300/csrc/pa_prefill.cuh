@@ -43,7 +43,8 @@ namespace pf {
 constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpLoadV = 18, kWarpReady = 19, kWarpFix0 = 20;
 constexpr int kThreads = 768;
 constexpr int kStreamThreads = 256;    // two warpgroups of softmax per stream
-constexpr int kBarStream = 1;          // named barriers 1, 2: the warps of a stream
+// Named barriers: 1-8 the two warps that share 32 rows, 9 and 10 the warps of a stream
+constexpr int kBarRows = 1, kBarStream = 9;
 constexpr float kRefSlack = 8.f;       // a reference is left behind by at most this (log2)
 constexpr int32_t kNoToken = 0x7fffffff;
 // Registers per thread: 80 at launch, re-divided among the six warpgroups.
@@ -899,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t taddr = tmem + ((uint32_t)(sw * 32) << 16);
         const uint32_t ts = taddr + C::COL_S + si * kPfTok + half * kCols;
         const uint32_t to = taddr + C::COL_O + si * D + half * kDims;
-        const int bar = kBarStream + si;
+        const int bar = kBarStream + si, row_bar = kBarRows + si * 4 + sw;
         const int32_t qtok = row / G;                   // new token of this row, within the stream
         const uint64_t scale2 = pack_f32(p.scale_log2, p.scale_log2);
         const float hidden = p.scale_log2 < 0.f ? INFINITY : -INFINITY;   // -inf once scaled
@@ -948,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // largest exponent), in both threads of a row, and rescales O.
                 auto settle = [&](float m) {
                     sm.red[si][half][row] = m;
-                    failed = consumers_any(!ok, kStreamThreads, bar);
+                    failed = consumers_any(!ok, 64, row_bar);
                     m = fmaxf(m, sm.red[si][half ^ 1][row]);
                     const bool move = m > kRefSlack || (ref == -INFINITY && m > -INFINITY);
                     const float next = move ? (ref == -INFINITY ? m : m + ref) : ref;
@@ -1013,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (again) break;
                     const float m = fmaxf(mx[0], mx[1]);
                     const bool move = m > kRefSlack || (ref == -INFINITY && m > -INFINITY);
-                    if (!consumers_any(!ok || move, kStreamThreads, bar)) break;
+                    if (!consumers_any(!ok || move, 64, row_bar)) break;
                     settle(m);   // rare
                     if (failed) break;
                 }
@@ -1025,9 +1026,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_full[si]);
             }
-            if (failed) break;
             // ---- the item's rows
-            if (cnt > 0) {
+            ok = !failed;
+            if (cnt > 0 && ok) {
                 ok = mbar_wait_warp(&sm.o_full[si], no & 1);
                 ++no;
                 tmem_fence_after_sync();
