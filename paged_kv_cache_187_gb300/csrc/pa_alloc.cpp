@@ -266,10 +266,16 @@ pa_status pa_alloc_shrink(pa_alloc* a, int32_t num_blocks, int32_t* pairs_out, i
         return fail(PA_ERR_INVALID_ARG, "alloc_shrink: num_blocks %d (1 .. %d)", num_blocks, a->num_blocks);
     if (!a->copies.empty())
         return fail(PA_ERR_INVALID_ARG, "alloc_shrink: %zu copy-on-write pairs are pending", a->copies.size() / 2);
-    std::vector<int32_t> high, low;
-    for (int32_t b = 0; b < a->num_blocks; ++b) {
-        if (b < num_blocks && a->refcount[b] == 0) low.push_back(b);
-        if (b >= num_blocks && a->refcount[b] > 0) high.push_back(b);
+    std::vector<int32_t> high, low, place;
+    try {
+        place.resize((size_t)a->num_blocks);
+        for (int32_t b = 0; b < a->num_blocks; ++b) {
+            place[b] = b;
+            if (b < num_blocks && a->refcount[b] == 0) low.push_back(b);
+            if (b >= num_blocks && a->refcount[b] > 0) high.push_back(b);
+        }
+    } catch (...) {
+        return fail(PA_ERR_INVALID_ARG, "alloc_shrink: out of host memory");
     }
     if (high.size() > low.size())
         return fail(PA_ERR_NO_BLOCKS, "alloc_shrink: %zu blocks are in use, more than %d",
@@ -278,8 +284,6 @@ pa_status pa_alloc_shrink(pa_alloc* a, int32_t num_blocks, int32_t* pairs_out, i
     if (*n_out > max_pairs)
         return fail(PA_ERR_INVALID_ARG, "alloc_shrink: %d pairs, room for %d", *n_out, max_pairs);
     if (*n_out > 0 && !pairs_out) return fail(PA_ERR_INVALID_ARG, "alloc_shrink: null output");
-    std::vector<int32_t> place((size_t)a->num_blocks);
-    for (int32_t b = 0; b < a->num_blocks; ++b) place[b] = b;
     for (size_t i = 0; i < high.size(); ++i) {
         pairs_out[2 * i] = high[i];
         pairs_out[2 * i + 1] = low[i];

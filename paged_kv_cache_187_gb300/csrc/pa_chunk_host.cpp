@@ -2,12 +2,11 @@
 // checks, workspace layout, TMA tensor maps and launches of pa_prefill(_fp8),
 // pa_rope_and_cache(_fp8) and pa_move_blocks.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <mutex>
-#include <unordered_map>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -68,21 +67,19 @@ pa_status encode(CUtensorMap* map, const void* base, bool bytes, int rank, const
     return PA_OK;
 }
 
+// Streaming multiprocessors of the current device, asked for once per device.
 pa_status sm_count(int* sms) {
-    static std::mutex mu;
-    static std::unordered_map<int, int> known;
+    static std::atomic<int> known[256];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    std::lock_guard<std::mutex> lk(mu);
-    auto it = known.find(dev);
-    if (it == known.end()) {
-        int n = 0;
+    int n = dev >= 0 && dev < 256 ? known[dev].load() : 0;
+    if (n == 0) {
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-        it = known.emplace(dev, n).first;
+        if (dev >= 0 && dev < 256) known[dev].store(n);
     }
-    *sms = it->second;
+    *sms = n;
     return PA_OK;
 }
 

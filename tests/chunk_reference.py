@@ -30,11 +30,11 @@ def prefill(q, kc, vc, tables, lens, starts, scale, k_scale=1.0, v_scale=1.0):
       2^-25 sum_t |v_t|    ... and below fp16's normal range by up to 2^-25 each, while the
                            weights are relative to one of at least 1 (bf16 has fp32's range);
       u_out |out|          the output is rounded once;
-      W (2 D 2^-24 A + 2^-20)  scores: D products summed in fp32, each step of the sum off by
-                           at most 2^-24 of A = scale sum_d |q_d k_d|, twice (numerator and
-                           weight sum); exp2, its argument, the sums and the division a few
-                           fp32 steps more (a context of up to 4096 tokens is summed in four
-                           chains per tile and once per tile).
+      W (2 D 2^-24 A + 2^-20 + (L / 16) 2^-23)
+                           scores: D products summed in fp32, each step of the sum off by at
+                           most 2^-24 of A = scale sum_d |q_d k_d|, twice (numerator and weight
+                           sum); exp2, its argument and the division a few fp32 steps; and the
+                           sums over the context, 16 tokens a step, numerator and weights.
     """
     T, Hq, D = q.shape
     Hkv, bs = kc.shape[1], kc.shape[2]
@@ -67,7 +67,7 @@ def prefill(q, kc, vc, tables, lens, starts, scale, k_scale=1.0, v_scale=1.0):
             W = torch.einsum("hnt,thd->nhd", w, vv.abs())
             out[a + j0:a + j1] = o
             t = half_step(pdt) * W + half_step(q.dtype) * o.abs()
-            t += W * (2 * D * FP32 * A.t()[..., None] + 2.0 ** -20)
+            t += W * (2 * D * FP32 * A.t()[..., None] + 2.0 ** -20 + L / 16 * 2 * FP32)
             if pdt == torch.float16:
                 t += 2.0 ** -25 * torch.einsum("nt,thd->nhd", (~hide).double(), vv.abs())
             tol[a + j0:a + j1] = t

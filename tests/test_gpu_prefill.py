@@ -142,3 +142,222 @@ def test_many_items_and_tiles_per_cta(cuda_device, Hq, Hkv, D, bs, dtype, fp8):
 ])
 def test_work_cut_into_shares(cuda_device, seqs, Hq, Hkv, D, bs, dtype, fp8):
     run(make(seqs, Hq, Hkv, D, bs, dtype, 23 + Hq, fp8))
+
+
+def test_chunks_longer_than_the_context_and_empty_contexts(cuda_device):
+    """Rows with nothing to attend to are zero rows: chunks whose first tokens lie before the
+    context's start (clamped metadata), and empty contexts."""
+    for fp8 in (False, True):
+        b = make([(10, 4), (3, 0), (140, 130), (1, 0), (300, 1)], 8, 2, 128, 16, torch.float16, 3, fp8)
+        out = run(b)
+        for s, (n, L) in enumerate([(10, 4), (3, 0), (140, 130), (1, 0), (300, 1)]):
+            a = int(b["starts"][s])
+            assert not out[a:a + max(n - L, 0)].any()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,bs,dtype,fp8", [
+    (8, 2, 128, 16, torch.bfloat16, False), (4, 4, 64, 32, torch.float16, False),
+    (8, 1, 128, 32, torch.float16, True)])
+@pytest.mark.parametrize("spread", [12.0, 40.0])
+def test_references_move(cuda_device, Hq, Hkv, D, bs, dtype, fp8, spread):
+    """Scores that spread over hundreds: the largest of a row turns up in late tiles, and the
+    accumulators are rescaled there."""
+    b = make([(33, 1400), (1, 3000), (200, 900), (5, 128)], Hq, Hkv, D, bs, dtype, 17, fp8,
+             spread=spread if not fp8 else min(spread, 3.0))
+    # growing along the context
+    for s, L in enumerate(b["lens"]):
+        for t, i in enumerate(b["tables"][s, :-(-L // bs)].tolist()):
+            f = 0.1 + 2.0 * t * bs / L
+            if not fp8:
+                b["kc"][i] = (b["kc"][i].float() * f).to(dtype)
+    run(b)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-4, 2.0])
+def test_scales(cuda_device, scale):
+    for fp8 in (False, True):
+        b = make([(40, 500), (1, 900)], 4, 2, 128, 16, torch.float16, 19, fp8)
+        b["scale"] = scale
+        run(b)
+
+
+def test_rows_outside_the_chunks_are_left_alone(cuda_device):
+    b = make([(9, 100), (0, 50), (130, 400)], 4, 2, 128, 16, torch.bfloat16, 29, extra=37)
+    shift = 11                                     # rows before the first chunk as well
+    b["starts"] = b["starts"] + shift
+    b["starts_d"] += shift
+    out = call(b, torch.full_like(b["q"], 7.0))
+    want, tol = reference(b)
+    n = int(b["starts"][-1])
+    assert (out[:shift] == 7).all() and (out[n:] == 7).all()
+    assert ((out[shift:n].double() - want[shift:n]).abs() <= tol[shift:n]).all()
+
+
+@pytest.mark.parametrize("D,dtype,fp8", [(128, torch.bfloat16, False), (64, torch.float16, False),
+                                         (128, torch.float16, True)])
+@pytest.mark.parametrize("seqs,at", [([(40, 300)], 270), ([(3, 200)], 198), ([(90, 1000), (5, 1700)], 950),
+                                     ([(1, 400), (20, 40)], 399), ([(257, 257)], 100)])
+def test_infinities_and_nan_in_masked_places(cuda_device, D, dtype, fp8, seqs, at):
+    """Token `at` of each sequence (or its last) holds infinite and NaN elements of V, and the
+    one after it NaN in K: rows before them come out as if they were not there, rows that see
+    the V elements get them, rows that see the K get NaN."""
+    Hq, Hkv, bs = 8, 2, 16
+    b = make(seqs, Hq, Hkv, D, bs, dtype, 31, fp8)
+    clean = {k: b[k].clone() for k in ("kc", "vc")}
+    nan, inf = (0x7F, None) if fp8 else (float("nan"), float("inf"))
+    hurt = []
+    for s, (n, L) in enumerate(seqs):
+        t = min(at, L - 1)
+        block = int(b["tables"][s, t // bs])
+        b["vc"][block, 0, t % bs, 5] = nan
+        if not fp8:
+            b["vc"][block, 0, t % bs, 7] = inf
+            b["vc"][block, 1, t % bs, 9] = -inf
+        t2 = min(t + 1, L - 1)
+        b["kc"][int(b["tables"][s, t2 // bs]), 1, t2 % bs] = nan
+        hurt.append((t, t2))
+    out = call(b, torch.zeros_like(b["q"]))
+    b["kc"], b["vc"] = clean["kc"], clean["vc"]
+    want, tol = reference(b)
+    g = Hq // Hkv
+    for s, (n, L) in enumerate(seqs):
+        a, (t, t2) = int(b["starts"][s]), hurt[s]
+        for j in range(n):
+            pos, row, w, e = L - n + j, out[a + j].double(), want[a + j], tol[a + j]
+            good = torch.ones(Hq, D, dtype=torch.bool, device="cuda")
+            if pos >= t:
+                assert torch.isnan(row[:g, 5]).all()
+                good[:g, 5] = False
+                if not fp8:
+                    assert (row[:g, 7] == inf).all() and (pos >= t2 or (row[g:, 9] == -inf).all())
+                    good[:g, 7] = False
+                    good[g:, 9] = False
+            if pos >= t2:
+                assert torch.isnan(row[g:]).all()
+                good[g:] = False
+            assert ((row - w).abs() <= e)[good].all(), (s, j)
+
+
+def test_bad_metadata_is_flagged_and_never_faults(cuda_device):
+    import paged_kv_cache_187_gb300 as pa
+    b = make([(30, 200), (20, 100)], 4, 2, 128, 16, torch.bfloat16, 37)
+    ws = workspace(b, 4096)
+    out = torch.zeros_like(b["q"])
+
+    def flags(**change):
+        c = dict(b, **change)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        call(c, out, ws=ws, mcl=change.get("mcl", 200), status=status)
+        torch.cuda.synchronize()
+        return int(status)
+
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    assert flags() == 0
+    assert flags(starts_d=i32([0, 40, 30])) == pa.PA_DEVERR_BAD_LEN          # descending
+    assert flags(starts_d=i32([-5, 30, 50])) == pa.PA_DEVERR_BAD_LEN
+    assert flags(starts_d=i32([0, 30, 2 ** 31 - 1])) == pa.PA_DEVERR_BAD_LEN
+    assert flags(starts_d=i32([50, 0, 50])) == pa.PA_DEVERR_BAD_LEN
+    assert flags(lens_d=i32([300, 100])) == pa.PA_DEVERR_BAD_LEN             # > max_context_len
+    assert flags(lens_d=i32([-1, 100])) == pa.PA_DEVERR_BAD_LEN
+    assert flags(lens_d=i32([2 ** 31 - 1, 100]), mcl=4096) == pa.PA_DEVERR_BAD_LEN   # > the row
+    bad = b["tables"].clone()
+    bad[0, 3], bad[1, 0] = b["kc"].shape[0], -7
+    assert flags(tables=bad) == pa.PA_DEVERR_BAD_BLOCK
+    # overlapping chunks want more row tiles than there is room for
+    many = make([(20, 20)] * 12, 16, 1, 128, 16, torch.bfloat16, 38)
+    many["starts_d"] = i32([0, 240] * 6 + [0])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call(many, torch.zeros_like(many["q"]), status=status)
+    torch.cuda.synchronize()
+    assert int(status) == pa.PA_DEVERR_BAD_LEN
+    check(b, call(b, out, ws=ws))                                            # and all is well
+
+
+def test_streams_graphs_and_shared_workspaces(cuda_device):
+    """Captured calls give the eager results bit for bit, replayed with other inputs in place
+    too; two graphs on one workspace take turns; a call on a side stream with its own."""
+    shapes = [[(40, 900), (1, 3000)], [(1, 700), (300, 300), (5, 64)]]
+    bs = [make(s, 8, 2, 128, 16, torch.bfloat16, 41 + i) for i, s in enumerate(shapes)]
+    ws = max((workspace(b, 3000) for b in bs), key=lambda w: w.numel())
+    eager = [call(b, torch.zeros_like(b["q"]), ws=ws, mcl=3000) for b in bs]
+    torch.cuda.synchronize()
+    outs, graphs = [torch.zeros_like(b["q"]) for b in bs], []
+    for b, o in zip(bs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(b, o, ws=ws, mcl=3000)
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        for e, o in zip(eager, outs):
+            assert torch.equal(e, o)
+    # new contents in the captured buffers
+    new = make(shapes[0], 8, 2, 128, 16, torch.bfloat16, 77)
+    for k in ("q", "kc", "vc", "tables"):
+        bs[0][k].copy_(new[k])
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    check(bs[0], outs[0])
+    # two streams at once, each with its own workspace
+    side = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.zeros_like(ws) for _ in range(2)]
+    got = [torch.zeros_like(b["q"]) for b in bs]
+    want = [call(b, torch.zeros_like(b["q"]), ws=ws, mcl=3000) for b in bs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, o, w, st in zip(bs, got, spaces, side):
+            call(b, o, ws=w, mcl=3000, stream=st)
+    torch.cuda.synchronize()
+    for o, w in zip(got, want):
+        assert torch.equal(o, w)
+
+
+def test_the_same_call_gives_the_same_bits(cuda_device):
+    for fp8 in (False, True):
+        b = make([(70, 5000), (1, 900), (20, 8000)], 16, 2, 128, 16, torch.bfloat16, 43, fp8)
+        first = call(b, torch.zeros_like(b["q"]))
+        for _ in range(5):
+            assert torch.equal(first, call(b, torch.zeros_like(b["q"])))
+
+
+def test_single_tokens_agree_with_the_decode(cuda_device):
+    """One new token per sequence is an ordinary decode: both within tolerance of the formula."""
+    import paged_kv_cache_187_gb300 as pa
+    lens = [1, 5, 128, 129, 700, 2500]
+    b = make([(1, L) for L in lens], 32, 8, 128, 16, torch.bfloat16, 47)
+    ref = reference(b)
+    check(b, call(b, torch.zeros_like(b["q"])), ref)
+    out = torch.zeros_like(b["q"])
+    pa.pa_decode_v1(out, b["q"], b["kc"], b["vc"], b["tables"], b["lens_d"], 2500, b["scale"])
+    check(b, out, ref)
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """A pool of more than 2^32 bytes and 2^31 elements, the sequences in its last blocks."""
+    NB, Hkv, bs, D = 150_000, 8, 16, 128
+    small = make([(50, 700), (1, 300)], 16, Hkv, D, bs, torch.bfloat16, 53)
+    n = small["kc"].shape[0]
+    big = {}
+    for k in ("kc", "vc"):
+        big[k] = torch.empty((NB, Hkv, bs, D), dtype=torch.bfloat16, device="cuda")
+        big[k][NB - n:] = small[k]
+    t = small["tables"]
+    b = dict(small, **big, tables=torch.where(t >= 0, t + (NB - n), t))
+    assert b["kc"].numel() > 2 ** 31
+    assert torch.equal(call(b, torch.zeros_like(b["q"])), call(small, torch.zeros_like(b["q"])))
+    check(small, call(b, torch.zeros_like(b["q"])))
+
+
+def test_long_context(cuda_device):
+    run(make([(3, 70_001)], 8, 1, 128, 32, torch.float16, 59))
+
+
+def test_empty_calls(cuda_device):
+    b = make([(0, 10), (0, 0)], 4, 2, 128, 16, torch.float16, 61, extra=4)
+    out = call(b, torch.full_like(b["q"], 3.0))
+    torch.cuda.synchronize()
+    assert (out == 3).all()
