@@ -186,3 +186,43 @@ def test_move_blocks(cuda_device, layers, NB, Hkv, bs, D, dtype):
     assert int(status) == pa.PA_DEVERR_BAD_BLOCK
     for a, b in zip(pools, want):
         assert torch.equal(a, b)
+
+
+def test_move_flags_pairs_out_of_order_and_moves_tables_alone(cuda_device):
+    import paged_kv_cache_187_gb300 as pa
+    pools = [torch.randint(0, 100, (12, 2, 16, 64), device="cuda").to(torch.float16) for _ in range(2)]
+    want = pools[0].clone()
+    pairs = torch.tensor([[9, 1], [8, 0]], dtype=torch.int32, device="cuda")
+    want[1], want[0] = want[9], want[8]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_move_blocks(pools[:1], pools[1:], pairs, status=status)
+    assert int(status) == pa.PA_DEVERR_BAD_BLOCK             # reported, and copied all the same
+    assert torch.equal(pools[0], want)
+
+
+def test_rope_and_move_in_a_graph(cuda_device):
+    import paged_kv_cache_187_gb300 as pa
+    b = rope_case(33, 8, 2, 128, 128, 16, 3, torch.bfloat16, False, 8)
+    out = torch.zeros((33, 8, 128), dtype=torch.bfloat16, device="cuda")
+    before = (b["kp"].clone(), b["vp"].clone())
+    NB = b["kp"].shape[0]
+    free = torch.zeros((2 * NB, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+    pairs = torch.tensor([[NB, 0], [NB + 1, 1]], dtype=torch.int32, device="cuda")
+    table = torch.arange(2 * NB, dtype=torch.int32, device="cuda")[None].contiguous()
+    rope_call(b, out)
+    torch.cuda.synchronize()
+    eager = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rope_call(b, out)
+        pa.pa_move_blocks([free], [free.clone()], pairs, block_tables=table)
+    out.zero_()
+    b["kp"].copy_(before[0])
+    b["vp"].copy_(before[1])
+    free[NB:NB + 2] = 3.0
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager)
+    check_rope(b, out, before, False)
+    assert (free[:2] == 3).all() and table[0, NB:NB + 2].tolist() == [0, 1]
