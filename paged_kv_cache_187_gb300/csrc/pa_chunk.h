@@ -21,6 +21,11 @@ constexpr int32_t kPfItemCost = 2;
 // Shortest share of the work, in tiles, worth a CTA of its own when contexts are cut.
 constexpr int32_t kPfMinShare = 6;
 
+// Calls small enough for one unit per CTA, with contexts too short to be cut, are not
+// planned: each CTA finds its own unit from up to 32 sequences' metadata, one per lane.
+// (One chunk of 17 tokens over 317: 13.3 us a call with the plan kernel, 9.3 us without.)
+constexpr int32_t kPfDirectTokens = 1024;
+
 // Head of the prefill workspace, written by the plan kernel.  A row tile is a run of up to
 // 2 * tpt new tokens of a sequence; a unit is a row tile with one kv head, of as many
 // 128-token tiles as its last row sees; its cost is its tiles + kPfItemCost.
@@ -51,6 +56,7 @@ struct PrefillParams {
     float out_scale;           // v_scale for fp8 caches, else 1
     int32_t grid;              // CTAs of the attention launch
     int32_t max_row_tiles;     // what the workspace has room for
+    int32_t direct;            // no plan: CTA b takes unit b (see kPfDirectTokens)
     PfHeader* hdr;
     int4* seqs;                // [num_seqs] (q_start, q_len, len, first row tile)
     int32_t* seq_of;           // [row tiles] the sequence

@@ -5,7 +5,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
-#include "pa_chunk.h"
+#include "pa_chunk_device.cuh"
 #include "pa_device.cuh"
 
 namespace pa {
@@ -60,23 +60,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
     if (tid == 0) longest = 0;
     // the sequences: chunk, context, first row tile; bad metadata is clamped and reported
     int32_t row_tiles = 0;
-    const int64_t row_cap = (int64_t)p.max_blocks_per_seq * p.block_size;
-    const int32_t cap = row_cap < p.max_context_len ? (int32_t)row_cap : p.max_context_len;
     for (int32_t base = 0; base < p.num_seqs; base += kPlanThreads) {
         const int32_t s = base + tid;
-        int32_t lo = 0, n = 0, len = 0, tiles = 0;
-        if (s < p.num_seqs) {
-            const int32_t a = p.query_starts[s], b = p.query_starts[s + 1], l = p.context_lens[s];
-            lo = min(max(a, 0), p.num_tokens);
-            const int32_t hi = min(max(b, lo), p.num_tokens);
-            n = hi - lo;
-            len = min(max(l, 0), cap);
-            if ((lo != a || hi != b || len != l) && p.status) atomicOr(p.status, kBadLen);
-            tiles = n / span + (n % span != 0);
-        }
+        const PfChunk c = chunk_of(p, s, true);
         int32_t sum;
-        const int32_t at = row_tiles + block_scan(tiles, buf, &sum);
-        if (s < p.num_seqs) p.seqs[s] = make_int4(lo, n, len, at);
+        const int32_t at = row_tiles + block_scan(c.row_tiles, buf, &sum);
+        if (s < p.num_seqs) p.seqs[s] = make_int4(c.start, c.count, c.len, at);
         // chunks that overlap could ask for more row tiles than there is room for
         row_tiles = min(row_tiles + sum, p.max_row_tiles + 1);
     }

@@ -168,6 +168,9 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
     const int64_t tiles = (int64_t)L.max_row_tiles * a.num_kv_heads *
                           std::max(1, (a.max_context_len + pa::kPfTok - 1) / pa::kPfTok);
     p.grid = (int32_t)std::min<int64_t>(std::min(sms, pa::kPfMaxGrid), tiles);
+    p.direct = a.num_seqs <= 32 && a.max_context_len <= pa::kPfDirectTokens &&
+               (int64_t)L.max_row_tiles * a.num_kv_heads <= std::min(sms, pa::kPfMaxGrid);
+    if (p.direct) p.grid = L.max_row_tiles * a.num_kv_heads;
     uint8_t* w = static_cast<uint8_t*>(ws);
     p.hdr = reinterpret_cast<pa::PfHeader*>(w + L.hdr);
     p.seqs = reinterpret_cast<int4*>(w + L.seqs);
@@ -193,7 +196,7 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
     if ((st = encode(&km, a.key_cache, a.kv8, 2, dims, str, box)) != PA_OK) return st;
     if ((st = encode(&vm, a.value_cache, a.kv8, 2, dims, str, box)) != PA_OK) return st;
 
-    cudaError_t e = pa::launch_prefill_plan(p, stream);
+    cudaError_t e = p.direct ? cudaSuccess : pa::launch_prefill_plan(p, stream);
     if (e != cudaSuccess) return cuda_fail(e, "prefill plan launch");
     const bool bf16 = a.dtype == PA_BF16;
     e = a.kv8 ? pa::launch_prefill_fp8(bf16, qm, km, vm, p, stream)

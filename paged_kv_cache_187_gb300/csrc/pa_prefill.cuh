@@ -34,7 +34,7 @@
 // warps of a stream decide together whether to stop.
 #pragma once
 
-#include "pa_chunk.h"
+#include "pa_chunk_device.cuh"
 #include "pa_decode.cuh"
 
 namespace pa {
@@ -186,6 +186,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+// Waits for this thread's tensor-memory loads; x, loaded before, is not used before that.
+__device__ __forceinline__ void tmem_arrived(float (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]),
+                   "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]), "+f"(x[9]),
+                   "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]),
+                   "+f"(x[15]), "+f"(x[16]), "+f"(x[17]), "+f"(x[18]), "+f"(x[19]),
+                   "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]), "+f"(x[24]),
+                   "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]),
+                   "+f"(x[30]), "+f"(x[31])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -378,7 +391,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (warp == kWarpLoad) {
             // ---------------------------------------- items, Q and K tiles
-            const PfHeader hdr = *p.hdr;
+            PfHeader hdr = {};
+            int4 mine = make_int4(0, 0, 0, 0);   // direct: sequence `lane`, as the plan lists it
+            if (!p.direct) {
+                hdr = *p.hdr;
+            } else {
+                const PfChunk c = chunk_of(p, lane, lane < p.num_seqs && blockIdx.x == 0);
+                int32_t tiles = c.row_tiles, before = tiles;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t y = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o) before += y;
+                }
+                mine = make_int4(c.start, c.count, c.len, before - tiles);
+                int32_t all = __shfl_sync(0xffffffffu, before, 31);
+                if (all > p.max_row_tiles) {   // chunks that overlap
+                    if (lane == 0 && blockIdx.x == 0) flag_error(p.status, PA_DEVERR_BAD_LEN_);
+                    all = p.max_row_tiles;
+                }
+                hdr.total_units = (uint32_t)(all * Hkv);
+            }
             const int64_t shares = hdr.shares;
             // cut 0: the unit to take next; cut 1: the cost at which this share goes on, and
             // where it ends
@@ -407,8 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp_sees_abort(sm.abort)) {
                 } else if (!hdr.cut) {
                     if (w < (int32_t)hdr.total_units) {
-                        if (lane == 0) claimed = (int32_t)(gridDim.x + atomicAdd(&p.hdr->counter, 1u));
-                        rt = p.order[w / Hkv];
+                        if (p.direct) claimed = (int32_t)hdr.total_units;
+                        else if (lane == 0) claimed = (int32_t)(gridDim.x + atomicAdd(&p.hdr->counter, 1u));
+                        rt = p.direct ? w / Hkv : p.order[w / Hkv];
                         u.kvh = w % Hkv;
                     }
                 } else {
@@ -451,8 +484,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } while (false);
                 }
                 if (rt >= 0) {
-                    u.seq = p.seq_of[rt];
-                    const int4 q = p.seqs[u.seq];
+                    int4 q;
+                    if (p.direct) {
+                        // the last sequence whose first row tile is at or before this one
+                        u.seq = 31 - __clz(__ballot_sync(0xffffffffu, lane < p.num_seqs && mine.w <= rt));
+                        q.x = __shfl_sync(0xffffffffu, mine.x, u.seq);
+                        q.y = __shfl_sync(0xffffffffu, mine.y, u.seq);
+                        q.z = __shfl_sync(0xffffffffu, mine.z, u.seq);
+                        q.w = __shfl_sync(0xffffffffu, mine.w, u.seq);
+                    } else {
+                        u.seq = p.seq_of[rt];
+                        q = p.seqs[u.seq];
+                    }
                     u.q_start = q.x;
                     u.q_len = q.y;
                     u.len = q.z;
@@ -936,10 +979,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_fence_after_sync();
                 const bool masked = t0 + kCols > whole;
                 const int32_t seen = limit - t0;
-                // 32 of the row's 64 scores, masked
+                // 32 of the row's 64 scores, loaded before, masked
                 auto scores = [&](int h, float (&x)[32]) {
-                    tmem_ld32(ts + 32 * h, x);
-                    tmem_wait_ld();
+                    tmem_arrived(x);
                     if (masked) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) x[c] = 32 * h + c < seen ? x[c] : hidden;
@@ -962,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int h = 0; h < kDims / 32; ++h) {
                             float o[32];
                             tmem_ld32(to + 32 * h, o);
-                            tmem_wait_ld();
+                            tmem_arrived(o);
 #pragma unroll
                             for (int c = 0; c < 32; ++c) o[c] *= a;
                             tmem_st32(to + 32 * h, reinterpret_cast<const uint32_t*>(o));
@@ -975,6 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int h = 0; h < kCols / 32; ++h) {
                         float x[32];
+                        tmem_ld32(ts + 32 * h, x);
                         scores(h, x);
 #pragma unroll
                         for (int c = 0; c < 32; ++c) m = fmaxf(m, x[c] * p.scale_log2);
@@ -993,14 +1036,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t nref2 = pack_f32(nref, nref);
                     float mx[2] = {-INFINITY, -INFINITY};
                     uint64_t s2[2] = {0ull, 0ull};
+                    // (the second half's scores are on their way while the first's weights
+                    // are taken)
+                    float x[kCols / 32][32];
+                    tmem_ld32(ts, x[0]);
 #pragma unroll
                     for (int h = 0; h < kCols / 32; ++h) {
-                        float x[32];
-                        scores(h, x);
+                        scores(h, x[h]);
+                        if (h + 1 < kCols / 32) tmem_ld32(ts + 32 * (h + 1), x[h + 1]);
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
                             float a, b;
-                            unpack_f32(fma_x2(pack_f32(x[2 * c], x[2 * c + 1]), scale2, nref2), a, b);
+                            unpack_f32(fma_x2(pack_f32(x[h][2 * c], x[h][2 * c + 1]), scale2, nref2), a, b);
                             mx[c & 1] = max3(mx[c & 1], a, b);
                             a = fast_exp2(a);
                             b = fast_exp2(b);

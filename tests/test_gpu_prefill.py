@@ -361,3 +361,16 @@ def test_empty_calls(cuda_device):
     out = call(b, torch.full_like(b["q"], 3.0))
     torch.cuda.synchronize()
     assert (out == 3).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,bs,dtype,fp8", [
+    (8, 2, 128, 16, torch.bfloat16, False), (4, 1, 64, 32, torch.float16, False),
+    (16, 1, 128, 16, torch.float16, True)])
+@pytest.mark.parametrize("seqs", [
+    [(17, 317)], [(1, 1)], [(1, 1024)], [(0, 3), (0, 0), (5, 70), (0, 9), (40, 40), (0, 1)],
+    [(1, 7 * i + 1) for i in range(32)], [(1, 40)] * 33, [(100, 1000), (3, 1), (9, 4)], [(1, 1025)],
+    [(600, 1000)]])
+def test_small_calls_without_a_plan_and_their_neighbours(cuda_device, Hq, Hkv, D, bs, dtype, fp8, seqs):
+    """Up to 32 sequences, a unit per CTA and contexts up to 1024 tokens are not planned; one
+    sequence, token or unit more are."""
+    run(make(seqs, Hq, Hkv, D, bs, dtype, 67, fp8))
