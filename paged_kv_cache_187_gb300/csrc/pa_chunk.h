@@ -97,7 +97,6 @@ struct RopeParams {
     const float* inv_freq;                    // [rot_dim / 2]
     int32_t num_tokens, num_q_heads, num_kv_heads, head_size, rot_dim, block_size, num_blocks;
     int32_t interleaved;
-    uint32_t unit_div;                        // ceil(2^32 / (head_size / 16)): e / units = umulhi(e, .)
     float k_inv, v_inv;                       // fp8: reciprocal scales
     int32_t* status;
     uint8_t axis[kMaxRopePairs];              // position axis of each rotated pair

@@ -135,20 +135,45 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
 }
 
 // ------------------------------------------------------------------ rotary + cache write
-constexpr int kRopeThreads = 128;
-constexpr int kRopeUnits = 4;      // 32-byte units a thread has in flight
+// Threads per token and 32-byte units a thread has in flight.  8200 tokens of 32 + 8 heads of
+// 128 (202 MB moved, slots at random): 64 threads with 2 units 34.7 us, 128 with 4 41, 32
+// with 3 36.7, against 30.1 us at the measured copy bandwidth.  More threads leave fewer
+// tokens per SM to cover the wait for a token's positions and angles.
+constexpr int kRopeThreads = 64;
+constexpr int kRopeUnits = 2;
+
+// A position's step in turns, as a 64-bit fraction: inv_freq / 2 pi modulo 1.  inv_freq is
+// m 2^e with an integer m below 2^24; m times the first 96 bits of 1 / 2 pi is shifted into
+// place.  Within 2^-64 of a turn (|inv_freq| < 2^24).
+__device__ __forceinline__ unsigned long long turn_step(float inv_freq) {
+    const uint32_t bits = __float_as_uint(inv_freq), ex = (bits >> 23) & 255u;
+    const uint32_t m = ex ? (bits & 0x7FFFFFu) | 0x800000u : bits & 0x7FFFFFu;
+    const int32_t shift = 32 + 150 - (int32_t)(ex ? ex : 1u);      // of the product, to the right
+    const unsigned long long p0 = (unsigned long long)m * 0x7F09D5F4u;
+    const unsigned long long p1 = (unsigned long long)m * 0x9391054Au + (p0 >> 32);
+    const unsigned long long p2 = (unsigned long long)m * 0x28BE60DBu + (p1 >> 32);
+    // words of the product, lowest first: (uint32)p0, (uint32)p1, p2 (two words)
+    const unsigned long long low = (p1 << 32) | (uint32_t)p0, high = p2;
+    unsigned long long f;
+    if (shift >= 128) f = 0;
+    else if (shift >= 64) f = high >> (shift - 64);
+    else if (shift > 0) f = (high << (64 - shift)) | (low >> shift);
+    else f = low << (-shift & 63);
+    return (bits >> 31) ? 0ull - f : f;
+}
 
 // Rotates the query and key rows of new tokens and writes K and V into the pools.
 //
 // Pair i of a row turns by the angle positions[axis(i)][token] * inv_freq[i].  In turns,
-// that product is taken in 64-bit fixed point: inv_freq / 2 pi is a 64-bit fraction of a
-// turn, its product with the integer position wraps modulo one turn exactly, and what is
-// left is rounded once, to fp32, so that far positions lose nothing: the fraction is
-// within 2^-53 of itself, 2^-22 radians at position 2^31.
+// that product is taken in 64-bit fixed point: the step is a 64-bit fraction of a turn, its
+// product with the integer position wraps modulo one turn exactly, and what is left is
+// rounded once, to fp32, so that far positions lose nothing: 2^31 steps are off by 2^-33
+// turns.
 //
 // A CTA takes a token.  Its rows are cut into 32-byte units (two 16-byte pieces: 8 pairs,
-// or 16 dimensions that do not turn); the first units are on their way while the pairs'
-// cosines and sines are computed, one thread per pair, into shared memory.
+// or 16 dimensions that do not turn), and a thread has the same unit of every few heads, so
+// that its pairs' cosines and sines are read once; the first heads' units are on their way
+// while those are computed, one thread per pair, into shared memory.
 template <bool BF16, bool KV8>
 __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const RopeParams p) {
     __shared__ float2 turn[kMaxRopePairs];
@@ -162,123 +187,119 @@ __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const Rope
         slot = -1;
     }
     const int64_t block = slot / p.block_size, offset = slot - block * p.block_size;
-    const uint32_t units = (uint32_t)p.head_size / 16, rot_units = (uint32_t)p.rot_dim / 16;
-    const uint32_t hq = (uint32_t)p.num_q_heads, hk = (uint32_t)p.num_kv_heads;
-    // a padding token's K and V are not written
-    const uint32_t all = (slot < 0 ? hq : hq + 2 * hk) * units;
-    struct Unit {
-        uint32_t kind, head, c;      // 0 query, 1 key, 2 value; head; unit within the row
-        bool rot;
-        uint32_t d0, d1;             // first dimensions of its two pieces
+    const int32_t units = p.head_size / 16, hq = p.num_q_heads, hk = p.num_kv_heads;
+    // this thread's unit c of heads h0, h0 + step, ..: first the query's, then the key's and
+    // the value's (a padding token's are not written)
+    const int32_t step = kRopeThreads / units, h0 = tid / units, c = tid - h0 * units;
+    const int32_t heads = h0 < step ? (slot < 0 ? hq : hq + 2 * hk) : 0;
+    const bool turns = c < p.rot_dim / 16, apart = turns && !p.interleaved;
+    struct Place {
+        int32_t kind, head;      // 0 query, 1 key, 2 value
+        int32_t d0, d1;          // first dimensions of the unit's pieces
     };
-    auto unit = [&](uint32_t e) {
-        Unit u;
-        const uint32_t h = units == 1 ? e : __umulhi(e, p.unit_div);
-        u.c = e - h * units;
-        u.kind = h < hq ? 0 : h < hq + hk ? 1 : 2;
-        u.head = u.kind == 0 ? h : u.kind == 1 ? h - hq : h - hq - hk;
-        u.rot = u.kind != 2 && u.c < rot_units;
-        const bool apart = u.rot && !p.interleaved;
-        u.d0 = apart ? 8 * u.c : 16 * u.c;
-        u.d1 = apart ? half + 8 * u.c : 16 * u.c + 8;
-        return u;
+    auto place = [&](int32_t h) {
+        Place q;
+        q.kind = h < hq ? 0 : h < hq + hk ? 1 : 2;
+        q.head = q.kind == 0 ? h : q.kind == 1 ? h - hq : h - hq - hk;
+        const bool a = apart && q.kind != 2;
+        q.d0 = a ? 8 * c : 16 * c;
+        q.d1 = a ? half + 8 * c : 16 * c + 8;
+        return q;
     };
     uint4 xa[kRopeUnits], xb[kRopeUnits];
-    auto load = [&](uint32_t base) {
+    auto load = [&](int32_t first) {
 #pragma unroll
         for (int k = 0; k < kRopeUnits; ++k) {
-            const uint32_t e = base + k * kRopeThreads;
-            if (e >= all) break;
-            const Unit u = unit(e);
-            const uint16_t* src = u.kind == 0   ? static_cast<const uint16_t*>(p.query) + i * p.q_stride
-                                  : u.kind == 1 ? static_cast<const uint16_t*>(p.key) + i * p.k_stride
+            const int32_t h = first + k * step;
+            if (h >= heads) break;
+            const Place q = place(h);
+            const uint16_t* src = q.kind == 0   ? static_cast<const uint16_t*>(p.query) + i * p.q_stride
+                                  : q.kind == 1 ? static_cast<const uint16_t*>(p.key) + i * p.k_stride
                                                 : static_cast<const uint16_t*>(p.value) + i * p.v_stride;
-            src += (size_t)u.head * p.head_size;
-            xa[k] = *reinterpret_cast<const uint4*>(src + u.d0);
-            xb[k] = *reinterpret_cast<const uint4*>(src + u.d1);
+            src += q.head * p.head_size;
+            xa[k] = *reinterpret_cast<const uint4*>(src + q.d0);
+            xb[k] = *reinterpret_cast<const uint4*>(src + q.d1);
         }
     };
-    load(tid);
+    load(h0);
     for (int32_t e = tid; e < half; e += kRopeThreads) {
-        double f = (double)p.inv_freq[e] * 0.15915494309189533577;   // 1 / (2 pi)
-        f -= floor(f);
-        const unsigned long long step = (unsigned long long)(f * 18446744073709551616.0);
         const unsigned long long pos = (unsigned long long)p.positions[(int64_t)p.axis[e] * p.num_tokens + i];
         // the upper half, as a signed number of half turns in [-1, 1)
-        const float x = (float)(int32_t)((step * pos) >> 32) * 4.656612873077392578125e-10f;
+        const float x = (float)(int32_t)((turn_step(p.inv_freq[e]) * pos) >> 32) * 4.656612873077392578125e-10f;
         float sn, cs;
         sincospif(x, &sn, &cs);
         turn[e] = make_float2(cs, sn);
     }
     __syncthreads();
-    for (uint32_t base = tid; base < all; base += kRopeUnits * kRopeThreads) {
-        if (base != (uint32_t)tid) load(base);
+    float4 w[4];                 // (cos, sin) of this thread's eight pairs
+    if (turns) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = reinterpret_cast<const float4*>(&turn[8 * c])[j];
+    }
+    for (int32_t first = h0; first < heads; first += kRopeUnits * step) {
+        if (first != h0) load(first);
 #pragma unroll
         for (int k = 0; k < kRopeUnits; ++k) {
-            const uint32_t e = base + k * kRopeThreads;
-            if (e >= all) break;
-            const Unit u = unit(e);
+            const int32_t h = first + k * step;
+            if (h >= heads) break;
+            const Place q = place(h);
+            const bool rot = turns && q.kind != 2;
+            uint4 ya = xa[k], yb = xb[k];      // a unit that does not turn goes out as it came in
             float a[8], b[8];
-            const uint32_t wa[4] = {xa[k].x, xa[k].y, xa[k].z, xa[k].w};
-            const uint32_t wb[4] = {xb[k].x, xb[k].y, xb[k].z, xb[k].w};
+            if (rot || (KV8 && q.kind != 0)) {
+                const uint32_t wa[4] = {xa[k].x, xa[k].y, xa[k].z, xa[k].w};
+                const uint32_t wb[4] = {xb[k].x, xb[k].y, xb[k].z, xb[k].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                unpack2<BF16>(wa[j], a[2 * j], a[2 * j + 1]);
-                unpack2<BF16>(wb[j], b[2 * j], b[2 * j + 1]);
+                for (int j = 0; j < 4; ++j) {
+                    unpack2<BF16>(wa[j], a[2 * j], a[2 * j + 1]);
+                    unpack2<BF16>(wb[j], b[2 * j], b[2 * j + 1]);
+                }
             }
-            if (u.rot) {
-                const float4* t4 = reinterpret_cast<const float4*>(&turn[8 * u.c]);
+            if (rot) {
                 if (!p.interleaved) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 w = t4[j];       // (cos, sin) of two pairs
                         const float x = a[2 * j], y = b[2 * j], z = a[2 * j + 1], v = b[2 * j + 1];
-                        a[2 * j] = x * w.x - y * w.y;
-                        b[2 * j] = x * w.y + y * w.x;
-                        a[2 * j + 1] = z * w.z - v * w.w;
-                        b[2 * j + 1] = z * w.w + v * w.z;
+                        a[2 * j] = x * w[j].x - y * w[j].y;
+                        b[2 * j] = x * w[j].y + y * w[j].x;
+                        a[2 * j + 1] = z * w[j].z - v * w[j].w;
+                        b[2 * j + 1] = z * w[j].w + v * w[j].z;
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 w = t4[j];
                         float* r = j < 2 ? a + 4 * j : b + 4 * (j - 2);
                         const float x = r[0], y = r[1], z = r[2], v = r[3];
-                        r[0] = x * w.x - y * w.y;
-                        r[1] = x * w.y + y * w.x;
-                        r[2] = z * w.z - v * w.w;
-                        r[3] = z * w.w + v * w.z;
+                        r[0] = x * w[j].x - y * w[j].y;
+                        r[1] = x * w[j].y + y * w[j].x;
+                        r[2] = z * w[j].z - v * w[j].w;
+                        r[3] = z * w[j].w + v * w[j].z;
                     }
                 }
+                ya = make_uint4(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]), pack2<BF16>(a[4], a[5]),
+                                pack2<BF16>(a[6], a[7]));
+                yb = make_uint4(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]), pack2<BF16>(b[4], b[5]),
+                                pack2<BF16>(b[6], b[7]));
             }
-            const int64_t row = u.kind == 0 ? i * hq + u.head
-                                            : (block * hk + u.head) * p.block_size + offset;
-            if (KV8 && u.kind != 0) {
+            const int64_t row = q.kind == 0 ? i * hq + q.head : (block * hk + q.head) * p.block_size + offset;
+            if (KV8 && q.kind != 0) {
                 // e4m3(x * (1 / scale)): fp32 product, nearest-even, saturated
-                uint8_t* dst = static_cast<uint8_t*>(u.kind == 1 ? p.key_cache : p.value_cache) + row * p.head_size;
-                const float inv = u.kind == 1 ? p.k_inv : p.v_inv;
+                uint8_t* dst = static_cast<uint8_t*>(q.kind == 1 ? p.key_cache : p.value_cache) + row * p.head_size;
+                const float inv = q.kind == 1 ? p.k_inv : p.v_inv;
                 uint32_t qa[4], qb[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     qa[j] = f32x2_to_e4m3x2(__fmul_rn(a[2 * j], inv), __fmul_rn(a[2 * j + 1], inv));
                     qb[j] = f32x2_to_e4m3x2(__fmul_rn(b[2 * j], inv), __fmul_rn(b[2 * j + 1], inv));
                 }
-                *reinterpret_cast<uint2*>(dst + u.d0) = make_uint2(qa[0] | (qa[1] << 16), qa[2] | (qa[3] << 16));
-                *reinterpret_cast<uint2*>(dst + u.d1) = make_uint2(qb[0] | (qb[1] << 16), qb[2] | (qb[3] << 16));
+                *reinterpret_cast<uint2*>(dst + q.d0) = make_uint2(qa[0] | (qa[1] << 16), qa[2] | (qa[3] << 16));
+                *reinterpret_cast<uint2*>(dst + q.d1) = make_uint2(qb[0] | (qb[1] << 16), qb[2] | (qb[3] << 16));
             } else {
                 uint16_t* dst =
-                    static_cast<uint16_t*>(u.kind == 0 ? p.query_out : u.kind == 1 ? p.key_cache : p.value_cache) +
+                    static_cast<uint16_t*>(q.kind == 0 ? p.query_out : q.kind == 1 ? p.key_cache : p.value_cache) +
                     row * p.head_size;
-                // a unit that does not turn goes out as it came in
-                uint4 ya = xa[k], yb = xb[k];
-                if (u.rot) {
-                    ya = make_uint4(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]), pack2<BF16>(a[4], a[5]),
-                                    pack2<BF16>(a[6], a[7]));
-                    yb = make_uint4(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]), pack2<BF16>(b[4], b[5]),
-                                    pack2<BF16>(b[6], b[7]));
-                }
-                *reinterpret_cast<uint4*>(dst + u.d0) = ya;
-                *reinterpret_cast<uint4*>(dst + u.d1) = yb;
+                *reinterpret_cast<uint4*>(dst + q.d0) = ya;
+                *reinterpret_cast<uint4*>(dst + q.d1) = yb;
             }
         }
     }

@@ -245,8 +245,6 @@ pa_status run_rope(pa::RopeParams& p, const int32_t* pair_axes, int32_t num_axes
         return fail(PA_ERR_INVALID_ARG, "rope_and_cache: buffers must be 16-byte aligned");
     if (p.query_out == p.query && p.q_stride != qrow)
         return fail(PA_ERR_INVALID_ARG, "rope_and_cache: query may be rotated in place only when dense");
-    const uint32_t units = (uint32_t)p.head_size / 16;
-    p.unit_div = units == 1 ? 0u : (uint32_t)(((1ull << 32) + units - 1) / units);
     p.k_inv = kv8 ? 1.0f / k_scale : 1.f;
     p.v_inv = kv8 ? 1.0f / v_scale : 1.f;
     cudaError_t e = pa::launch_rope_and_cache(p, dtype == PA_BF16, kv8, stream);
