@@ -61,6 +61,12 @@
  *           pa_decode_auto               out <- attention of each query over its
  *                                        sequence's pooled tokens (workspace of
  *                                        pa_decode_auto_workspace_size bytes)
+ * A prompt, or a piece of one, beside the running sequences (one layer)
+ *   host    pa_alloc_reserve_batch, pa_alloc_append   blocks and slots of the new tokens
+ *   device  pa_rope_and_cache            rotated queries out, rotated K and V into the pools
+ *           pa_prefill                   out <- attention of every new token over its
+ *                                        sequence's tokens up to its own position
+ *   pa_alloc_shrink and pa_move_blocks give the end of the pools back.
  *   pa_decode_step issues both device calls at once; pa_decode_step_host also copies
  *   the step's inputs from host memory and the output back; pa_advance_step moves the
  *   lengths and slots on the device between the steps of a multi-step loop.
@@ -403,7 +409,7 @@ pa_status pa_copy_blocks(void* key_cache, void* value_cache, const int32_t* bloc
  *   (text: one; images and video: time, height, width), any integer within +-2^31 (beyond,
  *   angles lose accuracy).  pair_axes: HOST int32 [rot_dim / 2], the axis of each rotated
  *   pair; NULL for one axis.  inv_freq: device fp32 [rot_dim / 2], radians per position,
- *   finite.
+ *   finite and below 2^24 in magnitude.
  * The first rot_dim dimensions of a query or key row turn in pairs, the others stay:
  *   (x, y) -> (x cos a - y sin a, x sin a + y cos a),
  *   a = positions[pair_axes[i]][token] * inv_freq[i] for pair i,
@@ -447,8 +453,9 @@ pa_status pa_rope_and_cache_fp8(void* query_out, const void* query, const void* 
  *   query, out    [num_tokens][num_q_heads][head_size], fp16 or bf16 (also the pools' type)
  *   query_starts  int32 [num_seqs + 1], ascending, within 0 .. num_tokens; rows outside
  *                 query_starts[0] .. query_starts[num_seqs] are left as they are
- * and the rest as for pa_decode_v2.  num_tokens is at most 2^24.  Scores and sums are fp32;
- * the softmax weights enter the product with V rounded to the cache's 16-bit type.
+ * and the rest as for pa_decode_v2.  num_tokens is at most 2^24; scale is finite.  Scores and
+ * sums are fp32 (scores up to 2^20 in magnitude); the softmax weights enter the product with
+ * V rounded to the cache's 16-bit type.  The same call gives the same bits every time.
  * Bad query_starts (descending, outside the rows) or lengths are clamped and flagged
  * PA_DEVERR_BAD_LEN; block-table entries outside the pool read as zero rows and are flagged
  * PA_DEVERR_BAD_BLOCK.
