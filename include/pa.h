@@ -61,15 +61,16 @@
  *           pa_decode_auto               out <- attention of each query over its
  *                                        sequence's pooled tokens (workspace of
  *                                        pa_decode_auto_workspace_size bytes)
+ *   pa_decode_step issues both device calls at once; pa_decode_step_host also copies
+ *   the step's inputs from host memory and the output back; pa_advance_step moves the
+ *   lengths and slots on the device between the steps of a multi-step loop.
+ *
  * A prompt, or a piece of one, beside the running sequences (one layer)
  *   host    pa_alloc_reserve_batch, pa_alloc_append   blocks and slots of the new tokens
  *   device  pa_rope_and_cache            rotated queries out, rotated K and V into the pools
  *           pa_prefill                   out <- attention of every new token over its
  *                                        sequence's tokens up to its own position
  *   pa_alloc_shrink and pa_move_blocks give the end of the pools back.
- *   pa_decode_step issues both device calls at once; pa_decode_step_host also copies
- *   the step's inputs from host memory and the output back; pa_advance_step moves the
- *   lengths and slots on the device between the steps of a multi-step loop.
  */
 #ifndef PA_H_
 #define PA_H_
