@@ -18,6 +18,8 @@ constexpr int32_t kPfTok = 128;
 constexpr int32_t kPfMaxGrid = 160;
 // What an item costs beside its tiles (Q, the first scores, the rows' output), in tiles.
 constexpr int32_t kPfItemCost = 2;
+// What cutting costs a CTA (partial results written, read and joined), in tiles.
+constexpr int32_t kPfCutCost = 6;
 // Shortest share of the work, in tiles, worth a CTA of its own when contexts are cut.
 constexpr int32_t kPfMinShare = 6;
 

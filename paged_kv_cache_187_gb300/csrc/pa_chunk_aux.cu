@@ -49,23 +49,25 @@ constexpr int kPlanSeqs = 512, kPlanTiles = 2048;
 
 // Lists the row tiles of a ragged batch and settles how the attention kernel shares them
 // out (see PfHeader).  Whole units are claimed longest first, which leaves the shortest for
-// the end; where the longest unit is more than half of a CTA's share of the work (few or
-// long units), the work is cut into equal shares instead, whatever the units' ends.  Both
-// sides, whole against cut (us; 32 query and 8 kv heads of 128 unless said): a prompt of 8192
-// tokens, longest 0.3 of a share, 370 / 476; 2 chunks beside 61 single tokens, 0.3, 176 / 212;
-// 2 chunks of about 1050 tokens behind 9-14 K, fp8, 0.7, 372 / 367; 4 chunks of 24 tokens
-// behind 50-62 K (64 query heads), 5 shares, 292 / 187.
+// the end.  Where that would still leave the longest CTA over an equal share by more than
+// what joining partial results costs (few or long units), the work is cut into equal shares
+// instead, whatever the units' ends.  Both sides, whole / cut (us a call; 32 query and 8 kv
+// heads of 128, bf16, 16-token blocks): prompts of 2048, 4096 and 8192 tokens 49 / 55, 112 /
+// 152 and 353 / 478; 2 chunks of 400-900 beside 61 single tokens 176 / 213; 16 chunks of 200
+// behind 1 K 80 / 96; 2 of 700 behind 4 K 112 / 89; 1 of 512 behind 16 K 191 / 108; 8 of 64
+// behind 8 K 104 / 79; 64 query heads, 4 chunks of 24 behind 50-62 K 640 / 188.  The rule takes
+// the better side of each.
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillParams p) {
     __shared__ int32_t buf[32];
     __shared__ int32_t hist[kBuckets], first[kBuckets];
-    __shared__ int32_t longest;
+    __shared__ int32_t longest, whole;
     __shared__ int4 seq_s[kPlanSeqs];
     __shared__ int32_t tiles_s[kPlanTiles];
     allow_dependent_launch();
     grid_dependency_wait();
     const int32_t tid = threadIdx.x, span = 2 * p.tpt;
     if (tid < kBuckets) hist[tid] = 0;
-    if (tid == 0) longest = 0;
+    if (tid == 0) longest = whole = 0;
     // the sequences: chunk, context, first row tile; bad metadata is clamped and reported
     int32_t row_tiles = 0;
     for (int32_t base = 0; base < p.num_seqs; base += kPlanThreads) {
@@ -122,19 +124,32 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
     const long long units = (long long)row_tiles * p.num_kv_heads, all = cost * p.num_kv_heads;
     // shares: all CTAs, unless that makes them too short to be worth it
     const long long shares = max(1ll, min((long long)p.grid, max(units, all / kPfMinShare)));
-    const bool cut = longest > 1 && 2 * (longest + kPfItemCost) * shares > all && units > 0;
-    if (!cut) {
-        const int32_t scale = longest + 1;
-        auto tiles_at = [&](int32_t i) { return i < kPlanTiles ? tiles_s[i] : tiles_of(i, p.seq_of[i]); };
-        auto bucket = [&](int32_t n) {
-            return kBuckets - 1 - min(kBuckets - 1, (int32_t)((int64_t)n * kBuckets / scale));
-        };
-        for (int32_t i = tid; i < row_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(tiles_at(i))], 1);
-        __syncthreads();
+    // Row tiles by length, longest first, and from that what whole units would take: with m
+    // CTAs some CTA gets j of the first (j - 1) m + 1 units, all at least as long as the last.
+    const int32_t scale = longest + 1;
+    auto tiles_at = [&](int32_t i) { return i < kPlanTiles ? tiles_s[i] : tiles_of(i, p.seq_of[i]); };
+    auto bucket = [&](int32_t n) {
+        return kBuckets - 1 - min(kBuckets - 1, (int32_t)((int64_t)n * kBuckets / scale));
+    };
+    for (int32_t i = tid; i < row_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(tiles_at(i))], 1);
+    __syncthreads();
+    {
         int32_t sum;
-        const int32_t at = block_scan(tid < kBuckets ? hist[tid] : 0, buf, &sum);
-        if (tid < kBuckets) first[tid] = at;
+        const int32_t h = tid < kBuckets ? hist[tid] : 0;
+        const int32_t at = block_scan(h, buf, &sum);
+        if (tid < kBuckets) {
+            first[tid] = at;
+            const int32_t most = (int32_t)(((int64_t)(kBuckets - tid) * scale + kBuckets - 1) / kBuckets) - 1;
+            for (int32_t j = 1; j <= 4; ++j) {
+                const long long k = (long long)(j - 1) * p.grid;
+                if ((long long)at * p.num_kv_heads <= k && k < (long long)(at + h) * p.num_kv_heads)
+                    atomicMax(&whole, j * (min(most, longest) + kPfItemCost));
+            }
+        }
         __syncthreads();
+    }
+    const bool cut = longest > 1 && (whole - kPfCutCost) * shares > all;
+    if (!cut) {
         for (int32_t i = tid; i < row_tiles; i += kPlanThreads)
             p.order[atomicAdd(&first[bucket(tiles_at(i))], 1)] = i;
     } else {
