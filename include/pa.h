@@ -454,7 +454,8 @@ pa_status pa_rope_and_cache_fp8(void* query_out, const void* query, const void* 
  *   query, out    [num_tokens][num_q_heads][head_size], fp16 or bf16 (also the pools' type)
  *   query_starts  int32 [num_seqs + 1], ascending, within 0 .. num_tokens; rows outside
  *                 query_starts[0] .. query_starts[num_seqs] are left as they are
- * and the rest as for pa_decode_v2.  num_tokens is at most 2^24; scale is finite.  Scores and
+ * and the rest as for pa_decode_v2.  num_tokens is at most 2^24, a context at most 2^30
+ * tokens (clamped and flagged past that); scale is finite.  Scores and
  * sums are fp32 (scores up to 2^20 in magnitude); the softmax weights enter the product with
  * V rounded to the cache's 16-bit type.  The same call gives the same bits every time.
  * Bad query_starts (descending, outside the rows) or lengths are clamped and flagged

@@ -113,8 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
             if (n > 0) atomicMax(&longest, n);
             n += kPfItemCost;
         }
-        int32_t sum;      // (512 row tiles of at most 2^24 tiles each: below 2^31 by far in use,
-                          // and a context of 2^31 tokens is 2^24 tiles)
+        int32_t sum;      // (512 row tiles of at most 2^21 each; a longer context counts as that)
         const int32_t at = block_scan(min(n, 1 << 21), buf, &sum);
         if (i < row_tiles) p.before[i] = cost + at;
         cost += sum;
@@ -206,7 +205,7 @@ __device__ __forceinline__ unsigned long long turn_step(float inv_freq) {
 // while those are computed, one thread per pair, into shared memory.
 template <bool BF16, bool KV8>
 __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const RopeParams p) {
-    __shared__ float2 turn[kMaxRopePairs];
+    __shared__ __align__(16) float2 turn[kMaxRopePairs];
     allow_dependent_launch();   // what follows waits for this kernel before it reads the pools
     grid_dependency_wait();
     const int64_t i = blockIdx.x;
@@ -419,7 +418,7 @@ cudaError_t launch_rope_and_cache(const RopeParams& p, bool bf16, bool kv8, cuda
 
 cudaError_t launch_move_blocks(const MoveParams& p, cudaStream_t stream) {
     // An ordinary launch: the tables it rewrites may be read early by a kernel after it.
-    move_blocks_kernel<<<dim3((unsigned)(p.num_pairs + (p.block_tables ? kMoveTableCtas : 0)),
+    move_blocks_kernel<<<dim3((unsigned)p.num_pairs + (p.block_tables ? kMoveTableCtas : 0u),
                               (unsigned)std::max(2 * p.num_layers, 1)),
                          kMoveThreads, 0, stream>>>(p);
     return cudaGetLastError();

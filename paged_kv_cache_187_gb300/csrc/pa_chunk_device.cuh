@@ -15,7 +15,8 @@ __device__ __forceinline__ PfChunk chunk_of(const PrefillParams& p, int32_t s, b
     PfChunk c = {0, 0, 0, 0};
     if (s >= p.num_seqs) return c;
     const int64_t row_cap = (int64_t)p.max_blocks_per_seq * p.block_size;
-    const int32_t cap = row_cap < p.max_context_len ? (int32_t)row_cap : p.max_context_len;
+    // (2^30 tokens: positions and their tiles stay within 32 bits)
+    const int32_t cap = (int32_t)min(min(row_cap, (int64_t)p.max_context_len), (int64_t)1 << 30);
     const int32_t a = p.query_starts[s], b = p.query_starts[s + 1], l = p.context_lens[s];
     c.start = min(max(a, 0), p.num_tokens);
     const int32_t end = min(max(b, c.start), p.num_tokens);

@@ -166,7 +166,7 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
     p.max_row_tiles = L.max_row_tiles;
     // one CTA per SM, but never more than tiles
     const int64_t tiles = (int64_t)L.max_row_tiles * a.num_kv_heads *
-                          std::max(1, (a.max_context_len + pa::kPfTok - 1) / pa::kPfTok);
+                          std::max(1, a.max_context_len / pa::kPfTok + (a.max_context_len % pa::kPfTok != 0));
     p.grid = (int32_t)std::min<int64_t>(std::min(sms, pa::kPfMaxGrid), tiles);
     p.direct = a.num_seqs <= 32 && a.max_context_len <= pa::kPfDirectTokens &&
                (int64_t)L.max_row_tiles * a.num_kv_heads <= std::min(sms, pa::kPfMaxGrid);
