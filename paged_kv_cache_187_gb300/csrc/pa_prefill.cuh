@@ -15,12 +15,15 @@
 //     O += P V    M = 128 rows, N = head dims, P read from tensor memory, V MN-major
 // The MMA thread issues PV of one stream and its next QK^T back to back, stream by stream,
 // so the tensor pipe works on one stream while the other's softmax runs.  A row's
-// reference moves (and O is rescaled in tensor memory) only when a score passes it by
-// 2^8: the weights stay below 2^8 and their sum is held in fp32.
+// reference moves (and O is rescaled in tensor memory) only when its largest score passes
+// the one that set it by 2^8; the weights' sum is held in fp32.
 //
 // Weights enter PV as one 16-bit term: rounding them costs at most half a step of the
 // 16-bit type relative to each weight (2^-8 bf16, 2^-11 fp16), as much as rounding the
-// output itself; a second term would cost half of PV's matrix rate again.
+// output itself; a second term would cost half of PV's matrix rate again.  fp16 weights are
+// taken 2^7 larger, up to 2^15: what is lost below fp16's normal range is then at most
+// 2^-32 of the row's largest weight per token, so that a long tail of small weights behind
+// one large one is not rounded away.
 //
 // Rows must not see what they are masked from, and a weight of 0 times an infinite or NaN
 // value would be NaN.  Only tiles that some row sees in part can hold such values; there
@@ -45,7 +48,6 @@ constexpr int kThreads = 768;
 constexpr int kStreamThreads = 256;    // two warpgroups of softmax per stream
 // Named barriers: 1-8 the two warps that share 32 rows, 9 and 10 the warps of a stream
 constexpr int kBarRows = 1, kBarStream = 9;
-constexpr float kRefSlack = 8.f;       // a reference is left behind by at most this (log2)
 constexpr int32_t kNoToken = 0x7fffffff;
 // Registers per thread: 80 at launch, re-divided among the six warpgroups.
 constexpr int kRegLaunch = 80, kRegSoft = 88, kRegAux = 72, kRegFix = 56;
@@ -65,6 +67,9 @@ struct Cfg {
     static constexpr int NST = KV8_ ? 3 : (D_ == 128 ? 4 : 8);
     static constexpr int N8 = KV8_ ? 3 : 0;                  // fp8 tiles on their way
     static constexpr uint32_t COL_S = 0, COL_O = 2 * kPfTok; // tensor-memory columns
+    // log2 of the weight of the score that sets a reference, and of the largest weight that
+    // leaves it in place
+    static constexpr float kLift = BF16_ ? 0.f : 7.f, kTop = kLift + 8.f;
     static_assert(!KV8_ || (D_ == 128 && !BF16_), "fp8 tiles are widened to fp16");
 };
 
@@ -993,8 +998,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sm.red[si][half][row] = m;
                     failed = consumers_any(!ok, 64, row_bar);
                     m = fmaxf(m, sm.red[si][half ^ 1][row]);
-                    const bool move = m > kRefSlack || (ref == -INFINITY && m > -INFINITY);
-                    const float next = move ? (ref == -INFINITY ? m : m + ref) : ref;
+                    const bool move = m > C::kTop || (ref == -INFINITY && m > -INFINITY);
+                    const float next = move ? (ref == -INFINITY ? m : m + ref) - C::kLift : ref;
                     const float a = move ? fast_exp2(ref - next) : 1.f;
                     sum *= a;
                     ref = next;
@@ -1060,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tile_sum = a + b;
                     if (again) break;
                     const float m = fmaxf(mx[0], mx[1]);
-                    const bool move = m > kRefSlack || (ref == -INFINITY && m > -INFINITY);
+                    const bool move = m > C::kTop || (ref == -INFINITY && m > -INFINITY);
                     if (!consumers_any(!ok || move, 64, row_bar)) break;
                     settle(m);   // rare
                     if (failed) break;

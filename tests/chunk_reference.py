@@ -27,8 +27,8 @@ def prefill(q, kc, vc, tables, lens, starts, scale, k_scale=1.0, v_scale=1.0):
     Tolerance of a row, with W = sum_t w_t |v_t| and u the half step of the 16-bit type that
     holds the weights:
       u W                  the weights are rounded once;
-      2^-25 sum_t |v_t|    ... and below fp16's normal range by up to 2^-25 each, while the
-                           weights are relative to one of at least 1 (bf16 has fp32's range);
+      2^-32 sum_t |v_t|    ... and below fp16's normal range by up to 2^-25 each, while the
+                           weights are relative to one of at least 2^7 (bf16 has fp32's range);
       u_out |out|          the output is rounded once;
       W (2 D 2^-24 A + 2^-20 + (L / 16) 2^-23)
                            scores: D products summed in fp32, each step of the sum off by at
@@ -69,7 +69,7 @@ def prefill(q, kc, vc, tables, lens, starts, scale, k_scale=1.0, v_scale=1.0):
             t = half_step(pdt) * W + half_step(q.dtype) * o.abs()
             t += W * (2 * D * FP32 * A.t()[..., None] + 2.0 ** -20 + L / 16 * 2 * FP32)
             if pdt == torch.float16:
-                t += 2.0 ** -25 * torch.einsum("nt,thd->nhd", (~hide).double(), vv.abs())
+                t += 2.0 ** -32 * torch.einsum("nt,thd->nhd", (~hide).double(), vv.abs())
             tol[a + j0:a + j1] = t
     return out, tol
 

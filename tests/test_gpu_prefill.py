@@ -1,5 +1,7 @@
 """GPU: attention of ragged chunks of new tokens over the paged cache (pa_prefill,
 pa_prefill_fp8) against the plain 64-bit form, within the tolerance derived there."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -170,6 +172,30 @@ def test_references_move(cuda_device, Hq, Hkv, D, bs, dtype, fp8, spread):
             f = 0.1 + 2.0 * t * bs / L
             if not fp8:
                 b["kc"][i] = (b["kc"][i].float() * f).to(dtype)
+    run(b)
+
+
+@pytest.mark.parametrize("D,dtype,fp8", [(128, torch.float16, False), (64, torch.float16, False),
+                                         (128, torch.bfloat16, False), (128, torch.bfloat16, True)])
+@pytest.mark.parametrize("C,L", [(1, 8192), (130, 3000)])
+def test_a_long_tail_behind_one_large_weight(cuda_device, D, dtype, fp8, C, L):
+    """Token 0 has nearly all the weight and a value of 0; the others, 2^-23.5 each, a value
+    near 1.  Relative to the largest weight they lie below fp16's smallest step, 2^-24, by a
+    rounding of a third."""
+    b = make([(C, L)], 4, 1, D, 16, dtype, 29, fp8)
+    ids = b["tables"][0, :-(-L // 16)].long()
+    b["q"].zero_()
+    b["q"][..., 0] = 16.0
+    key = 23.5 * math.log(2.0) / b["scale"] / 16.0
+    if fp8:
+        b["kc"][ids] = 0
+        b["vc"][ids] = torch.tensor(1.0 / b["vs"], device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+        b["kc"][ids[0], 0, 0, 0] = torch.tensor(key / b["ks"], device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        b["kc"][ids] = 0
+        b["vc"][ids] = 1.0
+        b["kc"][ids[0], 0, 0, 0] = key
+    b["vc"][ids[0], 0, 0] = 0
     run(b)
 
 
