@@ -341,7 +341,8 @@ constexpr int kMoveTableCtas = 8;
 // Copies block `from` to block `to` in both pools of every layer, and rewrites the block
 // tables' entries.  CTA (i, y): pair i of pool y (2 * layer, + 1 for V), or, past the
 // pairs and for y = 0, a share of the table entries: each entry looks itself up among the
-// pairs, which ascend by `from`.
+// pairs, which ascend by `from`.  Bound by HBM: 201 blocks of 32 KB in both pools of 32 layers
+// (843 MB read and written) take 123.5 us, 6.83 TB/s; every CTA has 32 KB on their way.
 __global__ void __launch_bounds__(kMoveThreads) move_blocks_kernel(const __grid_constant__ MoveParams p) {
     const int32_t i = blockIdx.x;
     if (i >= p.num_pairs) {
