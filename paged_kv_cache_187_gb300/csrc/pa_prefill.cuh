@@ -15,8 +15,9 @@
 //     O += P V    M = 128 rows, N = head dims, P read from tensor memory, V MN-major
 // The MMA thread issues PV of one stream and its next QK^T back to back, stream by stream,
 // so the tensor pipe works on one stream while the other's softmax runs.  A row's
-// reference moves (and O is rescaled in tensor memory) only when its largest score passes
-// the one that set it by 2^8; the weights' sum is held in fp32.
+// reference moves (and O is rescaled in tensor memory) only when 64 of its weights add up to
+// 2^8 times the weight of the score that set it: this is seen on the sum, which is needed
+// anyway, held in fp32, and takes no maximum.
 //
 // Weights enter PV as one 16-bit term: rounding them costs at most half a step of the
 // 16-bit type relative to each weight (2^-8 bf16, 2^-11 fp16), as much as rounding the
@@ -41,11 +42,12 @@
 // tokens of 32 query and 8 kv heads of 128, bf16, take 353 us (1,560 TFLOP/s) and, back to back
 // at the power cap, 376.  Both streams in step with their softmax cost 422, one thread per row
 // 434.  Few new tokens behind long contexts (4 x 24 tokens, 64 heads, 50-62 K): 200 us, 4.5 TB/s,
-// at the power cap too; single tokens: 6.2 TB/s of K/V.  Head size 64: the chain of a stream,
-// scores to weights to next scores, about 2,500 cycles for a pair with 1,024 of products and
-// as many of exponentials: 50 us for nine prompts of 40-1500 tokens with 16 heads.  fp8 caches: the widening, 1,300
-// cycles a tile for its four warps, and the lead that three stages leave (370 us where fp16
-// products alone take 211).
+// at the power cap too; single tokens: 6.2 TB/s of K/V.  Head size 64: the softmax
+// warps' work, about 2,500 cycles for a pair with 1,024 of products and as many of
+// exponentials (a third score buffer, so that no warp waits for scores, changed nothing: 303
+// against 300 us; without the maxima of each tile 289): 48 us for nine prompts of 40-1500
+// tokens with 16 heads.  fp8 caches: the widening, 1,300 cycles a tile for its four warps, and
+// the lead that three stages leave (367 us where fp16 products alone take 211).
 #pragma once
 
 #include "pa_chunk_device.cuh"
@@ -78,9 +80,9 @@ struct Cfg {
     static constexpr int NST = KV8_ ? 3 : (D_ == 128 ? 4 : 8);
     static constexpr int N8 = KV8_ ? 3 : 0;                  // fp8 tiles on their way
     static constexpr uint32_t COL_S = 0, COL_O = 2 * kPfTok; // tensor-memory columns
-    // log2 of the weight of the score that sets a reference, and of the largest weight that
-    // leaves it in place
-    static constexpr float kLift = BF16_ ? 0.f : 7.f, kTop = kLift + 8.f;
+    // log2 of the weight of the score that sets a reference, and the sum of 64 weights that
+    // moves it (2^8 of those): no weight is larger
+    static constexpr float kLift = BF16_ ? 0.f : 7.f, kMost = BF16_ ? 256.f : 32768.f;
     static_assert(!KV8_ || (D_ == 128 && !BF16_), "fp8 tiles are widened to fp16");
 };
 
@@ -180,11 +182,6 @@ __device__ __forceinline__ uint64_t fma_x2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add_x2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -1004,18 +1001,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 32; ++c) x[c] = 32 * h + c < seen ? x[c] : hidden;
                     }
                 };
-                // Moves the references that a score passes by too much (m: this thread's
-                // largest exponent), in both threads of a row, and rescales O.
-                auto settle = [&](float m) {
+                // The rows' largest scores become their references, in both threads of a row,
+                // and O is rescaled.
+                auto raise = [&]() {
+                    float m = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < kCols / 32; ++h) {
+                        float x[32];
+                        tmem_ld32(ts + 32 * h, x);
+                        scores(h, x);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) m = fmaxf(m, x[c] * p.scale_log2);
+                    }
                     sm.red[si][half][row] = m;
                     failed = consumers_any(!ok, 64, row_bar);
-                    m = fmaxf(m, sm.red[si][half ^ 1][row]);
-                    const bool move = m > C::kTop || (ref == -INFINITY && m > -INFINITY);
-                    const float next = move ? (ref == -INFINITY ? m : m + ref) - C::kLift : ref;
-                    const float a = move ? fast_exp2(ref - next) : 1.f;
+                    m = fmaxf(m, sm.red[si][half ^ 1][row]) - C::kLift;
+                    const float next = fmaxf(ref, m);
+                    const float a = ref == next ? 1.f : fast_exp2(ref - next);
                     sum *= a;
                     ref = next;
-                    if (j > 0 && __any_sync(0xffffffffu, move) && !failed) {
+                    if (j > 0 && __any_sync(0xffffffffu, a != 1.f) && !failed) {
                         // (the wait for S has also seen the previous tile's PV complete)
 #pragma unroll 1
                         for (int h = 0; h < kDims / 32; ++h) {
@@ -1029,29 +1034,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 if (j == 0) {
-                    // an item's first tile: the references are the rows' largest scores
-                    float m = -INFINITY;
-#pragma unroll 1
-                    for (int h = 0; h < kCols / 32; ++h) {
-                        float x[32];
-                        tmem_ld32(ts + 32 * h, x);
-                        scores(h, x);
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) m = fmaxf(m, x[c] * p.scale_log2);
-                    }
-                    settle(m);
+                    raise();
                     if (failed) break;
                 }
-                // Weights against the present reference, and their largest exponent, in one
-                // go; should a row's reference have to move, they are thrown away and taken
-                // once more (the scores stay in tensor memory until P overwrites them).
+                // Weights against the present reference and their sum, in one go.  A weight
+                // that is too large makes the sum too large: then the references are raised
+                // and the weights taken once more (the scores stay in tensor memory until P
+                // overwrites them).
                 uint32_t w[kCols / 2];
                 float tile_sum;
 #pragma unroll 1
                 for (bool again = j == 0;; again = true) {
                     const float nref = ref == -INFINITY ? 0.f : -ref;
                     const uint64_t nref2 = pack_f32(nref, nref);
-                    float mx[2] = {-INFINITY, -INFINITY};
                     uint64_t s2[2] = {0ull, 0ull};
                     // (the second half's scores are on their way while the first's weights
                     // are taken)
@@ -1065,7 +1060,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 16; ++c) {
                             float a, b;
                             unpack_f32(fma_x2(pack_f32(x[h][2 * c], x[h][2 * c + 1]), scale2, nref2), a, b);
-                            mx[c & 1] = max3(mx[c & 1], a, b);
                             a = fast_exp2(a);
                             b = fast_exp2(b);
                             s2[c & 1] = add_x2(s2[c & 1], pack_f32(a, b));
@@ -1076,10 +1070,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unpack_f32(add_x2(s2[0], s2[1]), a, b);
                     tile_sum = a + b;
                     if (again) break;
-                    const float m = fmaxf(mx[0], mx[1]);
-                    const bool move = m > C::kTop || (ref == -INFINITY && m > -INFINITY);
-                    if (!consumers_any(!ok || move, 64, row_bar)) break;
-                    settle(m);   // rare
+                    const bool over = tile_sum > C::kMost || (ref == -INFINITY && seen > 0);
+                    if (!consumers_any(!ok || over, 64, row_bar)) break;
+                    raise();   // rare
                     if (failed) break;
                 }
                 if (failed) break;
