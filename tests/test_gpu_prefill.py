@@ -146,6 +146,46 @@ def test_work_cut_into_shares(cuda_device, seqs, Hq, Hkv, D, bs, dtype, fp8):
     run(make(seqs, Hq, Hkv, D, bs, dtype, 23 + Hq, fp8))
 
 
+@pytest.mark.parametrize("seqs,fp8", [
+    # more sequences, and more row tiles, than the plan holds in shared memory: whole units ..
+    ([(1 + (i * 37) % 90, 1 + (i * 37) % 90 + (i * 13) % 50) for i in range(900)], False),
+    ([(1 + i % 3, 40 + i % 90) for i in range(600)], True),
+    # .. and shares, cut through one long context among 2100 short ones
+    ([(1, 1 + i % 9) for i in range(1500)] + [(2, 60000)] + [(1, 3)] * 600, False),
+])
+def test_batches_past_the_plans_tables(cuda_device, seqs, fp8):
+    D = 128 if fp8 else 64
+    run(make(seqs, 16, 1, D, 16, torch.float16, 61, fp8))
+
+
+def test_two_threads_at_once(cuda_device):
+    """Calls from two host threads, each on its own stream with its own workspace, give the
+    bits that they give alone."""
+    import threading
+    jobs = [make([(90, 1000), (1, 1700)], 8, 2, 128, 16, torch.bfloat16, 67),
+            make([(3, 4000), (200, 300)], 8, 2, 128, 16, torch.bfloat16, 71)]
+    alone = [run(b) for b in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(b, want):
+        st = torch.cuda.Stream()
+        mcl = max(b["lens"])
+        with torch.cuda.stream(st):
+            ws, status = workspace(b, mcl), torch.zeros(1, dtype=torch.int32, device="cuda")
+            for _ in range(20):
+                out = call(b, torch.zeros_like(b["q"]), ws=ws, mcl=mcl, status=status)
+                if not torch.equal(out, want) or int(status):
+                    wrong.append(1)
+
+    threads = [threading.Thread(target=work, args=j) for j in zip(jobs, alone)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_chunks_longer_than_the_context_and_empty_contexts(cuda_device):
     """Rows with nothing to attend to are zero rows: chunks whose first tokens lie before the
     context's start (clamped metadata), and empty contexts."""
