@@ -1001,9 +1001,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 32; ++c) x[c] = 32 * h + c < seen ? x[c] : hidden;
                     }
                 };
-                // The rows' largest scores become their references, in both threads of a row,
-                // and O is rescaled.
-                auto raise = [&]() {
+                // The largest scores of the rows that have to move (`over`, in either thread)
+                // become their references, and O is rescaled.  Other rows of the two warps go
+                // through this unchanged: a row's bits do not depend on its neighbours, some of
+                // which hold no query.
+                auto raise = [&](bool over) {
                     float m = -INFINITY;
 #pragma unroll 1
                     for (int h = 0; h < kCols / 32; ++h) {
@@ -1013,9 +1015,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 32; ++c) m = fmaxf(m, x[c] * p.scale_log2);
                     }
-                    sm.red[si][half][row] = m;
+                    sm.red[si][half][row] = over ? m : -INFINITY;
                     failed = consumers_any(!ok, 64, row_bar);
-                    m = fmaxf(m, sm.red[si][half ^ 1][row]) - C::kLift;
+                    m = fmaxf(sm.red[si][half][row], sm.red[si][half ^ 1][row]) - C::kLift;
                     const float next = fmaxf(ref, m);
                     const float a = ref == next ? 1.f : fast_exp2(ref - next);
                     sum *= a;
@@ -1034,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 if (j == 0) {
-                    raise();
+                    raise(true);
                     if (failed) break;
                 }
                 // Weights against the present reference and their sum, in one go.  A weight
@@ -1072,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (again) break;
                     const bool over = tile_sum > C::kMost || (ref == -INFINITY && seen > 0);
                     if (!consumers_any(!ok || over, 64, row_bar)) break;
-                    raise();   // rare
+                    raise(over);   // rare
                     if (failed) break;
                 }
                 if (failed) break;

@@ -390,6 +390,21 @@ def test_the_same_call_gives_the_same_bits(cuda_device):
             assert torch.equal(first, call(b, torch.zeros_like(b["q"])))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,fp8", [(6, 2, 64, torch.bfloat16, False), (6, 2, 128, torch.bfloat16, True),
+                                               (7, 1, 128, torch.float16, False)])
+def test_bits_do_not_depend_on_rows_without_a_query(cuda_device, Hq, Hkv, D, dtype, fp8):
+    """Groups of 3 and 7 leave rows of a stream's 128 unused, and short chunks leave more: what
+    an earlier call left there changes nothing."""
+    b = make([(40, 300), (1, 2500), (5, 64), (18, 900)], Hq, Hkv, D, 16, dtype, 79, fp8)
+    loud = make([(200, 400), (60, 2000)], Hq, Hkv, D, 16, dtype, 83, fp8)
+    loud["q"] *= 50.0
+    quiet = dict(loud, q=loud["q"] * 1e-4)
+    want = run(b)
+    for other in (loud, quiet, b, loud):
+        call(other, torch.empty_like(other["q"]))
+        assert torch.equal(call(b, torch.zeros_like(b["q"])), want)
+
+
 def test_single_tokens_agree_with_the_decode(cuda_device):
     """One new token per sequence is an ordinary decode: both within tolerance of the formula."""
     import paged_kv_cache_187_gb300 as pa
