@@ -158,6 +158,22 @@ def test_batches_past_the_plans_tables(cuda_device, seqs, fp8):
     run(make(seqs, 16, 1, D, 16, torch.float16, 61, fp8))
 
 
+@pytest.mark.parametrize("D,dtype,fp8", [(64, torch.float16, False), (128, torch.bfloat16, False),
+                                         (128, torch.bfloat16, True)])
+def test_output_at_any_16_bytes(cuda_device, D, dtype, fp8):
+    """Rows are stored 32 bytes at a time where the output's address allows it, else 16."""
+    b = make([(40, 300), (1, 2500), (5, 64)], 6, 2, D, 16, dtype, 73, fp8)
+    want = run(b)
+    flat = torch.full((b["q"].numel() + 32,), 7.0, dtype=dtype, device="cuda")
+    for skip in (8, 16, 24):
+        flat.fill_(7.0)
+        out = flat[skip:skip + b["q"].numel()].view(b["q"].shape)
+        call(b, out)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert bool((flat[:skip] == 7.0).all()) and bool((flat[skip + out.numel():] == 7.0).all())
+
+
 def test_two_threads_at_once(cuda_device):
     """Calls from two host threads, each on its own stream with its own workspace, give the
     bits that they give alone."""
