@@ -450,7 +450,10 @@ pa_status pa_rope_and_cache_fp8(void* query_out, const void* query, const void* 
  * them.  New token j sits at position L - C + j and attends to the tokens before and at it:
  *   out[query_starts[s] + j][h] = sum_t softmax_t(scale * q . k_t) v_t, t < L - C + j + 1;
  * a row with nothing to attend to (L < C - j) is a zero row.  A token's row does not depend
- * on what the pools hold past its own position, infinities and NaN included.
+ * on what the pools hold past its own position, infinities and NaN included.  No weight is 0,
+ * however small: an infinite element of a V row that a token sees makes that element of its
+ * output infinite, two of both signs, or a NaN, make it NaN (contexts up to 2^22 tokens; past
+ * that an infinity behind a weight that vanishes in fp32 or the cache's type is NaN).
  *   query, out    [num_tokens][num_q_heads][head_size], fp16 or bf16 (also the pools' type)
  *   query_starts  int32 [num_seqs + 1], ascending, within 0 .. num_tokens; rows outside
  *                 query_starts[0] .. query_starts[num_seqs] are left as they are

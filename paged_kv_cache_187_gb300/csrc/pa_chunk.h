@@ -47,6 +47,7 @@ struct PfHeader {
 
 struct PrefillParams {
     void* out;
+    const void* value_cache;
     const int32_t* block_tables;
     const int32_t* context_lens;
     const int32_t* query_starts;

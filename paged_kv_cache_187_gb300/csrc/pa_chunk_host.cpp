@@ -144,6 +144,7 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
     pa::PrefillParams p;
     std::memset(&p, 0, sizeof(p));
     p.out = a.out;
+    p.value_cache = a.value_cache;
     p.block_tables = a.block_tables;
     p.context_lens = a.context_lens;
     p.query_starts = a.query_starts;

@@ -32,6 +32,13 @@
 // and note for each head dim the first token with +inf, -inf and NaN; the rows that do see
 // that token get the value added at the end.
 //
+// Elsewhere an infinite value goes through the product, or through the join of partitions,
+// with a weight that may have vanished in its type: 0 times infinity is NaN, where the weight
+// of the formula is never 0.  An output element that is NaN while its row's weights are not is
+// therefore settled from V itself, by a second look at the rows that the token sees; outputs
+// are only checked for that otherwise (nine prompts of head size 64: 51.0 us, 49.6 without the
+// check and what it leads to; other cases within 0.3 %).
+//
 // Warps: 0-7 and 8-15 softmax and epilogue of streams 0 and 1, two threads per row; 16
 // producer (claims items, TMA of Q and K); 17 MMA issuer; 18 TMA of V; 19 waits for tiles;
 // 20-23 fix V tiles (16-bit caches), or widen the fp8 K/V tiles to fp16 and fix them.  Every
@@ -62,6 +69,9 @@ constexpr int kStreamThreads = 256;    // two warpgroups of softmax per stream
 // Named barriers: 1-8 the two warps that share 32 rows, 9 and 10 the warps of a stream
 constexpr int kBarRows = 1, kBarStream = 9;
 constexpr int32_t kNoToken = 0x7fffffff;
+// Longest context that is looked at again for infinite values: a warp takes a microsecond or
+// two for 32 tokens and 16 head dims, so about 1 s for its 64 dims; waits run out after 2 s.
+constexpr int32_t kSettleTokens = 1 << 22;
 // Registers per thread: 80 at launch, re-divided among the six warpgroups.
 constexpr int kRegLaunch = 80, kRegSoft = 88, kRegAux = 72, kRegFix = 56;
 static_assert(4 * kRegSoft + kRegAux + kRegFix <= 6 * kRegLaunch, "register split");
@@ -120,7 +130,7 @@ struct alignas(1024) Smem {
     // first token with +inf / -inf / NaN of each head dim among an item's fixed tiles
     int32_t nonfinite[2][3][C::D];
     int32_t any_nonfinite[2];
-    int32_t last_part[2];
+    int32_t last_part[2], last_seq[2];
     uint32_t tmem_base;
     volatile int32_t abort;
 };
@@ -273,6 +283,29 @@ __device__ __forceinline__ uint32_t taint(uint32_t acc, uint32_t x) {
     else
         asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
     return r;
+}
+
+// Which of the 16 values at `at` (16-byte aligned) are infinite or NaN: bit c of `inf` is
+// +inf, bit 16 + c -inf, bit c of `nan` NaN.
+template <bool kBf16>
+__device__ __forceinline__ void odd_values(const uint16_t* at, uint32_t& inf, uint32_t& nan) {
+    constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
+    uint32_t acc = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(at)[i];
+        acc = taint<kBf16>(acc, x.x);
+        acc = taint<kBf16>(acc, x.y);
+        acc = taint<kBf16>(acc, x.z);
+        acc = taint<kBf16>(acc, x.w);
+    }
+    if ((acc & kExp) != kExp && ((acc >> 16) & kExp) != kExp) return;
+#pragma unroll 1
+    for (int c = 0; c < 16; ++c) {
+        const uint32_t v = at[c];
+        if ((v & 0x7FFFu) == kExp) inf |= 1u << (c + ((v >> 15) ? 16 : 0));
+        else if ((v & kExp) == kExp) nan |= 1u << c;
+    }
 }
 
 template <class C>
@@ -1184,13 +1217,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < 16; ++c) o[c] = 0.f;
                 }
             };
-            auto store_row = [&](int d, const float (&o)[16], float f) {
-                const size_t orow =
-                    ((size_t)(u.q_start + tok) * p.num_q_heads + (size_t)u.kvh * G + row % G) * D;
-                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow + d);
+            // 16 outputs from head dim d on, packed, of rows among which some are infinite or NaN:
+            // where one is NaN in a row whose sum of weights is not, the V rows that the row sees
+            // say whether it is +inf or -inf.
+            auto settle = [&](int d, uint32_t (&y)[8], int32_t seq, bool has_sum) {
+                constexpr uint32_t kExp = C::kQBf16 ? 0x7F80u : 0x7C00u;
+                uint32_t odd = 0, inf = 0, nan = 0;
+                if (has_sum && mine && limit <= kSettleTokens) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        odd |= (y[k] & 0x7FFFu) > kExp ? 1u << (2 * k) : 0u;
+                        odd |= ((y[k] >> 16) & 0x7FFFu) > kExp ? 2u << (2 * k) : 0u;
+                    }
+                }
+                const uint32_t any = __reduce_or_sync(0xffffffffu, odd);
+                if (any == 0) return;
+                auto look = [&](int32_t t) {
+                    const int32_t block = p.block_tables[(size_t)seq * p.max_blocks_per_seq + t / C::BS];
+                    if (block < 0 || block >= p.num_blocks) return;
+                    const int64_t vrow = ((int64_t)block * Hkv + u.kvh) * C::BS + t % C::BS;
+                    odd_values<C::kBf16>(static_cast<const uint16_t*>(p.value_cache) + vrow * D + d, inf, nan);
+                };
+                // the tokens that all these rows see, the warp together, then each row's own
+                const int32_t all = __reduce_min_sync(0xffffffffu, odd ? limit : kNoToken);
+#pragma unroll 1
+                for (int32_t t = 0; t < all; t += 32) {
+                    if (t + lane < all) look(t + lane);
+                    if ((__reduce_or_sync(0xffffffffu, nan) & any) == any) break;
+                }
+                inf = __reduce_or_sync(0xffffffffu, inf);
+                nan = __reduce_or_sync(0xffffffffu, nan);
+#pragma unroll 1
+                for (int32_t t = all; odd && t < limit; ++t) look(t);
+                __syncwarp();
+                odd &= ~nan & (inf ^ (inf >> 16));
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    if ((odd >> c) & 1u) {
+                        const uint32_t v = kExp | ((inf >> c) & 1u ? 0u : 0x8000u);
+                        y[c / 2] = c & 1 ? (y[c / 2] & 0xFFFFu) | (v << 16) : (y[c / 2] & 0xFFFF0000u) | v;
+                    }
+            };
+            auto store_row = [&](int d, const float (&o)[16], float f, int32_t seq) {
                 uint32_t y[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) y[k] = pack2<C::kQBf16>(o[2 * k] * f, o[2 * k + 1] * f);
+                if constexpr (!C::kKv8) {      // (e4m3 has no infinity: NaN it is)
+                    uint32_t z0 = 0, z1 = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        z0 = taint<C::kQBf16>(z0, y[k]);
+                        z1 = taint<C::kQBf16>(z1, y[k + 4]);
+                    }
+                    if (__any_sync(0xffffffffu, mine && (z0 | z1) != 0)) settle(d, y, seq, f == f);
+                }
+                if (!mine) return;
+                const size_t orow =
+                    ((size_t)(u.q_start + tok) * p.num_q_heads + (size_t)u.kvh * G + row % G) * D;
+                uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow + d);
                 // (a warp's lanes write to as many rows, and what counts is the number of stores:
                 // 16 bytes at a time, a prompt of 8192 tokens took 353 us instead of 345)
                 if (wide) {
@@ -1221,7 +1305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < dims / 16; ++h) {
                     float o[16];
                     load_o(h, o);
-                    if (mine) store_row(dim0 + 16 * h, o, f);
+                    store_row(dim0 + 16 * h, o, f, un.seq);
                 }
                 release();
             } else {
@@ -1255,6 +1339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (row == 0 && half == 0) {
                         const int32_t worth = u.single && !both ? 2 : 1;
                         const int32_t full = u.single ? 2 * u.nparts : u.nparts;
+                        sm.last_seq[si] = u.seq;
                         sm.last_part[si] = atomicAdd(&p.arrive[2 * u.first + sj], worth) == full - worth;
                     }
                     named_bar_sync(bar, kStreamThreads);
@@ -1297,7 +1382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     for (int c = 0; c < 16; ++c) o[c] = fmaf(weight, v[t][c], o[c]);
                                 }
                             }
-                            if (mine) store_row(d, o, f);
+                            store_row(d, o, f, sm.last_seq[si]);
                         }
                     }
                 }
