@@ -499,7 +499,8 @@ pa_status pa_prefill_fp8(void* out, const void* query, const void* key_cache,
  * [num_rows][max_blocks_per_seq], NULL: none) may hold -1 padding.  A pair outside the pool
  * is skipped, and it or a pair out of order is flagged PA_DEVERR_BAD_BLOCK (out of order,
  * the tables' entries are unspecified; the copies are not).  A block that is a source and a
- * destination, or two destinations, race.  One launch per 64 layers. */
+ * destination, or two destinations, race.  num_layers may be 0: the tables alone.  One launch
+ * per 64 layers. */
 pa_status pa_move_blocks(void* const* key_caches, void* const* value_caches, int32_t num_layers,
                          const int32_t* block_pairs, int32_t num_pairs, int32_t* block_tables,
                          int32_t num_rows, int32_t max_blocks_per_seq, int32_t num_kv_heads,
