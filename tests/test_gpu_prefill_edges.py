@@ -1,9 +1,11 @@
 """GPU: attention of ragged chunks (pa_prefill, pa_prefill_fp8) where its parts meet: values that
-are infinite or NaN behind vanishing weights, on every way the work can be shared out."""
+are infinite or NaN behind vanishing weights, bad metadata and rows with nothing to attend to, on
+every way the work can be shared out."""
 import pytest
 import torch
 
-from test_gpu_prefill import call, make, reference
+import chunk_reference as R
+from test_gpu_prefill import call, check, make, reference, run
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +60,130 @@ def test_infinite_values_behind_vanishing_weights(cuda_device, seqs, Hq, Hkv, mc
     assert int(status) == 0
     want = check_classes(b, out)
     assert bool(torch.isinf(want).any()) and bool(torch.isnan(want).any())
+
+
+GUARD = 1 << 16
+
+
+def guarded(b, mcl):
+    """A workspace of exactly the size asked for, with a guard behind it."""
+    import paged_kv_cache_187_gb300 as pa
+    T, Hq, D = b["q"].shape
+    n = pa.pa_prefill_workspace_size(T, len(b["lens"]), Hq, b["kc"].shape[1], D, mcl)
+    whole = torch.full((n + GUARD,), 0x5A, dtype=torch.uint8, device="cuda")
+    assert whole.data_ptr() % 256 == 0
+    return whole[:n], whole[n:]
+
+
+def shared_out(ws):
+    """How the last call on a workspace was shared out: its plan's third word, unless it had none."""
+    cut = int(ws[8:12].view(torch.int32))
+    return {0: "whole", 1: "cut"}.get(cut, "no plan")
+
+
+def flags_of(b, mcl, how, **change):
+    """The status of a call with some of its metadata replaced; it writes nothing past its
+    workspace and its output."""
+    b = dict(b, **change)
+    ws, guard = guarded(b, mcl)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    room = torch.full((b["q"].numel() + 4096,), 7.0, dtype=b["q"].dtype, device="cuda")
+    call(b, room[:b["q"].numel()].view(b["q"].shape), ws=ws, mcl=mcl, status=status)
+    torch.cuda.synchronize()
+    assert bool((guard == 0x5A).all()) and bool((room[b["q"].numel():] == 7.0).all())
+    assert shared_out(ws) == how
+    return int(status)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# contexts up to 1024 tokens and a unit per CTA: no plan; a longer limit: the plan kernel
+@pytest.mark.parametrize("mcl,how", [(200, "no plan"), (4096, "whole")])
+@pytest.mark.parametrize("D,dtype,fp8", [(128, torch.bfloat16, False), (64, torch.float16, False),
+                                         (128, torch.bfloat16, True)])
+def test_bad_metadata_with_and_without_a_plan(cuda_device, mcl, how, D, dtype, fp8):
+    import paged_kv_cache_187_gb300 as pa
+    b = make([(30, 200), (20, 100)], 4, 2, D, 16, dtype, 37, fp8)
+    assert flags_of(b, mcl, how) == 0
+    for starts in ([0, 40, 30], [-5, 30, 50], [0, 30, 2 ** 31 - 1], [50, 0, 50], [-2 ** 31, -7, -1]):
+        assert flags_of(b, mcl, how, starts_d=i32(starts)) == pa.PA_DEVERR_BAD_LEN, starts
+    for lens in ([300, 100], [-1, 100], [-2 ** 31, 100]):
+        assert flags_of(b, mcl, how, lens_d=i32(lens)) == pa.PA_DEVERR_BAD_LEN, lens
+    # the second row of the tables is padding past its 100 tokens, and the clamped length reaches it
+    assert flags_of(b, mcl, how, lens_d=i32([200, 2 ** 31 - 1])) == pa.PA_DEVERR_BAD_LEN | pa.PA_DEVERR_BAD_BLOCK
+    bad = b["tables"].clone()
+    bad[0, 3], bad[1, 0] = b["kc"].shape[0], -7
+    assert flags_of(b, mcl, how, tables=bad) == pa.PA_DEVERR_BAD_BLOCK
+    check(b, call(b, torch.zeros_like(b["q"]), mcl=mcl))              # and all is well
+
+
+@pytest.mark.parametrize("L,mcl,how", [(20, 20, "no plan"), (20, 4096, "whole"), (5000, 5000, "cut")])
+@pytest.mark.parametrize("starts", [[0, 240] * 6 + [0], [0] + [240, 0] * 6, [0, 240] + [0] * 11])
+def test_overlapping_chunks_stay_within_the_workspace(cuda_device, L, mcl, how, starts):
+    """Chunks that overlap ask for more row tiles than the workspace has room for: flagged, and
+    neither the workspace nor the output is written past its end."""
+    import paged_kv_cache_187_gb300 as pa
+    b = make([(20, L)] * 12, 16, 1, 128, 16, torch.bfloat16, 38)
+    assert flags_of(b, mcl, how, starts_d=i32(starts)) == pa.PA_DEVERR_BAD_LEN
+    check(b, call(b, torch.zeros_like(b["q"]), mcl=mcl))
+
+
+# chunks whose first tokens lie before the context's start, and empty contexts: row tiles without
+# a single tile of tokens, next to others
+@pytest.mark.parametrize("seqs,mcl,how", [
+    ([(10, 4), (3, 0), (140, 130), (1, 0), (300, 1)], 300, "no plan"),
+    ([(10, 4), (3, 0), (140, 130), (1, 0), (300, 1)], 4096, "whole"),
+    ([(300, 1), (1, 30000), (500, 100), (2, 0), (40, 40)], 30000, "cut"),   # such units first,
+    ([(1, 30000), (600, 30), (5, 0)], 30000, "cut"),                        # .. and last
+    ([(400, 0), (200, 190), (7, 9000), (0, 50), (90, 3)], 9000, "cut"),
+    ([(400, 0), (3, 0)], 4096, "whole"),                                    # nothing else
+])
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,fp8", [(8, 1, 128, torch.bfloat16, False), (8, 2, 64, torch.float16, False),
+                                                (8, 2, 128, torch.float16, True)])
+def test_row_tiles_without_tokens(cuda_device, seqs, mcl, how, Hq, Hkv, D, dtype, fp8):
+    b = make(seqs, Hq, Hkv, D, 16, dtype, 3, fp8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws, guard = guarded(b, mcl)
+    out = call(b, torch.full_like(b["q"], 7.0), ws=ws, mcl=mcl, status=status)
+    assert int(status) == 0 and bool((guard == 0x5A).all()) and shared_out(ws) == how
+    check(b, out)
+    for s, (n, L) in enumerate(seqs):
+        a = int(b["starts"][s])
+        assert not out[a:a + max(n - L, 0)].any()
+
+
+@pytest.mark.parametrize("mcl", [10, 4096])
+def test_calls_without_a_row_of_query(cuda_device, mcl):
+    b = make([(0, 10), (0, 0)], 4, 2, 128, 16, torch.float16, 61, extra=4)
+    ws, guard = guarded(b, mcl)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = call(b, torch.full_like(b["q"], 3.0), ws=ws, mcl=mcl, status=status)
+    assert int(status) == 0 and bool((out == 3).all()) and bool((guard == 0x5A).all())
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv", [([(33, 1400), (1, 3000), (200, 900), (5, 256)], 8, 1),
+                                         ([(2, 9001), (40, 2600)], 4, 2)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_references_move_over_8_bit_caches(cuda_device, seqs, Hq, Hkv, dtype):
+    """Keys that grow along the context under large queries: most rows find their largest score
+    late, and the accumulators are rescaled there, several times in a row."""
+    b = make(seqs, Hq, Hkv, 128, 32, dtype, 17, True, spread=3.0)
+    b["q"] *= 8.0
+    moved = rows = 0
+    for s, (n, L) in enumerate(seqs):
+        for t, i in enumerate(b["tables"][s, :-(-L // 32)].tolist()):
+            k = b["kc"][i].view(torch.float8_e4m3fn).float() * (0.1 + 2.0 * t * 32 / L)
+            b["kc"][i] = k.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        # rows whose largest score in bits lies more than 16 (2^8 and 2^7 of fp16's weights, and
+        # one) above that of their first 128 tokens: their reference moves
+        ids = b["tables"][s, :-(-L // 32)].long()
+        k = R.cache_values(b["kc"][ids], b["ks"]).transpose(1, 2).reshape(-1, Hkv, 128)[:L - n]
+        x = b["q"][int(b["starts"][s]):int(b["starts"][s]) + n].double()
+        y = torch.einsum("nhd,thd->nht", x, k.repeat_interleave(Hq // Hkv, 1)) * b["scale"] / 0.6931471805599453
+        if L - n > 128:
+            moved += int((y.amax(-1) > y[..., :128].amax(-1) + 16).sum())
+            rows += y.shape[0] * y.shape[1]
+    assert moved > rows // 2
+    run(b)
