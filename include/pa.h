@@ -460,7 +460,12 @@ pa_status pa_rope_and_cache_fp8(void* query_out, const void* query, const void* 
  * and the rest as for pa_decode_v2.  num_tokens is at most 2^24, a context at most 2^30
  * tokens (clamped and flagged past that); scale is finite.  Scores and
  * sums are fp32 (scores up to 2^20 in magnitude); the softmax weights enter the product with
- * V rounded to the cache's 16-bit type.  The same call gives the same bits every time.
+ * V rounded to the cache's 16-bit type (pa_decode_* hold them in two such terms over a 16-bit
+ * cache, so a single token's row is a little less exact here); bf16 V values up to 2^96 in
+ * magnitude, so that no sum overflows.  The same call gives the same bits every time.  A call
+ * of single tokens alone is faster as a decode: 256 tokens over contexts of 200-4000 (32 query
+ * and 8 kv heads of 128) take 342 us here and 301 by pa_decode_auto over a bf16 cache, 402 and
+ * 162 (pa_decode_fp8) over an fp8 one.
  * Bad query_starts (descending, outside the rows) or lengths are clamped and flagged
  * PA_DEVERR_BAD_LEN; block-table entries outside the pool read as zero rows and are flagged
  * PA_DEVERR_BAD_BLOCK.

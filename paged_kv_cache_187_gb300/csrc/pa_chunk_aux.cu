@@ -51,12 +51,14 @@ constexpr int kPlanSeqs = 512, kPlanTiles = 2048;
 // out (see PfHeader).  Whole units are claimed longest first, which leaves the shortest for
 // the end.  Where that would still leave the longest CTA over an equal share by more than
 // what joining partial results costs (few or long units), the work is cut into equal shares
-// instead, whatever the units' ends.  Both sides, whole / cut (us a call; 32 query and 8 kv
-// heads of 128, bf16, 16-token blocks): prompts of 2048, 4096 and 8192 tokens 49 / 55, 112 /
-// 152 and 353 / 478; 2 chunks of 400-900 beside 61 single tokens 176 / 213; 16 chunks of 200
-// behind 1 K 80 / 96; 2 of 700 behind 4 K 112 / 89; 1 of 512 behind 16 K 191 / 108; 8 of 64
-// behind 8 K 104 / 79; 64 query heads, 4 chunks of 24 behind 50-62 K 640 / 188.  The rule takes
-// the better side of each.
+// instead, whatever the units' ends.  Both sides, whole / cut (us a call, calls back to back;
+// 32 query and 8 kv heads of 128, bf16, 16-token blocks): prompts of 2048, 4096 and 8192 tokens
+// 48 / 54, 106 / 126 and 360 / 411; chunks of 640 and 760 beside 61 single tokens, all behind
+// 200-4000, 126 / 156; 16 chunks of 200 behind 1 K 76 / 91; 2 of 700 behind 4 K 112 / 88; 1 of
+// 512 behind 16 K 192 / 110; 8 of 64 behind 8 K 104 / 79; 40 of 32 behind 8 K 264 / 230; 64
+// query heads, 4 chunks of 24 behind 50-62 K 665 / 190.  The rule takes the better side of each
+// of these.  It looks at the first four rounds of units only, so a short fifth one goes unseen:
+// 77 chunks of 32 behind 8 K (616 units on 152 CTAs) are taken whole, 448 / 417.
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillParams p) {
     __shared__ int32_t buf[32];
     __shared__ int32_t hist[kBuckets], first[kBuckets];

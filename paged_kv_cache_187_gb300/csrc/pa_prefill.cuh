@@ -36,8 +36,8 @@
 // with a weight that may have vanished in its type: 0 times infinity is NaN, where the weight
 // of the formula is never 0.  An output element that is NaN while its row's weights are not is
 // therefore settled from V itself, by a second look at the rows that the token sees; outputs
-// are only checked for that otherwise (nine prompts of head size 64: 51.0 us, 49.6 without the
-// check and what it leads to; other cases within 0.3 %).
+// are only checked for that otherwise (nine prompts of head size 64: 51.0-51.8 us, 49.4-49.7
+// without the check and what it leads to; other cases within 0.5 %).
 //
 // Warps: 0-7 and 8-15 softmax and epilogue of streams 0 and 1, two threads per row; 16
 // producer (claims items, TMA of Q and K); 17 MMA issuer; 18 TMA of V; 19 waits for tiles;
@@ -46,15 +46,16 @@
 //
 // What bounds it, and what it measured.  Long prompts: the tensor pipe.  A pair of tiles is
 // 2,048 cycles of products and takes about 2,740 (issue gaps at the streams' turns); 8192
-// tokens of 32 query and 8 kv heads of 128, bf16, take 345 us (1,590 TFLOP/s) and, back to back
-// at the power cap, 371.  Both streams in step with their softmax cost 422, one thread per row
-// 434.  Few new tokens behind long contexts (4 x 24 tokens, 64 heads, 50-62 K): 200 us, 4.5 TB/s,
-// at the power cap too; single tokens: 6.2 TB/s of K/V.  Head size 64: the softmax
-// warps' work, about 2,500 cycles for a pair with 1,024 of products and as many of
-// exponentials (a third score buffer, so that no warp waits for scores, changed nothing: 303
-// against 300 us; without the maxima of each tile 289): 48 us for nine prompts of 40-1500
-// tokens with 16 heads.  fp8 caches: the widening, 1,300 cycles a tile for its four warps, and
-// the lead that three stages leave (367 us where fp16 products alone take 211).
+// tokens of 32 query and 8 kv heads of 128, bf16, take 345 us (1,590 TFLOP/s) until the power
+// cap sets in and 360-371 back to back.  Few new tokens behind long contexts (4 x 24 tokens, 64
+// heads, 50-62 K): 190-200 us, 4.5-4.8 TB/s, at the power cap too; 256 single tokens behind
+// 200-4000: 342 us, 6.2 TB/s of K/V.  Head size 64: neither pipe is full (products 23 % of the
+// cycles, exponentials 24 %, issue slots 48 %); a pair of tiles with 1,024 cycles of products and
+// as many of exponentials takes 2,500, the softmax warps' own chain of wait, load, weights, store
+// and arrival: 51 us for nine prompts of 40-1500 tokens with 16 heads, 292 for one of 8192 with
+// 32.  fp8 caches: the widening, 1,300 cycles a tile for its four warps, and the lead that three
+// stages leave (365 us where fp16 products alone take 211); single tokens pay it in full: the
+// 256 take 402 us, more than over a 16-bit cache.
 #pragma once
 
 #include "pa_chunk_device.cuh"
