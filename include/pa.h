@@ -71,6 +71,14 @@
  *           pa_prefill                   out <- attention of every new token over its
  *                                        sequence's tokens up to its own position
  *   pa_alloc_shrink and pa_move_blocks give the end of the pools back.
+ *
+ * A step that verifies drafted trees, the drafts decoded over selected blocks (one layer)
+ *   device  pa_select_blocks, pa_decode_sparse   each draft step: a few blocks of the context
+ *           pa_rope_and_cache            the drafted tokens' K and V into the pools
+ *           pa_decode_tree               the model's own rows for every drafted token
+ *           pa_tree_accept, pa_move_tokens   the accepted path, its rows moved together (all
+ *                                        layers), the new lengths
+ *           pa_key_bounds                the touched blocks' bounds, for the next drafts
  */
 #ifndef PA_H_
 #define PA_H_
@@ -511,6 +519,172 @@ pa_status pa_move_blocks(void* const* key_caches, void* const* value_caches, int
                          int32_t num_rows, int32_t max_blocks_per_seq, int32_t num_kv_heads,
                          int32_t head_size, int32_t block_size, int32_t num_blocks, pa_dtype dtype,
                          int32_t* status_dev, pa_stream stream);
+
+/* ------------------------------------------------------------------------------ */
+/* Trees of drafted tokens (speculative decoding with several continuations, verified in  */
+/* one pass [TALK, the part on speculative decoding])                                     */
+/* ------------------------------------------------------------------------------ */
+/* A sequence brings C new tokens that form a tree (or a forest): a token's parent stands
+ * before it, and it continues the path from the root to itself.  Their K and V rows are in the
+ * pools already, at positions L - C .. L - 1 in the tokens' order, whatever their rotary
+ * positions (pa_rope_and_cache takes positions of their own: a node's is L - C + its depth).
+ *   tree_mask   int32 [num_tokens][mask_words], 32 bits to a word: bit i % 32 of word i / 32 of
+ *               a token's row is set if the token sees new token i of its sequence.  Bits past
+ *               the token itself are ignored; its own bit is not implied.
+ * pa_decode_tree: new token j of sequence s attends to every token before the tree, and to the
+ * new tokens i <= j whose bit is set:
+ *   out[query_starts[s] + j][h] = sum_t softmax_t(scale * q . k_t) v_t over those tokens t;
+ * a row that sees nothing is a zero row.  What a row does not see does not touch it, infinities
+ * and NaN included.  With all bits set up to each token it is pa_prefill, whose arguments,
+ * limits, errors, accuracy and workspace it has otherwise; mask_words >= 1.  A sequence with
+ * more than 32 mask_words new tokens is flagged PA_DEVERR_BAD_LEN, and nothing sees its tokens
+ * past those. */
+size_t pa_decode_tree_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t head_size, int32_t max_context_len);
+pa_status pa_decode_tree(void* out, const void* query, const void* key_cache, const void* value_cache,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* query_starts,
+                         const int32_t* tree_mask, int32_t mask_words, int32_t num_tokens,
+                         int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                         int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
+                         pa_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                         pa_stream stream);
+/* The same over fp8 E4M3 pools, as pa_prefill_fp8. */
+pa_status pa_decode_tree_fp8(void* out, const void* query, const void* key_cache,
+                             const void* value_cache, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* query_starts, const int32_t* tree_mask, int32_t mask_words,
+                             int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                             int32_t num_blocks, int32_t max_context_len, float scale, float k_scale,
+                             float v_scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                             int32_t* status_dev, pa_stream stream);
+
+/* pa_tree_accept: the path of each tree that the model's own choices accept.  The parent of new
+ * token i is the highest bit below i in its mask row.  New token 0 (the root, a token that
+ * stands) is accepted; another one is if its parent is and draft_tokens of it equals
+ * target_tokens of its parent; one without a parent never is.  The path leads from the root to
+ * the deepest accepted token, of several to the first.  Of sequence s:
+ *   accepted      int32 [num_seqs][max_accepted]: the path's tokens by their place in the tree,
+ *                 ascending from 0, cut after max_accepted, then -1
+ *   num_accepted  int32 [num_seqs]: how many (0 for a sequence without new tokens)
+ *   next_tokens   int64 [num_seqs]: target_tokens of the last one, the token that follows (-1: none)
+ *   new_lens      int32 [num_seqs]: context_lens[s] - C + num_accepted[s]; may be context_lens
+ *   draft_tokens, target_tokens  int64 [num_tokens]: each new token's id, and the id that the
+ *                 model chooses after it
+ * mask_words is at most 64 here.  Another rule of acceptance (sampling) can fill accepted,
+ * num_accepted and new_lens itself.  Bad query_starts, or a context shorter than its tree, are
+ * clamped and flagged PA_DEVERR_BAD_LEN. */
+pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_accepted,
+                         int64_t* next_tokens, int32_t* new_lens, const int64_t* draft_tokens,
+                         const int64_t* target_tokens, const int32_t* tree_mask, int32_t mask_words,
+                         const int32_t* query_starts, const int32_t* context_lens, int32_t num_tokens,
+                         int32_t num_seqs, int32_t* status_dev, pa_stream stream);
+
+/* pa_move_tokens: moves the K and V rows of the accepted tokens together, in every layer's pools
+ * (bit-exact, in place): the row at position b + accepted[s][j] goes to position b + j for
+ * j < num_accepted[s], b = new_lens[s] - num_accepted[s] being the position of the tree's first
+ * token.  The sequence then holds new_lens[s] tokens; what the pools hold past them is unused.
+ * accepted[s] has to ascend with accepted[s][j] >= j; an entry that does not is left out and flagged
+ * PA_DEVERR_BAD_SLOT, one past the block table's row PA_DEVERR_BAD_LEN, one in a block outside the
+ * pool PA_DEVERR_BAD_BLOCK; num_accepted or new_lens out of range: the sequence is left out and
+ * flagged PA_DEVERR_BAD_LEN.  key_caches / value_caches as for pa_move_blocks (PA_F16, PA_BF16 or
+ * PA_FP8_E4M3, rows of a multiple of 16 bytes).  The blocks that new tokens sit in must not be
+ * shared between sequences (pa_alloc_reserve_batch sees to that).  On the host: reserve the blocks
+ * of the whole tree with pa_alloc_reserve_batch, take the slots from pa_alloc_slots, and append the
+ * accepted tokens alone.  One launch per 64 layers. */
+pa_status pa_move_tokens(void* const* key_caches, void* const* value_caches, int32_t num_layers,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* new_lens, const int32_t* accepted, int32_t max_accepted,
+                         const int32_t* num_accepted, int32_t num_seqs, int32_t num_kv_heads,
+                         int32_t head_size, int32_t block_size, int32_t num_blocks, pa_dtype dtype,
+                         int32_t* status_dev, pa_stream stream);
+
+/* ------------------------------------------------------------------------------ */
+/* Decoding over selected blocks of a long context                                      */
+/* ------------------------------------------------------------------------------ */
+/* A query token reads only some blocks of its context: those that a cheap score ranks highest,
+ * and the first and last ones.  Three calls: the bounds of the blocks that new tokens were
+ * written to (after pa_reshape_and_cache, pa_rope_and_cache or pa_move_tokens), the selection,
+ * and the attention.  All of it is approximate attention by intent; each call computes its own
+ * definition exactly.
+ *
+ * pa_key_bounds: for each kv head of a block, the largest and smallest value of every dim of the
+ * key rows that hold tokens (t < context_lens[s]), in 8 bits with one step:
+ *   step        = 2^(clamp(floor(log2 m), -100, 96) - 6), m the largest magnitude (m = 0: -100)
+ *   bounds [num_blocks][num_kv_heads][2][head_size] int8: the largest, then the smallest, of
+ *                 round(k / step), halves to even, clamped to +-127
+ *   bound_steps [num_blocks][num_kv_heads] fp32
+ * An infinity counts as the type's largest number; a NaN is passed over and makes the step NaN.
+ * Keys of fp8 pools are taken without their scale.  Blocks: those of sequence s that hold its last
+ * query_starts[s+1] - query_starts[s] <= max_new_tokens tokens (query_starts int32 [num_seqs + 1];
+ * NULL: max_new_tokens each), each anew from all its rows, so a block may be bounded any number of
+ * times, and has to be after its tokens change (a rejected tree among them).  dtype is the pool's
+ * (PA_F16, PA_BF16, PA_FP8_E4M3); head_size 64 or 128, block_size 16 or 32. */
+pa_status pa_key_bounds(int8_t* bounds, float* bound_steps, const void* key_cache,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                        const int32_t* context_lens, const int32_t* query_starts,
+                        int32_t max_new_tokens, int32_t num_seqs, int32_t num_kv_heads,
+                        int32_t head_size, int32_t block_size, int32_t num_blocks, pa_dtype dtype,
+                        int32_t* status_dev, pa_stream stream);
+
+/* pa_select_blocks: the blocks that each query token and kv head reads.  Query token j of a
+ * sequence (q_len each, as for pa_decode_mq) sees n = context_lens[s] - q_len + j + 1 tokens in
+ * B = ceil(n / block_size) blocks.  B <= num_selected: all of them.  Else the first num_first, the
+ * last num_last, and of the others those with the highest scores, num_selected in all; of equal
+ * scores the lowest block.  With the bounds hi, lo and the step of a block,
+ *   score = step * sum over the group's query heads and the dims of max(p hi, p lo),
+ *   p     = round(q / 2^(e - 5)), halves to even, e = max(floor(log2 m), -100), m the largest
+ *           magnitude of the group's rows of q (so |p| <= 64; m = 0: e = -100),
+ * an upper bound of the group's summed scores up to the rounding to 8 bits, in whole numbers: the
+ * selection is exact.  A NaN of q counts as 0, an infinity as the type's largest number; a NaN step
+ * scores highest; a block outside the pool scores 0 and is flagged PA_DEVERR_BAD_BLOCK.
+ *   selected  int32 [num_seqs][q_len][num_kv_heads][num_selected]: block indices within the
+ *             sequence, ascending, then -1
+ *   query     [num_seqs][q_len][num_q_heads][head_size], fp16 or bf16 (dtype)
+ * head_size 64 or 128, block_size 16 or 32, groups up to 16, contexts of up to 2^17 blocks; lengths
+ * past max_context_len or the table's row are clamped and flagged PA_DEVERR_BAD_LEN.  `workspace`
+ * (device, 256-byte aligned, of pa_select_blocks_workspace_size bytes) needs no initialisation and
+ * is dead after the call. */
+size_t pa_select_blocks_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_kv_heads,
+                                       int32_t block_size, int32_t max_context_len);
+pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* bounds,
+                           const float* bound_steps, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                           int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                           int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                           int32_t num_selected, int32_t num_first, int32_t num_last, pa_dtype dtype,
+                           void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                           pa_stream stream);
+
+/* pa_decode_sparse: attention of each query token over the tokens that it sees in its kv heads'
+ * selected blocks:
+ *   out[s][j][h] = sum_t softmax_t(scale * q . k_t) v_t,
+ *   t < context_lens[s] - q_len + j + 1 and t / block_size in selected[s][j][h / group].
+ * A row of selected ascends; -1 entries are skipped, and entries that do not ascend or lie outside
+ * the context are left out and flagged PA_DEVERR_BAD_BLOCK.  A row without tokens is a zero row.
+ * Other arguments, limits and accuracy as for pa_decode_auto (num_seqs * q_len * num_kv_heads at
+ * most 2^24, num_selected * block_size too).  `workspace` as for pa_decode_v2, of
+ * pa_decode_sparse_workspace_size bytes (0 for bad sizes). */
+size_t pa_decode_sparse_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
+                                       int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                                       int32_t num_selected);
+pa_status pa_decode_sparse(void* out, const void* query, const void* key_cache, const void* value_cache,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* selected, int32_t num_selected,
+                           int32_t num_seqs, int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                           int32_t head_size, int32_t block_size, int32_t num_blocks, float scale,
+                           pa_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                           pa_stream stream);
+/* The same over fp8 E4M3 pools (head_size 128), as pa_decode_fp8. */
+pa_status pa_decode_sparse_fp8(void* out, const void* query, const void* key_cache, const void* value_cache,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* context_lens, const int32_t* selected,
+                               int32_t num_selected, int32_t num_seqs, int32_t q_len,
+                               int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                               int32_t block_size, int32_t num_blocks, float scale, float k_scale,
+                               float v_scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                               int32_t* status_dev, pa_stream stream);
 
 /* Self-test of the failure path: launches a one-warp kernel that waits on a pipeline
  * barrier nobody arrives on, gives up after limit_us (1 .. 2,000,000) microseconds and

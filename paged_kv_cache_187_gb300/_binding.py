@@ -100,6 +100,19 @@ def _load():
         "pa_rope_and_cache_fp8": ([P, P, P, P, i64, i64, i64, P, P, P, P, i32, P, P, i32, i32, i32,
                                    i32, i32, i32, i32, i32, i32, f32, f32, P, P], i32),
         "pa_move_blocks": ([P, P, i32, P, i32, P, i32, i32, i32, i32, i32, i32, i32, P, P], i32),
+        "pa_decode_tree_workspace_size": ([i32] * 6, sz),
+        "pa_decode_tree": ([P, P, P, P, P, i32, P, P, P, i32] + [i32] * 8 + [f32, i32, P, sz, P, P], i32),
+        "pa_decode_tree_fp8": ([P, P, P, P, P, i32, P, P, P, i32] + [i32] * 8 +
+                               [f32, f32, f32, i32, P, sz, P, P], i32),
+        "pa_tree_accept": ([P, i32, P, P, P, P, P, P, i32, P, P, i32, i32, P, P], i32),
+        "pa_move_tokens": ([P, P, i32, P, i32, P, P, i32, P, i32, i32, i32, i32, i32, i32, P, P], i32),
+        "pa_key_bounds": ([P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32, i32, P, P], i32),
+        "pa_select_blocks_workspace_size": ([i32] * 5, sz),
+        "pa_select_blocks": ([P, P, P, P, P, i32, P] + [i32] * 12 + [P, sz, P, P], i32),
+        "pa_decode_sparse_workspace_size": ([i32] * 7, sz),
+        "pa_decode_sparse": ([P, P, P, P, P, i32, P, P] + [i32] * 8 + [f32, i32, P, sz, P, P], i32),
+        "pa_decode_sparse_fp8": ([P, P, P, P, P, i32, P, P] + [i32] * 8 +
+                                 [f32, f32, f32, i32, P, sz, P, P], i32),
         "pa_alloc_shrink": ([P, i32, P, i32, ctypes.POINTER(i32)], i32),
         "pa_alloc_create": ([i32, i32, u64, ctypes.POINTER(P)], i32),
         "pa_alloc_destroy": ([P], None),
@@ -576,7 +589,7 @@ class _Call:
 
 
 def _prefill(fn, pool, scales, out, query, key_cache, value_cache, block_tables, context_lens,
-             query_starts, max_context_len, scale, workspace, status, stream):
+             query_starts, max_context_len, scale, workspace, status, stream, *tree_mask):
     import torch
     i32 = torch.int32
     c = _Call()
@@ -589,6 +602,14 @@ def _prefill(fn, pool, scales, out, query, key_cache, value_cache, block_tables,
             or query_starts.dim() != 1 or query_starts.shape[0] != S + 1):
         raise ValueError("prefill: block_tables [S, max_blocks], context_lens [S] and "
                          "query_starts [S + 1] expected")
+    tree = ()
+    if tree_mask:
+        mask = tree_mask[0]
+        if not isinstance(mask, torch.Tensor):
+            raise TypeError("decode_tree: tree_mask must be a tensor")
+        if mask.dim() != 2 or mask.shape[0] != T:
+            raise ValueError("decode_tree: tree_mask [T, words] expected")
+        tree = (c.ptr(mask, "tree_mask", i32), mask.shape[1])
     wp, wb = None, 0
     if workspace is not None:
         wp, wb = c.ptr(workspace, "workspace", workspace.dtype), workspace.nbytes
@@ -601,7 +622,7 @@ def _prefill(fn, pool, scales, out, query, key_cache, value_cache, block_tables,
     _check(fn(
         c.ptr(out, "out", qt), c.ptr(query, "query", qt), k, v,
         c.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
-        c.ptr(context_lens, "context_lens", i32), c.ptr(query_starts, "query_starts", i32), T, S, Hq,
+        c.ptr(context_lens, "context_lens", i32), c.ptr(query_starts, "query_starts", i32), *tree, T, S, Hq,
         Hkv, D, bs, NB, max_context_len, scale, *scales, dt, wp, wb,
         None if status is None else c.ptr(status, "status", i32), c.stream(stream)))
 
@@ -715,6 +736,213 @@ def pa_move_blocks(key_caches, value_caches, block_pairs, block_tables=None, sta
         base, base + 8 * L, L, c.ptr(block_pairs, "block_pairs", torch.int32), block_pairs.shape[0],
         tables, rows, width, Hkv, D, bs, NB, dt,
         None if status is None else c.ptr(status, "status", torch.int32), c.stream(stream)))
+
+
+def pa_decode_tree_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_size,
+                                  max_context_len) -> int:
+    return int(_lib.pa_decode_tree_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads,
+                                                  head_size, max_context_len))
+
+
+def pa_decode_tree(out, query, key_cache, value_cache, block_tables, context_lens, query_starts,
+                   tree_mask, max_context_len: int, scale: float, workspace=None, status=None,
+                   stream=None):
+    """pa_prefill for new tokens that form a tree: tree_mask int32 [T, words], bit i % 32 of word
+    i / 32 of a token's row set if the token sees new token i of its sequence."""
+    _prefill(_lib.pa_decode_tree, None, (), out, query, key_cache, value_cache, block_tables,
+             context_lens, query_starts, int(max_context_len), float(scale), workspace, status,
+             stream, tree_mask)
+
+
+def pa_decode_tree_fp8(out, query, key_cache, value_cache, block_tables, context_lens, query_starts,
+                       tree_mask, max_context_len: int, scale: float, k_scale: float, v_scale: float,
+                       workspace=None, status=None, stream=None):
+    """pa_decode_tree over fp8 E4M3 pools (uint8 or float8_e4m3fn), head_size 128."""
+    _prefill(_lib.pa_decode_tree_fp8, True, (float(k_scale), float(v_scale)), out, query, key_cache,
+             value_cache, block_tables, context_lens, query_starts, int(max_context_len),
+             float(scale), workspace, status, stream, tree_mask)
+
+
+def pa_tree_accept(accepted, num_accepted, next_tokens, new_lens, draft_tokens, target_tokens,
+                   tree_mask, query_starts, context_lens, status=None, stream=None):
+    """The path of each tree that the model's choices accept: accepted int32 [S, max_accepted],
+    num_accepted int32 [S], next_tokens int64 [S], new_lens int32 [S] (may be context_lens), from
+    draft_tokens / target_tokens int64 [T] and tree_mask int32 [T, words]."""
+    import torch
+    i32, i64 = torch.int32, torch.int64
+    c = _Call()
+    T, S = draft_tokens.shape[0], context_lens.shape[0]
+    if (accepted.dim() != 2 or accepted.shape[0] != S or num_accepted.shape != (S,)
+            or next_tokens.shape != (S,) or new_lens.shape != (S,) or context_lens.dim() != 1
+            or query_starts.shape != (S + 1,)):
+        raise ValueError("tree_accept: accepted [S, max_accepted]; num_accepted, next_tokens, "
+                         "new_lens, context_lens [S] and query_starts [S + 1] expected")
+    if draft_tokens.dim() != 1 or target_tokens.shape != (T,) or tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise ValueError("tree_accept: draft_tokens, target_tokens [T] and tree_mask [T, words] expected")
+    _check(_lib.pa_tree_accept(
+        c.ptr(accepted, "accepted", i32), accepted.shape[1], c.ptr(num_accepted, "num_accepted", i32),
+        c.ptr(next_tokens, "next_tokens", i64), c.ptr(new_lens, "new_lens", i32),
+        c.ptr(draft_tokens, "draft_tokens", i64), c.ptr(target_tokens, "target_tokens", i64),
+        c.ptr(tree_mask, "tree_mask", i32), tree_mask.shape[1], c.ptr(query_starts, "query_starts", i32),
+        c.ptr(context_lens, "context_lens", i32), T, S,
+        None if status is None else c.ptr(status, "status", i32), c.stream(stream)))
+
+
+def pa_move_tokens(key_caches, value_caches, block_tables, new_lens, accepted, num_accepted,
+                   status=None, stream=None):
+    """Moves the rows of the accepted tokens together in every layer's pools (lists of
+    [NB, Hkv, bs, D] tensors): position b + accepted[s][j] to b + j, b = new_lens[s] -
+    num_accepted[s]."""
+    import torch
+    i32 = torch.int32
+    c = _Call()
+    L = len(key_caches)
+    if L == 0 or len(value_caches) != L:
+        raise ValueError("move_tokens: key_caches and value_caches of at least one layer expected")
+    k0 = key_caches[0]
+    NB, Hkv, bs, D = shape = k0.shape
+    S = new_lens.shape[0]
+    if (block_tables.dim() != 2 or block_tables.shape[0] != S or new_lens.dim() != 1
+            or accepted.dim() != 2 or accepted.shape[0] != S or num_accepted.shape != (S,)):
+        raise ValueError("move_tokens: block_tables [S, max_blocks], new_lens and num_accepted [S], "
+                         "accepted [S, max_accepted] expected")
+    pt = k0.dtype
+    dt = PA_FP8_E4M3 if k0.element_size() == 1 else _dt(k0)
+    if dt == PA_FP8_E4M3:
+        c.pool8(k0, "pool")
+    pools = array.array("Q")
+    for t in (*key_caches, *value_caches):
+        if t.shape != shape:
+            raise ValueError("move_tokens: the pools must have one shape and type")
+        pools.append(c.ptr(t, "pool", pt))
+    base = pools.buffer_info()[0]
+    _check(_lib.pa_move_tokens(
+        base, base + 8 * L, L, c.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
+        c.ptr(new_lens, "new_lens", i32), c.ptr(accepted, "accepted", i32), accepted.shape[1],
+        c.ptr(num_accepted, "num_accepted", i32), S, Hkv, D, bs, NB, dt,
+        None if status is None else c.ptr(status, "status", i32), c.stream(stream)))
+
+
+def pa_key_bounds(bounds, bound_steps, key_cache, block_tables, context_lens, max_new_tokens: int,
+                  query_starts=None, status=None, stream=None):
+    """Bounds of the keys of the blocks that hold each sequence's last tokens: max_new_tokens each,
+    or query_starts[s + 1] - query_starts[s] of them.  bounds int8 [NB, Hkv, 2, D] (largest, then
+    smallest), bound_steps fp32 [NB, Hkv]."""
+    import torch
+    i32 = torch.int32
+    c = _Call()
+    NB, Hkv, bs, D = key_cache.shape
+    S = context_lens.shape[0]
+    if bounds.shape != (NB, Hkv, 2, D) or bound_steps.shape != (NB, Hkv):
+        raise ValueError("key_bounds: bounds [NB, Hkv, 2, D] and bound_steps [NB, Hkv] expected")
+    if (context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S
+            or (query_starts is not None and query_starts.shape != (S + 1,))):
+        raise ValueError("key_bounds: block_tables [S, max_blocks], context_lens [S] and "
+                         "query_starts [S + 1] expected")
+    if key_cache.element_size() == 1:
+        dt, k = PA_FP8_E4M3, c.pool8(key_cache, "key_cache")
+    else:
+        dt, k = _dt(key_cache), c.ptr(key_cache, "key_cache", key_cache.dtype)
+    _check(_lib.pa_key_bounds(
+        c.ptr(bounds, "bounds", torch.int8), c.ptr(bound_steps, "bound_steps", torch.float32), k,
+        c.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
+        c.ptr(context_lens, "context_lens", i32),
+        None if query_starts is None else c.ptr(query_starts, "query_starts", i32),
+        int(max_new_tokens), S, Hkv, D, bs, NB, dt,
+        None if status is None else c.ptr(status, "status", i32), c.stream(stream)))
+
+
+def pa_select_blocks_workspace_size(num_seqs, q_len, num_kv_heads, block_size, max_context_len) -> int:
+    return int(_lib.pa_select_blocks_workspace_size(num_seqs, q_len, num_kv_heads, block_size,
+                                                    max_context_len))
+
+
+def _rows4(t, name):
+    """Shape of query tokens [S, q_len, ..]; [S, ..] is one query token each."""
+    if t.dim() == 4:
+        return tuple(t.shape)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [S, q_len, heads, ..] or [S, heads, ..]")
+    return t.shape[0], 1, t.shape[1], t.shape[2]
+
+
+def pa_select_blocks(selected, query, bounds, bound_steps, block_tables, context_lens, block_size: int,
+                     max_context_len: int, num_first: int, num_last: int, workspace=None, status=None,
+                     stream=None):
+    """The blocks that each query token and kv head reads: selected int32 [S, q_len, Hkv, n] (or
+    [S, Hkv, n]), ascending, then -1; query [S, q_len, Hq, D] (or [S, Hq, D])."""
+    import torch
+    i32 = torch.int32
+    c = _Call()
+    S, QL, Hq, D = _rows4(query, "query")
+    S2, QL2, Hkv, n = _rows4(selected, "selected")
+    NB = bounds.shape[0]
+    if (S2, QL2) != (S, QL) or bounds.shape != (NB, Hkv, 2, D) or bound_steps.shape != (NB, Hkv):
+        raise ValueError("select_blocks: inconsistent shapes")
+    if context_lens.shape != (S,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("select_blocks: block_tables [S, max_blocks] and context_lens [S] expected")
+    wp, wb = None, 0
+    if workspace is not None:
+        wp, wb = c.ptr(workspace, "workspace", workspace.dtype), workspace.nbytes
+    _check(_lib.pa_select_blocks(
+        c.ptr(selected, "selected", i32), c.ptr(query, "query", query.dtype),
+        c.ptr(bounds, "bounds", torch.int8), c.ptr(bound_steps, "bound_steps", torch.float32),
+        c.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
+        c.ptr(context_lens, "context_lens", i32), S, QL, Hq, Hkv, D, int(block_size), NB,
+        int(max_context_len), n, int(num_first), int(num_last), _dt(query), wp, wb,
+        None if status is None else c.ptr(status, "status", i32), c.stream(stream)))
+
+
+def pa_decode_sparse_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, head_size, block_size,
+                                    num_selected) -> int:
+    return int(_lib.pa_decode_sparse_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads,
+                                                    head_size, block_size, num_selected))
+
+
+def _sparse(fn, pool, scales, out, query, key_cache, value_cache, block_tables, context_lens, selected,
+            scale, workspace, status, stream):
+    import torch
+    i32 = torch.int32
+    c = _Call()
+    S, QL, Hq, D = _rows4(query, "query")
+    S2, QL2, Hkv, n = _rows4(selected, "selected")
+    NB, Hkv2, bs, D2 = key_cache.shape
+    if (out.shape != query.shape or value_cache.shape != key_cache.shape
+            or (S2, QL2, Hkv2, D2) != (S, QL, Hkv, D)):
+        raise ValueError("decode_sparse: inconsistent shapes")
+    if context_lens.shape != (S,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("decode_sparse: block_tables [S, max_blocks] and context_lens [S] expected")
+    wp, wb = None, 0
+    if workspace is not None:
+        wp, wb = c.ptr(workspace, "workspace", workspace.dtype), workspace.nbytes
+    qt = query.dtype
+    dt = _dt(query)
+    if pool is None:
+        k, v = c.ptr(key_cache, "key_cache", qt), c.ptr(value_cache, "value_cache", qt)
+    else:
+        k, v = c.pool8(key_cache, "key_cache"), c.pool8(value_cache, "value_cache")
+    _check(fn(
+        c.ptr(out, "out", qt), c.ptr(query, "query", qt), k, v,
+        c.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
+        c.ptr(context_lens, "context_lens", i32), c.ptr(selected, "selected", i32), n, S, QL, Hq, Hkv, D,
+        bs, NB, scale, *scales, dt, wp, wb,
+        None if status is None else c.ptr(status, "status", i32), c.stream(stream)))
+
+
+def pa_decode_sparse(out, query, key_cache, value_cache, block_tables, context_lens, selected,
+                     scale: float, workspace=None, status=None, stream=None):
+    """Attention of query tokens [S, q_len, Hq, D] (or [S, Hq, D]) over the blocks that selected
+    int32 [S, q_len, Hkv, n] (or [S, Hkv, n]) names."""
+    _sparse(_lib.pa_decode_sparse, None, (), out, query, key_cache, value_cache, block_tables,
+            context_lens, selected, float(scale), workspace, status, stream)
+
+
+def pa_decode_sparse_fp8(out, query, key_cache, value_cache, block_tables, context_lens, selected,
+                         scale: float, k_scale: float, v_scale: float, workspace=None, status=None,
+                         stream=None):
+    """pa_decode_sparse over fp8 E4M3 pools (uint8 or float8_e4m3fn), head_size 128."""
+    _sparse(_lib.pa_decode_sparse_fp8, True, (float(k_scale), float(v_scale)), out, query, key_cache,
+            value_cache, block_tables, context_lens, selected, float(scale), workspace, status, stream)
 
 
 def pa_selftest_wait_timeout(status, limit_us: int, stream=None):

@@ -31,11 +31,18 @@ SOURCES = [
     "pa_prefill_bf16.cu",
     "pa_prefill_f16.cu",
     "pa_prefill_fp8.cu",
+    "pa_tree_bf16.cu",
+    "pa_tree_f16.cu",
+    "pa_tree_fp8.cu",
     "pa_aux.cu",
     "pa_chunk_aux.cu",
+    "pa_blocks.cu",
+    "pa_sparse.cu",
+    "pa_tree_aux.cu",
     "pa_noalloc.cu",
     "pa_host.cpp",
     "pa_chunk_host.cpp",
+    "pa_masked_host.cpp",
     "pa_alloc.cpp",
 ]
 

@@ -72,6 +72,10 @@ struct PrefillParams {
                                // of one that goes on
     float* part_acc;           // [CTAs][2][2 streams][head_size][128]
     int32_t* status;
+    // trees of new tokens (null: causal): bit i of word w of a token's row is set if the token
+    // sees new token 32 w + i of its sequence
+    const uint32_t* tree_mask; // [num_tokens][mask_words]
+    int32_t mask_words;
 };
 
 struct PfWorkspace {
@@ -88,6 +92,13 @@ cudaError_t launch_prefill_f16(const CUtensorMap& qmap, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, const PrefillParams& p, cudaStream_t stream);
 cudaError_t launch_prefill_fp8(bool q_bf16, const CUtensorMap& qmap, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, const PrefillParams& p, cudaStream_t stream);
+// The same for trees of new tokens (tree_mask not null).
+cudaError_t launch_tree_bf16(const CUtensorMap& qmap, const CUtensorMap& kmap,
+                             const CUtensorMap& vmap, const PrefillParams& p, cudaStream_t stream);
+cudaError_t launch_tree_f16(const CUtensorMap& qmap, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, const PrefillParams& p, cudaStream_t stream);
+cudaError_t launch_tree_fp8(bool q_bf16, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, const PrefillParams& p, cudaStream_t stream);
 
 constexpr int32_t kMaxRopePairs = 128;
 struct RopeParams {

@@ -22,7 +22,9 @@ __device__ __forceinline__ PfChunk chunk_of(const PrefillParams& p, int32_t s, b
     const int32_t end = min(max(b, c.start), p.num_tokens);
     c.count = end - c.start;
     c.len = min(max(l, 0), cap);
-    if (report && (c.start != a || end != b || c.len != l) && p.status) atomicOr(p.status, 4 /* PA_DEVERR_BAD_LEN */);
+    const bool wide = p.tree_mask && c.count > 32ll * p.mask_words;   // a tree past its masks
+    if (report && (c.start != a || end != b || c.len != l || wide) && p.status)
+        atomicOr(p.status, 4 /* PA_DEVERR_BAD_LEN */);
     const int32_t span = 2 * p.tpt;
     c.row_tiles = c.count / span + (c.count % span != 0);
     return c;

@@ -1,6 +1,6 @@
 // pa_chunk_host.cpp -- host side of the chunk operators declared in include/pa.h: argument
 // checks, workspace layout, TMA tensor maps and launches of pa_prefill(_fp8),
-// pa_rope_and_cache(_fp8) and pa_move_blocks.
+// pa_decode_tree(_fp8), pa_rope_and_cache(_fp8) and pa_move_blocks.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -97,46 +97,52 @@ struct PrefillArgs {
     float scale, k_scale, v_scale;
     pa_dtype dtype;
     bool kv8;
+    const char* who = "prefill";
+    bool tree = false;              // the new tokens see each other by tree_mask
+    const void* tree_mask = nullptr;
+    int32_t mask_words = 0;
 };
 
 pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* status,
                       cudaStream_t stream) {
     if (a.num_tokens < 0 || a.num_seqs < 0 || a.num_q_heads <= 0 || a.num_kv_heads <= 0 ||
         a.num_blocks <= 0 || a.max_blocks_per_seq <= 0 || a.max_context_len < 0)
-        return fail(PA_ERR_INVALID_ARG, "prefill: sizes must be positive (num_tokens, num_seqs >= 0)");
+        return fail(PA_ERR_INVALID_ARG, "%s: sizes must be positive (num_tokens, num_seqs >= 0)", a.who);
     if (a.num_tokens > kMaxTokens)
-        return fail(PA_ERR_UNSUPPORTED, "prefill: num_tokens %d > %d", a.num_tokens, kMaxTokens);
-    if (a.dtype != PA_F16 && a.dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "prefill: dtype");
+        return fail(PA_ERR_UNSUPPORTED, "%s: num_tokens %d > %d", a.who, a.num_tokens, kMaxTokens);
+    if (a.dtype != PA_F16 && a.dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "%s: dtype", a.who);
     if (a.head_size != 64 && a.head_size != 128)
-        return fail(PA_ERR_UNSUPPORTED, "prefill: head_size %d (64 or 128)", a.head_size);
+        return fail(PA_ERR_UNSUPPORTED, "%s: head_size %d (64 or 128)", a.who, a.head_size);
     if (a.kv8 && a.head_size != 128)
-        return fail(PA_ERR_UNSUPPORTED, "prefill: an fp8 cache needs head_size 128");
+        return fail(PA_ERR_UNSUPPORTED, "%s: an fp8 cache needs head_size 128", a.who);
     if (a.kv8 && !(a.k_scale > 0.f && a.v_scale > 0.f))
-        return fail(PA_ERR_INVALID_ARG, "prefill: k_scale and v_scale must be positive");
+        return fail(PA_ERR_INVALID_ARG, "%s: k_scale and v_scale must be positive", a.who);
     if (a.block_size != 16 && a.block_size != 32)
-        return fail(PA_ERR_UNSUPPORTED, "prefill: block_size %d (16 or 32)", a.block_size);
-    if (!std::isfinite(a.scale)) return fail(PA_ERR_INVALID_ARG, "prefill: scale must be finite");
+        return fail(PA_ERR_UNSUPPORTED, "%s: block_size %d (16 or 32)", a.who, a.block_size);
+    if (!std::isfinite(a.scale)) return fail(PA_ERR_INVALID_ARG, "%s: scale must be finite", a.who);
     if (a.num_q_heads % a.num_kv_heads)
-        return fail(PA_ERR_INVALID_ARG, "prefill: num_q_heads %% num_kv_heads != 0");
+        return fail(PA_ERR_INVALID_ARG, "%s: num_q_heads %% num_kv_heads != 0", a.who);
     const int32_t group = a.num_q_heads / a.num_kv_heads;
-    if (group > 16) return fail(PA_ERR_UNSUPPORTED, "prefill: query group %d > 16", group);
+    if (group > 16) return fail(PA_ERR_UNSUPPORTED, "%s: query group %d > 16", a.who, group);
     const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * a.block_size;
     if (rows + (int64_t)a.num_kv_heads * a.block_size > INT32_MAX)
-        return fail(PA_ERR_UNSUPPORTED, "prefill: pool has more than 2^31 rows");
+        return fail(PA_ERR_UNSUPPORTED, "%s: pool has more than 2^31 rows", a.who);
+    if (a.tree && a.mask_words < 1) return fail(PA_ERR_INVALID_ARG, "%s: mask_words %d", a.who, a.mask_words);
     if (a.num_tokens == 0 || a.num_seqs == 0) return ok();
     if (!a.out || !a.query || !a.key_cache || !a.value_cache || !a.block_tables || !a.context_lens ||
         !a.query_starts)
-        return fail(PA_ERR_INVALID_ARG, "prefill: null pointer");
+        return fail(PA_ERR_INVALID_ARG, "%s: null pointer", a.who);
+    if (a.tree && !a.tree_mask) return fail(PA_ERR_INVALID_ARG, "%s: null tree_mask", a.who);
     if (!aligned16(a.out) || !aligned16(a.query) || !aligned16(a.key_cache) || !aligned16(a.value_cache))
-        return fail(PA_ERR_INVALID_ARG, "prefill: device buffers must be 16-byte aligned");
+        return fail(PA_ERR_INVALID_ARG, "%s: device buffers must be 16-byte aligned", a.who);
     const pa::PfWorkspace L = pa::prefill_workspace(a.num_tokens, a.num_seqs, a.num_q_heads,
                                                     a.num_kv_heads, a.head_size, a.max_context_len);
     if ((int64_t)L.max_row_tiles * a.num_kv_heads > INT32_MAX)
-        return fail(PA_ERR_UNSUPPORTED, "prefill: too many work items");
+        return fail(PA_ERR_UNSUPPORTED, "%s: too many work items", a.who);
     if (!ws || ws_bytes < L.total)
-        return fail(PA_ERR_WORKSPACE, "prefill: workspace of %zu bytes, need %zu", ws_bytes, L.total);
+        return fail(PA_ERR_WORKSPACE, "%s: workspace of %zu bytes, need %zu", a.who, ws_bytes, L.total);
     if (reinterpret_cast<uintptr_t>(ws) & 255u)
-        return fail(PA_ERR_INVALID_ARG, "prefill: workspace must be 256-byte aligned");
+        return fail(PA_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", a.who);
     int sms = 0;
     pa_status st = sm_count(&sms);
     if (st != PA_OK) return st;
@@ -182,6 +188,8 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
     p.part_ml = reinterpret_cast<float2*>(w + L.part_ml);
     p.part_acc = reinterpret_cast<float*>(w + L.part_acc);
     p.status = status;
+    p.tree_mask = a.tree ? static_cast<const uint32_t*>(a.tree_mask) : nullptr;
+    p.mask_words = a.mask_words;
 
     // query [tokens][heads][dims]: a box is 64 dims (the swizzle span) of one kv head's
     // group and the tokens of a stream; the pools as matrices of rows, a box one block
@@ -198,12 +206,17 @@ pa_status run_prefill(const PrefillArgs& a, void* ws, size_t ws_bytes, int32_t* 
     if ((st = encode(&vm, a.value_cache, a.kv8, 2, dims, str, box)) != PA_OK) return st;
 
     cudaError_t e = p.direct ? cudaSuccess : pa::launch_prefill_plan(p, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "prefill plan launch");
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: plan launch: %s", a.who, cudaGetErrorString(e));
     const bool bf16 = a.dtype == PA_BF16;
-    e = a.kv8 ? pa::launch_prefill_fp8(bf16, qm, km, vm, p, stream)
-        : bf16 ? pa::launch_prefill_bf16(qm, km, vm, p, stream)
-               : pa::launch_prefill_f16(qm, km, vm, p, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+    if (a.tree)
+        e = a.kv8 ? pa::launch_tree_fp8(bf16, qm, km, vm, p, stream)
+            : bf16 ? pa::launch_tree_bf16(qm, km, vm, p, stream)
+                   : pa::launch_tree_f16(qm, km, vm, p, stream);
+    else
+        e = a.kv8 ? pa::launch_prefill_fp8(bf16, qm, km, vm, p, stream)
+            : bf16 ? pa::launch_prefill_bf16(qm, km, vm, p, stream)
+                   : pa::launch_prefill_f16(qm, km, vm, p, stream);
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", a.who, cudaGetErrorString(e));
     return ok();
 }
 
@@ -356,6 +369,43 @@ pa_status pa_prefill_fp8(void* out, const void* query, const void* key_cache,
                         context_lens, query_starts, num_tokens, num_seqs, num_q_heads, num_kv_heads,
                         head_size, block_size, num_blocks, max_context_len, scale, k_scale, v_scale,
                         dtype, true};
+    return run_prefill(a, workspace, workspace_bytes, status_dev, (cudaStream_t)stream);
+}
+
+size_t pa_decode_tree_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t head_size, int32_t max_context_len) {
+    return pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_size,
+                                     max_context_len);
+}
+
+pa_status pa_decode_tree(void* out, const void* query, const void* key_cache, const void* value_cache,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* query_starts,
+                         const int32_t* tree_mask, int32_t mask_words, int32_t num_tokens,
+                         int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                         int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
+                         pa_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                         pa_stream stream) {
+    const PrefillArgs a{out, query, key_cache, value_cache, block_tables, max_blocks_per_seq,
+                        context_lens, query_starts, num_tokens, num_seqs, num_q_heads, num_kv_heads,
+                        head_size, block_size, num_blocks, max_context_len, scale, 1.f, 1.f, dtype,
+                        false, "decode_tree", true, tree_mask, mask_words};
+    return run_prefill(a, workspace, workspace_bytes, status_dev, (cudaStream_t)stream);
+}
+
+pa_status pa_decode_tree_fp8(void* out, const void* query, const void* key_cache,
+                             const void* value_cache, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* query_starts, const int32_t* tree_mask, int32_t mask_words,
+                             int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                             int32_t num_blocks, int32_t max_context_len, float scale, float k_scale,
+                             float v_scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                             int32_t* status_dev, pa_stream stream) {
+    const PrefillArgs a{out, query, key_cache, value_cache, block_tables, max_blocks_per_seq,
+                        context_lens, query_starts, num_tokens, num_seqs, num_q_heads, num_kv_heads,
+                        head_size, block_size, num_blocks, max_context_len, scale, k_scale, v_scale,
+                        dtype, true, "decode_tree", true, tree_mask, mask_words};
     return run_prefill(a, workspace, workspace_bytes, status_dev, (cudaStream_t)stream);
 }
 

@@ -1,0 +1,393 @@
+// pa_masked_host.cpp -- host side of the operators around reads of the cache that follow a mask:
+// argument checks, workspaces and launches of pa_tree_accept, pa_move_tokens, pa_key_bounds,
+// pa_select_blocks and pa_decode_sparse(_fp8), declared in include/pa.h.  (pa_decode_tree is a
+// form of the chunk attention: pa_chunk_host.cpp.)
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "../../include/pa.h"
+#include "pa_internal.h"
+#include "pa_masked.h"
+
+namespace {
+
+pa_status fail(pa_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    return (pa_status)pa::set_last_error(st, buf);
+}
+
+pa_status ok() { return (pa_status)pa::set_last_error(PA_OK, ""); }
+
+pa_status cuda_fail(cudaError_t e, const char* what) {
+    return fail(PA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+constexpr int32_t kMaxGridY = 65535;
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_accepted,
+                         int64_t* next_tokens, int32_t* new_lens, const int64_t* draft_tokens,
+                         const int64_t* target_tokens, const int32_t* tree_mask, int32_t mask_words,
+                         const int32_t* query_starts, const int32_t* context_lens, int32_t num_tokens,
+                         int32_t num_seqs, int32_t* status_dev, pa_stream stream) {
+    if (num_tokens < 0 || num_seqs < 0 || max_accepted <= 0 || mask_words <= 0)
+        return fail(PA_ERR_INVALID_ARG, "tree_accept: sizes must be positive (num_tokens, num_seqs >= 0)");
+    if (mask_words > pa::kMaxTreeWords)
+        return fail(PA_ERR_UNSUPPORTED, "tree_accept: mask_words %d > %d", mask_words, pa::kMaxTreeWords);
+    if (num_seqs == 0) return ok();
+    if (!accepted || !num_accepted || !next_tokens || !new_lens || !query_starts || !context_lens ||
+        (num_tokens > 0 && (!draft_tokens || !target_tokens || !tree_mask)))
+        return fail(PA_ERR_INVALID_ARG, "tree_accept: null pointer");
+    pa::AcceptParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.accepted = accepted;
+    p.num_accepted = num_accepted;
+    p.next_tokens = next_tokens;
+    p.new_lens = new_lens;
+    p.draft = draft_tokens;
+    p.target = target_tokens;
+    p.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
+    p.query_starts = query_starts;
+    p.context_lens = context_lens;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.mask_words = mask_words;
+    p.max_accepted = max_accepted;
+    p.status = status_dev;
+    const cudaError_t e = pa::launch_tree_accept(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "tree_accept launch");
+    return ok();
+}
+
+pa_status pa_move_tokens(void* const* key_caches, void* const* value_caches, int32_t num_layers,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* new_lens, const int32_t* accepted, int32_t max_accepted,
+                         const int32_t* num_accepted, int32_t num_seqs, int32_t num_kv_heads,
+                         int32_t head_size, int32_t block_size, int32_t num_blocks, pa_dtype dtype,
+                         int32_t* status_dev, pa_stream stream) {
+    if (num_layers < 0 || num_seqs < 0 || max_blocks_per_seq <= 0 || max_accepted <= 0 ||
+        num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks <= 0)
+        return fail(PA_ERR_INVALID_ARG, "move_tokens: sizes must be positive (num_layers, num_seqs >= 0)");
+    if (dtype != PA_F16 && dtype != PA_BF16 && dtype != PA_FP8_E4M3)
+        return fail(PA_ERR_UNSUPPORTED, "move_tokens: dtype");
+    const int64_t row = (int64_t)head_size * (dtype == PA_FP8_E4M3 ? 1 : 2);
+    if (row % 16) return fail(PA_ERR_INVALID_ARG, "move_tokens: rows must be 16-byte multiples");
+    if (row / 16 * num_kv_heads > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "move_tokens: too many heads");
+    if (num_seqs == 0 || num_layers == 0) return ok();
+    if (!key_caches || !value_caches || !block_tables || !new_lens || !accepted || !num_accepted)
+        return fail(PA_ERR_INVALID_ARG, "move_tokens: null pointer");
+    for (int32_t l = 0; l < num_layers; ++l) {
+        if (!key_caches[l] || !value_caches[l]) return fail(PA_ERR_INVALID_ARG, "move_tokens: null pool");
+        if (!aligned16(key_caches[l]) || !aligned16(value_caches[l]))
+            return fail(PA_ERR_INVALID_ARG, "move_tokens: pools must be 16-byte aligned");
+    }
+    pa::MoveTokensParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.block_tables = block_tables;
+    p.new_lens = new_lens;
+    p.accepted = accepted;
+    p.num_accepted = num_accepted;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.max_accepted = max_accepted;
+    p.num_blocks = num_blocks;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.row_vecs = (int32_t)(row / 16);
+    p.status = status_dev;
+    for (int32_t l0 = 0; l0 < num_layers; l0 += p.num_layers) {
+        p.num_layers = std::min(num_layers - l0, pa::kMoveTokenLayers);
+        for (int32_t l = 0; l < p.num_layers; ++l) {
+            p.key[l] = key_caches[l0 + l];
+            p.value[l] = value_caches[l0 + l];
+        }
+        p.report = l0 == 0;
+        const cudaError_t e = pa::launch_move_tokens(p, (cudaStream_t)stream);
+        if (e != cudaSuccess) return cuda_fail(e, "move_tokens launch");
+    }
+    return ok();
+}
+
+pa_status pa_key_bounds(int8_t* bounds, float* bound_steps, const void* key_cache,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                        const int32_t* context_lens, const int32_t* query_starts,
+                        int32_t max_new_tokens, int32_t num_seqs, int32_t num_kv_heads,
+                        int32_t head_size, int32_t block_size, int32_t num_blocks, pa_dtype dtype,
+                        int32_t* status_dev, pa_stream stream) {
+    if (num_seqs < 0 || max_new_tokens < 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0)
+        return fail(PA_ERR_INVALID_ARG, "key_bounds: sizes must be positive (num_seqs, max_new_tokens >= 0)");
+    if (dtype != PA_F16 && dtype != PA_BF16 && dtype != PA_FP8_E4M3)
+        return fail(PA_ERR_UNSUPPORTED, "key_bounds: dtype");
+    if (head_size != 64 && head_size != 128)
+        return fail(PA_ERR_UNSUPPORTED, "key_bounds: head_size %d (64 or 128)", head_size);
+    if (block_size != 16 && block_size != 32)
+        return fail(PA_ERR_UNSUPPORTED, "key_bounds: block_size %d (16 or 32)", block_size);
+    if (num_seqs == 0 || max_new_tokens == 0) return ok();
+    if (!bounds || !bound_steps || !key_cache || !block_tables || !context_lens)
+        return fail(PA_ERR_INVALID_ARG, "key_bounds: null pointer");
+    if (!aligned16(bounds) || !aligned16(key_cache))
+        return fail(PA_ERR_INVALID_ARG, "key_bounds: buffers must be 16-byte aligned");
+    pa::BoundsParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.bounds = bounds;
+    p.steps = bound_steps;
+    p.key_cache = key_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_starts = query_starts;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.num_kv_heads = num_kv_heads;
+    p.head_size = head_size;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.max_new_tokens = max_new_tokens;
+    // n tokens in a row touch (n - 1) / bs + 1 blocks, and one more where they cross an edge
+    p.slots = (int32_t)std::min<int64_t>(((int64_t)max_new_tokens + block_size - 2) / block_size + 1,
+                                         max_blocks_per_seq);
+    p.status = status_dev;
+    if ((int64_t)num_seqs * p.slots * num_kv_heads > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "key_bounds: too many blocks");
+    const cudaError_t e = pa::launch_key_bounds(p, dtype == PA_FP8_E4M3 ? pa::BoundsType::kFp8
+                                                   : dtype == PA_BF16   ? pa::BoundsType::kBf16
+                                                                        : pa::BoundsType::kF16,
+                                                (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "key_bounds launch");
+    return ok();
+}
+
+size_t pa_select_blocks_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_kv_heads,
+                                       int32_t block_size, int32_t max_context_len) {
+    if (num_seqs < 0 || q_len <= 0 || num_kv_heads <= 0 || block_size <= 0 || max_context_len < 0) return 0;
+    const size_t blocks = (size_t)max_context_len / block_size + 1;
+    return align256(sizeof(uint32_t) * (size_t)num_seqs * q_len * num_kv_heads * blocks);
+}
+
+pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* bounds,
+                           const float* bound_steps, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                           int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                           int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                           int32_t num_selected, int32_t num_first, int32_t num_last, pa_dtype dtype,
+                           void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                           pa_stream stream) {
+    if (num_seqs < 0 || q_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0 || max_context_len < 0 || num_selected <= 0)
+        return fail(PA_ERR_INVALID_ARG, "select_blocks: sizes must be positive (num_seqs >= 0)");
+    if (num_first < 0 || num_last < 0 || (int64_t)num_first + num_last > num_selected)
+        return fail(PA_ERR_INVALID_ARG, "select_blocks: num_first %d and num_last %d of %d blocks", num_first,
+                    num_last, num_selected);
+    if (dtype != PA_F16 && dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "select_blocks: dtype");
+    if (head_size != 64 && head_size != 128)
+        return fail(PA_ERR_UNSUPPORTED, "select_blocks: head_size %d (64 or 128)", head_size);
+    if (block_size != 16 && block_size != 32)
+        return fail(PA_ERR_UNSUPPORTED, "select_blocks: block_size %d (16 or 32)", block_size);
+    if (num_q_heads % num_kv_heads)
+        return fail(PA_ERR_INVALID_ARG, "select_blocks: num_q_heads %% num_kv_heads != 0");
+    if (num_q_heads / num_kv_heads > 16)
+        return fail(PA_ERR_UNSUPPORTED, "select_blocks: query group %d > 16", num_q_heads / num_kv_heads);
+    if (num_kv_heads > kMaxGridY) return fail(PA_ERR_UNSUPPORTED, "select_blocks: too many heads");
+    if ((int64_t)num_seqs * q_len > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "select_blocks: too many rows");
+    const int64_t context = std::min<int64_t>(max_context_len, (int64_t)max_blocks_per_seq * block_size);
+    const int32_t blocks = (int32_t)((context + block_size - 1) / block_size);
+    if (blocks > pa::kMaxSelectBlocks)
+        return fail(PA_ERR_UNSUPPORTED, "select_blocks: contexts of %d blocks (at most %d)", blocks,
+                    pa::kMaxSelectBlocks);
+    if (num_seqs == 0) return ok();
+    if (!selected || !query || !bounds || !bound_steps || !block_tables || !context_lens)
+        return fail(PA_ERR_INVALID_ARG, "select_blocks: null pointer");
+    if (!aligned16(query) || !aligned16(bounds))
+        return fail(PA_ERR_INVALID_ARG, "select_blocks: buffers must be 16-byte aligned");
+    const size_t need = sizeof(uint32_t) * (size_t)num_seqs * q_len * num_kv_heads * blocks;
+    if (blocks > num_selected) {
+        if (!workspace || workspace_bytes < need)
+            return fail(PA_ERR_WORKSPACE, "select_blocks: workspace of %zu bytes, need %zu", workspace_bytes, need);
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+            return fail(PA_ERR_INVALID_ARG, "select_blocks: workspace must be 256-byte aligned");
+    }
+    pa::SelectParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.selected = selected;
+    p.query = query;
+    p.bounds = bounds;
+    p.steps = bound_steps;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.q_len = q_len;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.head_size = head_size;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.max_context_len = (int32_t)context;
+    p.num_selected = num_selected;
+    p.num_first = num_first;
+    p.num_last = num_last;
+    p.max_blocks = blocks;
+    p.chunk = 64;
+    p.keys = static_cast<uint32_t*>(workspace);
+    p.status = status_dev;
+    const cudaError_t e = pa::launch_select_blocks(p, dtype == PA_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "select_blocks launch");
+    return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// The workspace of the attention over selected blocks: the rows' tables and lengths, then the
+// decode's own.
+struct SparseWorkspace {
+    size_t tables, lens, decode, total;
+};
+SparseWorkspace sparse_workspace(int64_t rows, int32_t group, int32_t head_size, int32_t block_size,
+                                 int32_t num_selected) {
+    SparseWorkspace L;
+    L.tables = 0;
+    L.lens = align256(sizeof(int32_t) * (size_t)rows * num_selected);
+    L.decode = L.lens + align256(sizeof(int32_t) * (size_t)rows);
+    L.total = L.decode + pa_decode_auto_workspace_size((int32_t)rows, group, 1, head_size, block_size,
+                                                       num_selected * block_size);
+    return L;
+}
+
+struct SparseArgs {
+    void* out;
+    const void *query, *key_cache, *value_cache;
+    const int32_t* block_tables;
+    int32_t max_blocks_per_seq;
+    const int32_t* context_lens;
+    const int32_t* selected;
+    int32_t num_selected, num_seqs, q_len, num_q_heads, num_kv_heads, head_size, block_size, num_blocks;
+    float scale, k_scale, v_scale;
+    pa_dtype dtype;
+    bool kv8;
+};
+
+pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* status, cudaStream_t stream) {
+    if (a.num_seqs < 0 || a.q_len <= 0 || a.num_q_heads <= 0 || a.num_kv_heads <= 0 || a.num_blocks <= 0 ||
+        a.max_blocks_per_seq <= 0 || a.num_selected <= 0)
+        return fail(PA_ERR_INVALID_ARG, "decode_sparse: sizes must be positive (num_seqs >= 0)");
+    if (a.dtype != PA_F16 && a.dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "decode_sparse: dtype");
+    if (a.head_size != 64 && a.head_size != 128)
+        return fail(PA_ERR_UNSUPPORTED, "decode_sparse: head_size %d (64 or 128)", a.head_size);
+    if (a.kv8 && a.head_size != 128)
+        return fail(PA_ERR_UNSUPPORTED, "decode_sparse: an fp8 cache needs head_size 128");
+    if (a.kv8 && !(a.k_scale > 0.f && a.v_scale > 0.f))
+        return fail(PA_ERR_INVALID_ARG, "decode_sparse: k_scale and v_scale must be positive");
+    if (a.block_size != 16 && a.block_size != 32)
+        return fail(PA_ERR_UNSUPPORTED, "decode_sparse: block_size %d (16 or 32)", a.block_size);
+    if (!std::isfinite(a.scale)) return fail(PA_ERR_INVALID_ARG, "decode_sparse: scale must be finite");
+    if (a.num_q_heads % a.num_kv_heads)
+        return fail(PA_ERR_INVALID_ARG, "decode_sparse: num_q_heads %% num_kv_heads != 0");
+    const int32_t group = a.num_q_heads / a.num_kv_heads;
+    if (group > 16) return fail(PA_ERR_UNSUPPORTED, "decode_sparse: query group %d > 16", group);
+    const int64_t pool_rows = (int64_t)a.num_blocks * a.num_kv_heads * a.block_size;
+    if (pool_rows + (int64_t)a.num_kv_heads * a.block_size > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "decode_sparse: pool has more than 2^31 rows");
+    const int64_t rows = (int64_t)a.num_seqs * a.q_len * a.num_kv_heads;
+    if (rows > (1 << 24)) return fail(PA_ERR_UNSUPPORTED, "decode_sparse: more than 2^24 (token, kv head) rows");
+    if ((int64_t)a.num_selected * a.block_size > (1 << 24))
+        return fail(PA_ERR_UNSUPPORTED, "decode_sparse: more than 2^24 selected tokens a row");
+    if (a.num_seqs == 0) return ok();
+    if (!a.out || !a.query || !a.key_cache || !a.value_cache || !a.block_tables || !a.context_lens || !a.selected)
+        return fail(PA_ERR_INVALID_ARG, "decode_sparse: null pointer");
+    if (!aligned16(a.out) || !aligned16(a.query) || !aligned16(a.key_cache) || !aligned16(a.value_cache))
+        return fail(PA_ERR_INVALID_ARG, "decode_sparse: device buffers must be 16-byte aligned");
+    const SparseWorkspace L = sparse_workspace(rows, group, a.head_size, a.block_size, a.num_selected);
+    if (!ws || ws_bytes < L.total)
+        return fail(PA_ERR_WORKSPACE, "decode_sparse: workspace of %zu bytes, need %zu", ws_bytes, L.total);
+    if (reinterpret_cast<uintptr_t>(ws) & 255u)
+        return fail(PA_ERR_INVALID_ARG, "decode_sparse: workspace must be 256-byte aligned");
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    pa::SparseParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.selected = a.selected;
+    p.block_tables = a.block_tables;
+    p.context_lens = a.context_lens;
+    p.max_blocks_per_seq = a.max_blocks_per_seq;
+    p.num_seqs = a.num_seqs;
+    p.q_len = a.q_len;
+    p.num_kv_heads = a.num_kv_heads;
+    p.block_size = a.block_size;
+    p.num_blocks = a.num_blocks;
+    p.num_selected = a.num_selected;
+    p.tables = reinterpret_cast<int32_t*>(w + L.tables);
+    p.lens = reinterpret_cast<int32_t*>(w + L.lens);
+    p.status = status;
+    const cudaError_t e = pa::launch_sparse_tables(p, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "decode_sparse launch");
+    const int32_t tokens = a.num_selected * a.block_size, blocks = a.num_blocks * a.num_kv_heads;
+    if (a.kv8)
+        return pa_decode_fp8(a.out, a.query, a.key_cache, a.value_cache, p.tables, a.num_selected, p.lens,
+                             (int32_t)rows, group, 1, a.head_size, a.block_size, blocks, tokens, a.scale,
+                             a.k_scale, a.v_scale, a.dtype, 0, 0, w + L.decode, L.total - L.decode, status,
+                             (pa_stream)stream);
+    return pa_decode_auto(a.out, a.query, a.key_cache, a.value_cache, p.tables, a.num_selected, p.lens,
+                          (int32_t)rows, group, 1, a.head_size, a.block_size, blocks, tokens, a.scale, a.dtype,
+                          w + L.decode, L.total - L.decode, status, (pa_stream)stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_decode_sparse_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
+                                       int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                                       int32_t num_selected) {
+    if (num_seqs < 0 || q_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+        block_size <= 0 || num_selected <= 0 || num_q_heads % num_kv_heads ||
+        (int64_t)num_seqs * q_len * num_kv_heads > (1 << 24) || (int64_t)num_selected * block_size > (1 << 24))
+        return 0;
+    return sparse_workspace((int64_t)num_seqs * q_len * num_kv_heads, num_q_heads / num_kv_heads, head_size,
+                            block_size, num_selected).total;
+}
+
+pa_status pa_decode_sparse(void* out, const void* query, const void* key_cache, const void* value_cache,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* selected, int32_t num_selected,
+                           int32_t num_seqs, int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                           int32_t head_size, int32_t block_size, int32_t num_blocks, float scale,
+                           pa_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                           pa_stream stream) {
+    const SparseArgs a{out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                       selected, num_selected, num_seqs, q_len, num_q_heads, num_kv_heads, head_size,
+                       block_size, num_blocks, scale, 1.f, 1.f, dtype, false};
+    return run_sparse(a, workspace, workspace_bytes, status_dev, (cudaStream_t)stream);
+}
+
+pa_status pa_decode_sparse_fp8(void* out, const void* query, const void* key_cache, const void* value_cache,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* context_lens, const int32_t* selected,
+                               int32_t num_selected, int32_t num_seqs, int32_t q_len,
+                               int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                               int32_t block_size, int32_t num_blocks, float scale, float k_scale,
+                               float v_scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                               int32_t* status_dev, pa_stream stream) {
+    const SparseArgs a{out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                       selected, num_selected, num_seqs, q_len, num_q_heads, num_kv_heads, head_size,
+                       block_size, num_blocks, scale, k_scale, v_scale, dtype, true};
+    return run_sparse(a, workspace, workspace_bytes, status_dev, (cudaStream_t)stream);
+}
+
+}  // extern "C"

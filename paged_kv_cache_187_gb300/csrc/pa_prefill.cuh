@@ -78,9 +78,10 @@ constexpr int kRegLaunch = 80, kRegSoft = 88, kRegAux = 72, kRegFix = 56;
 static_assert(4 * kRegSoft + kRegAux + kRegFix <= 6 * kRegLaunch, "register split");
 
 // BF16: type of the MMA operands (fp16 for fp8 caches); QBF16: type of query and out.
-template <bool BF16_, bool QBF16_, int D_, int BS_, bool KV8_>
+// TREE: the new tokens see each other by a mask, not causally.
+template <bool BF16_, bool QBF16_, int D_, int BS_, bool KV8_, bool TREE_ = false>
 struct Cfg {
-    static constexpr bool kBf16 = BF16_, kQBf16 = QBF16_, kKv8 = KV8_;
+    static constexpr bool kBf16 = BF16_, kQBf16 = QBF16_, kKv8 = KV8_, kTree = TREE_;
     static constexpr int D = D_, BS = BS_;
     static constexpr int BLOCKS = kPfTok / BS_;
     static constexpr int HALVES = D_ / 64;                   // 128-byte swizzle spans per row
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         u.cnt[1] = u.nt / 2;
                     }
                     // first tile that some row does not see whole
-                    u.fix0 = max(u.len - u.q_len + u.tok0 + 1, 0) / kPfTok - tile0;
+                    u.fix0 = max(u.len - u.q_len + (C::kTree ? 0 : u.tok0 + 1), 0) / kPfTok - tile0;
                 }
                 // no one reads the table of two items ago any more
                 if (sm.any_nonfinite[us]) {
@@ -1022,8 +1023,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t cnt = un.cnt[si];
             const bool both = !C::kKv8 && un.both;
             // tokens this row sees, and the fewest any row of the stream sees
-            const int32_t whole = un.len - un.q_len + un.tok0 + (both ? 0 : si * p.tpt) + 1;
-            const int32_t limit = min(whole + qtok, un.len);
+            const int32_t first_row = un.tok0 + (both ? 0 : si * p.tpt);
+            const int32_t whole = un.len - un.q_len + (C::kTree ? 0 : first_row + 1);
+            const int32_t limit = min(whole + qtok + (C::kTree ? first_row + 1 : 0), un.len);
+            // A tree's row, 32 bits of its mask from new token i0 on: 1 for the tokens that it
+            // sees, those before the tree among them.  (A row past the tree's last has no mask
+            // and sees nothing of it.)
+            auto tree_bits = [&](int32_t i0) -> uint32_t {
+                const int32_t tok = first_row + qtok;
+                auto word = [&](int32_t w) -> uint32_t {
+                    if (w < 0) return 0xffffffffu;
+                    return tok < un.q_len && w < p.mask_words
+                               ? __ldg(p.tree_mask + (size_t)(un.q_start + tok) * p.mask_words + w)
+                               : 0u;
+                };
+                return __funnelshift_r(word(i0 >> 5), word((i0 >> 5) + 1), (uint32_t)i0 & 31u);
+            };
             // first token of the half tile
             int32_t t0 = (un.tile0 + (both ? si : 0)) * kPfTok + half * kCols;
             const int32_t t_step = both ? 2 * kPfTok : kPfTok;
@@ -1038,7 +1053,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 32 of the row's 64 scores, loaded before, masked
                 auto scores = [&](int h, float (&x)[32]) {
                     tmem_arrived(x);
-                    if (masked) {
+                    if constexpr (C::kTree) {
+                        if (masked) {
+                            // (and nothing past the row's own token)
+                            const int32_t n = seen - 32 * h;
+                            uint32_t bits = tree_bits(t0 + 32 * h - whole);
+                            bits = n >= 32 ? bits : n <= 0 ? 0u : bits & ((1u << n) - 1u);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1u ? x[c] : hidden;
+                        }
+                    } else if (masked) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) x[c] = 32 * h + c < seen ? x[c] : hidden;
                     }
@@ -1172,6 +1196,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 top_here = si ? ref > theirs : ref >= theirs;
                 ref = top;
             }
+            // Element d of token t's V row: 0 +inf, 1 -inf, 2 NaN, -1 none of them.
+            [[maybe_unused]] auto odd_class = [&](int32_t t, int d) -> int {
+                const int32_t block = p.block_tables[(size_t)u.seq * p.max_blocks_per_seq + t / C::BS];
+                if (block < 0 || block >= p.num_blocks) return -1;
+                const size_t at = (((size_t)block * Hkv + u.kvh) * C::BS + t % C::BS) * D + d;
+                if constexpr (C::kKv8) {
+                    return (static_cast<const uint8_t*>(p.value_cache)[at] & 0x7Fu) == 0x7Fu ? 2 : -1;
+                } else {
+                    constexpr uint32_t kExp = C::kBf16 ? 0x7F80u : 0x7C00u;
+                    const uint32_t v = static_cast<const uint16_t*>(p.value_cache)[at];
+                    return (v & kExp) != kExp ? -1 : (v & 0x7FFFu) != kExp ? 2 : (int)(v >> 15);
+                }
+            };
             // infinite and NaN values that were kept out of the products, for the rows that
             // see them
             if (nonfinite && cnt > 0) {
@@ -1179,9 +1216,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int d = 0; d < kDims; ++d) {
                     float o = tmem_ld1(to + d);
                     const int32_t* const first = &sm.nonfinite[us][0][half * kDims + d];
-                    if (top_here && first[0] < limit) o += INFINITY;
-                    if (top_here && first[D] < limit) o -= INFINITY;
-                    if (top_here && first[2 * D] < limit) o = __int_as_float(0x7fc00000);
+                    // (a tree's row sees all before the tree; within it, it looks for itself)
+                    const int32_t sure = C::kTree ? whole : limit;
+                    bool pos = first[0] < sure, neg = first[D] < sure, nan = first[2 * D] < sure;
+                    if constexpr (C::kTree) {
+                        const int32_t from = max(whole, min(min(first[0], first[D]), first[2 * D]));
+                        if (top_here && mine && max(max(first[0], first[D]), first[2 * D]) >= whole)
+#pragma unroll 1
+                            for (int32_t t = from; t < limit; ++t) {
+                                if (!(tree_bits(t - whole) & 1u)) continue;
+                                const int c = odd_class(t, half * kDims + d);
+                                pos |= c == 0;
+                                neg |= c == 1;
+                                nan |= c == 2;
+                            }
+                        __syncwarp();
+                    }
+                    if (top_here && pos) o += INFINITY;
+                    if (top_here && neg) o -= INFINITY;
+                    if (top_here && nan) o = __int_as_float(0x7fc00000);
                     tmem_st1(to + d, o);
                 }
             }
@@ -1240,7 +1293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     odd_values<C::kBf16>(static_cast<const uint16_t*>(p.value_cache) + vrow * D + d, inf, nan);
                 };
                 // the tokens that all these rows see, the warp together, then each row's own
-                const int32_t all = __reduce_min_sync(0xffffffffu, odd ? limit : kNoToken);
+                const int32_t all =
+                    __reduce_min_sync(0xffffffffu, odd ? (C::kTree ? min(max(whole, 0), limit) : limit) : kNoToken);
 #pragma unroll 1
                 for (int32_t t = 0; t < all; t += 32) {
                     if (t + lane < all) look(t + lane);
@@ -1249,7 +1303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 inf = __reduce_or_sync(0xffffffffu, inf);
                 nan = __reduce_or_sync(0xffffffffu, nan);
 #pragma unroll 1
-                for (int32_t t = all; odd && t < limit; ++t) look(t);
+                for (int32_t t = all; odd && t < limit; ++t)
+                    if (!C::kTree || (tree_bits(t - whole) & 1u)) look(t);
                 __syncwarp();
                 odd &= ~nan & (inf ^ (inf >> 16));
 #pragma unroll
