@@ -37,7 +37,9 @@ SOURCES = [
     "pa_aux.cu",
     "pa_chunk_aux.cu",
     "pa_blocks.cu",
-    "pa_sparse.cu",
+    "pa_sparse_bf16.cu",
+    "pa_sparse_f16.cu",
+    "pa_sparse_fp8.cu",
     "pa_tree_aux.cu",
     "pa_noalloc.cu",
     "pa_host.cpp",

@@ -1,6 +1,6 @@
-// pa_blocks.cu -- decoding over selected blocks of a long context: bounds of each block's keys,
-// and the selection of blocks by a score of the query against them.  (The attention over the
-// selected blocks is in pa_sparse.cu.)
+// pa_blocks.cu -- decoding over selected blocks of a long context: bounds of each block's keys, the
+// selection of blocks by a score of the query against them, and the tables that the attention over
+// the selected blocks (pa_sparse.cuh) reads.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -160,144 +160,257 @@ __device__ __forceinline__ int32_t blocks_of(const SelectParams& p, int32_t len,
     return seen / p.block_size + (seen % p.block_size != 0);
 }
 
+// The score of a block needs of a group's queries only the sums of their positive and of their
+// negative values: with p the queries as whole numbers,
+//     sum_j sum_d max(p_jd hi_d, p_jd lo_d) = sum_d P_d hi_d + N_d lo_d,
+//     P = sum_j max(p_j, 0), N = sum_j min(p_j, 0),
+// however many heads.  D / 16 lanes take a (query token, kv head), 16 dims each, and write its
+// weights, 16 bits each: P of 16 dims, then N, lane by lane.
+constexpr int kWeightThreads = 128;
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kWeightThreads) select_weights_kernel(const SelectParams p) {
+    constexpr int kLanes = D / 16;
+    grid_dependency_wait();
+    allow_dependent_launch();      // (after the wait: the scores read all but the weights early)
+    const int64_t row = ((int64_t)blockIdx.x * kWeightThreads + threadIdx.x) / kLanes;   // token and head
+    const int32_t c = threadIdx.x % kLanes;
+    const int64_t rows = (int64_t)p.num_seqs * p.q_len * p.num_kv_heads;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) +
+                                                    min(row, rows - 1) * p.group * D + c * 16);
+    // four heads' rows at once (those past the group: the last one's again, not counted)
+    uint4 x[4][2];
+    auto load = [&](int32_t g0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int32_t g = min(g0 + k, p.group - 1);
+            x[k][0] = q[g * (D / 8)];
+            x[k][1] = q[g * (D / 8) + 1];
+        }
+    };
+    // calls f(i, v) for the 16 values of head k (NaN: 0)
+    auto each = [&](int k, auto&& f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4& y = x[k][i >> 2];
+            float a, b;
+            unpack2<BF16>((i & 3) == 0 ? y.x : (i & 3) == 1 ? y.y : (i & 3) == 2 ? y.z : y.w, a, b);
+            f(2 * i, a == a ? a : 0.f);
+            f(2 * i + 1, b == b ? b : 0.f);
+        }
+    };
+    float most = 0.f;
+    for (int32_t g0 = 0; g0 < p.group; g0 += 4) {
+        load(g0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) each(k, [&](int, float v) { most = fmaxf(most, fabsf(v)); });
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    // (an infinity counts as the largest number, which comes to 64 as well)
+    constexpr float kBig = BF16 ? 3.38953139e38f : 65504.f;
+    const float inv = power_of_two(5 - exponent_of(fminf(most, kBig)));
+    int32_t up[16], down[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) up[i] = down[i] = 0;
+    for (int32_t g0 = 0; g0 < p.group; g0 += 4) {
+        if (p.group > 4) load(g0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (g0 + k < p.group)
+                each(k, [&](int i, float v) {
+                    const int32_t z = __float2int_rn(fminf(fmaxf(v * inv, -64.f), 64.f));
+                    up[i] += max(z, 0);
+                    down[i] += min(z, 0);
+                });
+    }
+    if (row >= rows) return;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w[i] = (uint32_t)((up[2 * i] & 0xFFFF) | (up[2 * i + 1] << 16));
+        w[8 + i] = (uint32_t)((down[2 * i] & 0xFFFF) | (down[2 * i + 1] << 16));
+    }
+    uint4* out = reinterpret_cast<uint4*>(p.weights + (row * kLanes + c) * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
 constexpr int kScoreThreads = 256;
 constexpr int kScoreBatch = 4;            // records that a lane has on their way
 
-// Two signed 16-bit by two signed 8-bit products, added: the lower (upper) bytes of b.
-__device__ __forceinline__ int32_t dp2_lo(int32_t a, int32_t b, int32_t c) { return __dp2a_lo(a, b, c); }
-__device__ __forceinline__ int32_t dp2_hi(int32_t a, int32_t b, int32_t c) { return __dp2a_hi(a, b, c); }
+// Blocks of a sequence with scores: the last query token's, without the first and last ones.
+__device__ __forceinline__ int32_t scored_of(const SelectParams& p, int32_t s) {
+    const int32_t blocks = blocks_of(p, context_of(p, s, false), p.q_len - 1);
+    return blocks > p.num_selected ? blocks - p.num_first - p.num_last : 0;
+}
 
-// Scores of a chunk of one sequence's blocks: CTA (sequence, chunk, kv heads by the groups of
-// lanes that it has).  The heads of a kv head's group are quantised with one power-of-two step
-// to whole numbers of at most 64 and added, the positive ones against the upper bounds, the
-// negative ones against the lower: sum_j sum_d max(q hi, q lo) = sum_d P hi + N lo, however
-// many heads.  A group of lanes has a head's weights (16-bit) in registers and 16 bytes of a
-// record (2 D bytes) each; whole-number products, exact sums (below 2^24), one exact product
-// with the block's step.  Bound by HBM: 2 D + 4 bytes per block and kv head.
-template <bool BF16, int D, int QT>
-__global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const SelectParams p) {
-    constexpr int kLanes = 2 * D / 16;                       // lanes per record
+// Scores of the sequences' blocks, laid end to end (and once more for each further turn of kv
+// heads, as many at a time as the CTA has groups of lanes) and cut into equal slices, one per CTA:
+// contexts of any lengths keep all CTAs busy to the end.  (20 contexts of 60-126 K tokens: 43 us,
+// with a CTA per piece of 64 blocks of a sequence 51.)  A lane has 16 dims of a head: their weights
+// in registers, and 16 bytes of upper and of lower bounds of four records on their way; D / 16 lanes
+// share a record.  Whole-number products, exact sums (below 2^24), one exact product with the
+// block's step.  All that the weights do not come with is read before the kernel that writes them
+// has finished.  Bound by HBM: 2 D + 4 bytes per block and kv head.
+template <int D, int QT>
+__global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const SelectParams p) {
+    constexpr int kLanes = D / 16;                           // lanes per record
     constexpr int kGroups = kScoreThreads / kLanes;
-    __shared__ int32_t phys_s[kMaxScoreChunk];
-    grid_dependency_wait();
+    __shared__ int32_t rec_s[kMaxScoreChunk];                // first record of the blocks; -1: none
     allow_dependent_launch();
-    const int32_t s = blockIdx.x, tid = threadIdx.x;
-    const int32_t len = context_of(p, s, blockIdx.y == 0 && blockIdx.z == 0 && tid == 0);
-    // blocks to score: the last query token's, without the first and last ones
-    const int32_t blocks = blocks_of(p, len, p.q_len - 1);
-    const int32_t b0 = max((int32_t)blockIdx.y * p.chunk, p.num_first);
-    const int32_t b1 = min(((int32_t)blockIdx.y + 1) * p.chunk, blocks - p.num_last);
-    if (blocks <= p.num_selected || b0 >= b1) return;
+    const int32_t tid = threadIdx.x, lane = tid & 31;
     const int32_t heads = min(p.num_kv_heads, kGroups);      // kv heads of this CTA at a time
-    for (int32_t i = tid; i < b1 - b0; i += kScoreThreads) {
-        int32_t phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + b0 + i];
-        if (phys < 0 || phys >= p.num_blocks) {
-            if (p.status && blockIdx.z == 0) atomicOr(p.status, kDevBadBlock);
-            phys = -1;
-        }
-        phys_s[i] = phys;
-    }
+    const int32_t turns = (p.num_kv_heads + heads - 1) / heads;
     const int32_t grp = tid / kLanes, c = tid % kLanes;
-    const int32_t h = (int32_t)blockIdx.z * heads + grp % heads, sub = grp / heads, subs = kGroups / heads;
-    const bool mine = sub < subs && h < p.num_kv_heads;
-    const bool low = c >= kLanes / 2;                        // this lane has lower bounds
-    const int32_t d0 = (c % (kLanes / 2)) * 16;
-    __syncthreads();
-    for (int32_t j0 = 0; j0 < p.q_len; j0 += QT) {
-        int32_t w[QT][8];                                    // 16 weights, two to a register
+    const int32_t sub = grp / heads, subs = kGroups / heads;
+    // Sequences s0 .. s0 + 31, one per lane: blocks with scores, and their running sum.
+    int32_t own = 0, upto = 0;
+    auto sequences = [&](int32_t s0) {
+        own = s0 + lane < p.num_seqs ? scored_of(p, s0 + lane) : 0;
+        upto = own;
 #pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            const int32_t j = min(j0 + t, p.q_len - 1);
-            const uint4* q = reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(p.query) +
-                (((size_t)s * p.q_len + j) * p.num_q_heads + (size_t)(mine ? h : 0) * p.group) * D + d0);
-            constexpr float kBig = BF16 ? 3.38953139e38f : 65504.f;
-            auto dims = [&](int32_t g, float (&v)[16]) {
-                const uint4 a = q[g * (D / 8)], b = q[g * (D / 8) + 1];
-                const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    unpack2<BF16>(x[i], v[2 * i], v[2 * i + 1]);
-                    // (NaN counts as 0, an infinity as the largest number)
-                    v[2 * i] = v[2 * i] == v[2 * i] ? fminf(fmaxf(v[2 * i], -kBig), kBig) : 0.f;
-                    v[2 * i + 1] = v[2 * i + 1] == v[2 * i + 1] ? fminf(fmaxf(v[2 * i + 1], -kBig), kBig) : 0.f;
-                }
-            };
-            float most = 0.f;
-            for (int32_t g = 0; g < p.group; ++g) {
-                float v[16];
-                dims(g, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(v[i]));
-            }
-#pragma unroll
-            for (int o = 1; o < kLanes / 2; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const float inv = power_of_two(5 - exponent_of(most));
-            int32_t sum[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum[i] = 0;
-            for (int32_t g = 0; g < p.group; ++g) {
-                float v[16];
-                dims(g, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int32_t x = __float2int_rn(v[i] * inv);
-                    sum[i] += low ? min(x, 0) : max(x, 0);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[t][i] = (sum[2 * i] & 0xFFFF) | (sum[2 * i + 1] << 16);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        // (a warp's groups go through the batches together: its shuffles need every lane)
-        for (int32_t first = 0; first < b1 - b0; first += kScoreBatch * subs) {
-            uint4 x[kScoreBatch];
-            // the record whose score this lane ends up with
-            const int32_t u = (c / (kLanes / 4)) & 3;
-            float step = 0.f;
+        return __shfl_sync(0xffffffffu, upto, 31);
+    };
+    // this CTA's slice
+    int64_t all = 0;
+    for (int32_t s0 = 0; s0 < p.num_seqs; s0 += 32) all += sequences(s0);
+    const int64_t total = all * turns;
+    int64_t at0 = total * blockIdx.x / gridDim.x;
+    const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
+    bool waited = false;
+    while (at0 < end) {
+        // the sequence and block of `at0` (every warp for itself)
+        const int32_t turn = (int32_t)(at0 / all);
+        int64_t before = turn * all;
+        int32_t s = 0, b0 = 0, n = 0;
+        for (int32_t s0 = 0; s0 < p.num_seqs; s0 += 32) {
+            if (p.num_seqs > 32) sequences(s0);
+            const uint32_t past = __ballot_sync(0xffffffffu, before + upto > at0);
+            if (past) {
+                const int32_t l = __ffs(past) - 1;
+                s = s0 + l;
+                n = __shfl_sync(0xffffffffu, own, l);
+                b0 = (int32_t)(at0 - before) - (__shfl_sync(0xffffffffu, upto, l) - n);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        n = (int32_t)min(min((int64_t)(n - b0), end - at0), (int64_t)kMaxScoreChunk);
+        at0 += n;
+        b0 += p.num_first;
+        bool bad = false;
+        for (int32_t i = tid; i < n; i += kScoreThreads) {
+            const int32_t phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + b0 + i];
+            const bool out = phys < 0 || phys >= p.num_blocks;
+            bad |= out;
+            rec_s[i] = out ? -1 : phys * p.num_kv_heads;     // (a pool has fewer than 2^31 rows)
+        }
+        __syncthreads();
+        const int32_t h = turn * heads + grp % heads;
+        const bool mine = sub < subs && h < p.num_kv_heads;
+        const int32_t head = mine ? h : 0;
+        // the record whose score this lane ends up with, of four
+        const int32_t u = (c / (kLanes / 4)) & 3;
+        const int8_t* const at = p.bounds + c * 16;
+        // Four records of this lane, from place `first` on, on their way (past the end: the last
+        // one again).
+        struct Batch {
+            uint4 x[kScoreBatch][2];
+            float step;
+        };
+        auto fetch = [&](int32_t first, Batch& t) {
+            int32_t rec[kScoreBatch];
+#pragma unroll
+            for (int k = 0; k < kScoreBatch; ++k) rec[k] = rec_s[min(first + k * subs, n - 1)];
 #pragma unroll
             for (int k = 0; k < kScoreBatch; ++k) {
-                const int32_t i = first + k * subs + sub;
-                x[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (mine && i < b1 - b0 && phys_s[i] >= 0) {
-                    const size_t rec = (size_t)phys_s[i] * p.num_kv_heads + h;
-                    x[k] = __ldg(reinterpret_cast<const uint4*>(p.bounds + rec * 2 * D) + c);
-                    if (k == u) step = __ldg(p.steps + rec);
-                }
+                const int8_t* src = at + (size_t)(uint32_t)(max(rec[k], 0) + head) * (2 * D);
+                t.x[k][0] = __ldg(reinterpret_cast<const uint4*>(src));
+                t.x[k][1] = __ldg(reinterpret_cast<const uint4*>(src + D));
             }
+            const int32_t r = u == 0 ? rec[0] : u == 1 ? rec[1] : u == 2 ? rec[2] : rec[3];
+            t.step = __ldg(p.steps + (size_t)(uint32_t)(max(r, 0) + head));
+            if (r < 0) t.step = 0.f;
+        };
+        const int32_t stride = kScoreBatch * subs;
+        Batch one, two;
+        fetch(sub, one);
+        if (!waited) {
+            grid_dependency_wait();
+            waited = true;
+        }
+        if (bad && turn == 0 && p.status) atomicOr(p.status, kDevBadBlock);
+        for (int32_t j0 = 0; j0 < p.q_len; j0 += QT) {
+            int32_t wp[QT][8], wn[QT][8];                    // 16 weights each, two to a register
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
-                int32_t dot[kScoreBatch];
+                const int64_t row = ((int64_t)s * p.q_len + min(j0 + t, p.q_len - 1)) * p.num_kv_heads + head;
+                const int4* src = reinterpret_cast<const int4*>(p.weights + (row * kLanes + c) * 16);
 #pragma unroll
-                for (int k = 0; k < kScoreBatch; ++k) {
-                    int32_t a = dp2_lo(w[t][0], (int32_t)x[k].x, 0), b = dp2_hi(w[t][1], (int32_t)x[k].x, 0);
-                    a = dp2_lo(w[t][2], (int32_t)x[k].y, a);
-                    b = dp2_hi(w[t][3], (int32_t)x[k].y, b);
-                    a = dp2_lo(w[t][4], (int32_t)x[k].z, a);
-                    b = dp2_hi(w[t][5], (int32_t)x[k].z, b);
-                    a = dp2_lo(w[t][6], (int32_t)x[k].w, a);
-                    b = dp2_hi(w[t][7], (int32_t)x[k].w, b);
-                    dot[k] = a + b;
-                }
-                // the lanes' sums: half of the lanes go on with records 2, 3, then with the odd one
-                constexpr int kHalf = kLanes / 2, kQuarter = kLanes / 4;
-                const bool up = c & kHalf, odd = c & kQuarter;
-                int32_t a = up ? dot[2] : dot[0], b = up ? dot[3] : dot[1];
-                a += __shfl_xor_sync(0xffffffffu, up ? dot[0] : dot[2], kHalf);
-                b += __shfl_xor_sync(0xffffffffu, up ? dot[1] : dot[3], kHalf);
-                int32_t y = odd ? b : a;
-                y += __shfl_xor_sync(0xffffffffu, odd ? a : b, kQuarter);
-#pragma unroll
-                for (int o = kQuarter / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                const int32_t i = first + u * subs + sub;
-                if (mine && c % kQuarter == 0 && i < b1 - b0 && j0 + t < p.q_len) {
-                    const float score = (float)y * step;
-                    const uint32_t bits = __float_as_uint(score);
-                    const uint32_t key = score != score ? 0xffffffffu : (bits >> 31) ? ~bits : bits | 0x80000000u;
-                    p.keys[(((size_t)s * p.q_len + j0 + t) * p.num_kv_heads + h) * p.max_blocks + b0 + i] = key;
+                for (int i = 0; i < 2; ++i) {
+                    const int4 a = src[i], b = src[2 + i];
+                    wp[t][4 * i] = a.x, wp[t][4 * i + 1] = a.y, wp[t][4 * i + 2] = a.z, wp[t][4 * i + 3] = a.w;
+                    wn[t][4 * i] = b.x, wn[t][4 * i + 1] = b.y, wn[t][4 * i + 2] = b.z, wn[t][4 * i + 3] = b.w;
                 }
             }
+            uint32_t* const keys =
+                p.keys + (((size_t)s * p.q_len + j0) * p.num_kv_heads + head) * p.max_blocks + b0;
+            auto score = [&](int32_t first, const Batch& y) {
+                const int32_t i = first + u * subs;
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    int32_t dot[kScoreBatch];
+#pragma unroll
+                    for (int k = 0; k < kScoreBatch; ++k) {
+                        int32_t a = 0, b = 0;
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const uint4 &v = y.x[k][0], &z = y.x[k][1];
+                            const int32_t hi = (int32_t)(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w);
+                            const int32_t lo = (int32_t)(m == 0 ? z.x : m == 1 ? z.y : m == 2 ? z.z : z.w);
+                            a = __dp2a_lo(wp[t][2 * m], hi, a);
+                            b = __dp2a_hi(wp[t][2 * m + 1], hi, b);
+                            a = __dp2a_lo(wn[t][2 * m], lo, a);
+                            b = __dp2a_hi(wn[t][2 * m + 1], lo, b);
+                        }
+                        dot[k] = a + b;
+                    }
+                    // the lanes' sums: half of the lanes go on with records 2, 3, then with the odd one
+                    constexpr int kHalf = kLanes / 2, kQuarter = kLanes / 4;
+                    const bool top = c & kHalf, odd = c & kQuarter;
+                    int32_t a = top ? dot[2] : dot[0], b = top ? dot[3] : dot[1];
+                    a += __shfl_xor_sync(0xffffffffu, top ? dot[0] : dot[2], kHalf);
+                    b += __shfl_xor_sync(0xffffffffu, top ? dot[1] : dot[3], kHalf);
+                    int32_t d = odd ? b : a;
+                    d += __shfl_xor_sync(0xffffffffu, odd ? a : b, kQuarter);
+#pragma unroll
+                    for (int o = kQuarter / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                    if (mine && c % kQuarter == 0 && i < n && j0 + t < p.q_len) {
+                        const float f = (float)d * y.step;
+                        const uint32_t bits = __float_as_uint(f);
+                        keys[(size_t)t * p.num_kv_heads * p.max_blocks + i] =
+                            f != f ? 0xffffffffu : (bits >> 31) ? ~bits : bits | 0x80000000u;
+                    }
+                }
+            };
+            // (a warp's groups go through the steps together: its shuffles need every lane)
+            if (j0 > 0) fetch(sub, one);
+            for (int32_t first = sub; first - sub < n; first += 2 * stride) {
+                fetch(first + stride, two);
+                score(first, one);
+                fetch(first + 2 * stride, one);
+                score(first + stride, two);
+            }
         }
+        __syncthreads();                                     // rec_s is free again
     }
+    if (!waited) grid_dependency_wait();
+    if (blockIdx.x == 0)
+        for (int32_t s = tid; s < p.num_seqs; s += kScoreThreads) (void)context_of(p, s, true);   // reports
 }
 
 constexpr int kSelThreads = 512;
@@ -332,23 +445,35 @@ __device__ __forceinline__ int32_t scan_cta(int32_t x, int32_t* buf, int32_t* to
     return before;
 }
 
-// CTA (query token, kv head): the `want` largest of its row's scores, by histograms over the
-// range that still holds the smallest of them: each pass divides it by 2048, starting from the
-// scores' own range, so that the counts spread.  What is taken is a bit per block, which puts
-// the list in order; of equal scores the first ones are taken.  Bound by latency: about three
-// passes over at most 16 keys a thread, with the scans between them.
+// CTA (query token, kv head): the `want` largest of its row's scores.  A histogram over the
+// scores' own range (2048 bins, so that the counts spread) finds the bin that holds the smallest
+// of them; what is in that bin is ranked one against the other, or, where that is more than there
+// are threads, the range is narrowed to the bin and divided again, until one value is left, of
+// which the first blocks are taken.  What is taken is a bit per block, which puts the list in
+// order.  Bound by latency: the passes over at most 16 keys a thread and the scans between them.
 __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectParams p) {
     extern __shared__ uint32_t sel_smem[];
     __shared__ int32_t buf[32];
-    __shared__ int32_t hist[kSelBins];
+    __shared__ __align__(16) int32_t hist[kSelBins];
     __shared__ uint32_t range[2];             // the scores' least and greatest
     __shared__ int32_t found[2];              // the bin, and the scores above it
-    grid_dependency_wait();
-    allow_dependent_launch();
+    __shared__ int32_t gathered;
+    static_assert(2 * kSelThreads <= kSelBins, "the candidates take the histogram's place");
     const int32_t tid = threadIdx.x, lane = tid & 31;
+    // (where scores come first, the kernel that writes the weights has waited for all before it)
+    if (p.max_blocks <= p.num_selected) grid_dependency_wait();
     const int64_t row = (int64_t)blockIdx.x * p.num_kv_heads + blockIdx.y;
     const int32_t s = (int32_t)(blockIdx.x / p.q_len), j = (int32_t)(blockIdx.x % p.q_len);
     const int32_t blocks = blocks_of(p, context_of(p, s, false), j);
+    for (int32_t i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+    if (tid == 0) {
+        range[0] = 0xffffffffu;
+        range[1] = 0u;
+        gathered = 0;
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    allow_dependent_launch();
     int32_t* out = p.selected + row * p.num_selected;
     if (blocks <= p.num_selected) {
         for (int32_t i = tid; i < p.num_selected; i += kSelThreads) out[i] = i < blocks ? i : -1;
@@ -378,11 +503,6 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             if (i >= m0) f(i, keys[i]);
     };
     uint32_t lo = 0xffffffffu, hi = 0u;
-    if (tid == 0) {
-        range[0] = 0xffffffffu;
-        range[1] = 0u;
-    }
-    __syncthreads();
     each([&](int32_t, uint32_t k) {
         lo = min(lo, k);
         hi = max(hi, k);
@@ -396,13 +516,16 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     __syncthreads();
     lo = range[0];
     hi = range[1];
-    // narrow lo .. hi until all of it is taken, or one value is left; `want` of it are
-    bool all = want == 0;
+    // Narrow lo .. hi until all of it is taken (`all`), few enough of it are left to be ranked
+    // (`rank`), or one value is; `want` of it are taken.
+    bool all = want == 0, rank = false;
     if (all) lo = hi = 0xffffffffu;               // (nothing above, nothing within)
-    while (!all && lo < hi) {
+    for (bool again = false; !all && !rank && lo < hi; again = true) {
         const int32_t shift = max(0, 21 - __clz(hi - lo));
-        for (int32_t i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
+        if (again) {
+            for (int32_t i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+        }
         each([&](int32_t, uint32_t k) {
             if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1);
         });
@@ -427,21 +550,27 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             }
         }
         __syncthreads();
-        const int32_t bin = found[0];
+        const int32_t bin = found[0], here = hist[bin];
         want -= found[1];
-        all = hist[bin] == want;
+        all = here == want;
+        rank = !all && here <= kSelThreads;
         lo += (uint32_t)bin << shift;
         hi = lo + min(hi - lo, (1u << shift) - 1u);      // (lo + a bin may pass 32 bits)
         __syncthreads();
     }
-    // the bits: everything above the range, and the range itself if all of it is taken
+    // the bits: everything above the range, and the range itself if all of it is taken; what is
+    // to be ranked goes to a list, what is equal to bits of its own
+    uint2* const cand = reinterpret_cast<uint2*>(hist);
     auto mark = [&](int32_t i, uint32_t k, bool scored) {
-        const bool here = scored && k >= lo && k <= hi && !(want == 0);
-        const bool in = i < blocks && (!scored || (want > 0 ? k > hi : false) || (here && all));
-        const uint32_t t = __ballot_sync(0xffffffffu, in), e = __ballot_sync(0xffffffffu, here && !all);
-        if (lane == 0 && (i >> 5) < words) {
-            take[i >> 5] = t;
-            tie[i >> 5] = e;
+        const bool here = scored && want > 0 && k >= lo && k <= hi;
+        const bool in = i < blocks && (!scored || (want > 0 && k > hi) || (here && all));
+        const uint32_t t = __ballot_sync(0xffffffffu, in);
+        if (lane == 0 && (i >> 5) < words) take[i >> 5] = t;
+        if (!all && !rank) {
+            const uint32_t e = __ballot_sync(0xffffffffu, here);
+            if (lane == 0 && (i >> 5) < words) tie[i >> 5] = e;
+        } else if (here && rank) {
+            cand[atomicAdd(&gathered, 1)] = make_uint2(k, (uint32_t)i);
         }
     };
 #pragma unroll
@@ -457,13 +586,26 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
         mark(i, scored ? keys[i] : 0u, scored);
     }
     __syncthreads();
+    if (rank) {
+        const int32_t n = gathered;
+        if (tid < n) {
+            const uint2 me = cand[tid];
+            int32_t better = 0;
+            for (int32_t i = 0; i < n; ++i) {
+                const uint2 x = cand[i];
+                better += x.x > me.x || (x.x == me.x && x.y < me.y);
+            }
+            if (better < want) atomicOr(&take[me.y >> 5], 1u << (me.y & 31));
+        }
+        __syncthreads();
+    }
     // of the ties, the first `want`; then the list, word by word
     int32_t ties = 0, at = 0;
     for (int32_t w0 = 0; w0 < words; w0 += kSelThreads) {
         const int32_t w = w0 + tid;
         uint32_t bits = w < words ? take[w] : 0u;
         int32_t total;
-        if (!all) {
+        if (!all && !rank) {
             uint32_t e = w < words ? tie[w] : 0u;
             const int32_t before = ties + scan_cta(__popc(e), buf, &total);
             ties += total;
@@ -477,6 +619,58 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
         for (; bits; bits &= bits - 1u) out[to++] = 32 * w + __ffs(bits) - 1;
     }
 }
+
+// ------------------------------------------------------------------ attention over the selection
+constexpr int kTableWarps = 4;
+
+// A warp per (query token, kv head): its selected blocks that hold tokens it sees, in order, as
+// blocks of the pools with one kv head each, and the tokens in them.  The list has to ascend, so
+// only its last block can end early; entries that do not, or lie outside the context, are left
+// out and flagged.
+__global__ void __launch_bounds__(32 * kTableWarps) sparse_tables_kernel(const SparseParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();      // (after the wait: the attention reads the lengths early)
+    const int32_t lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kTableWarps + (threadIdx.x >> 5);
+    if (row >= (int64_t)p.num_seqs * p.q_len * p.num_kv_heads) return;
+    const int32_t h = (int32_t)(row % p.num_kv_heads);
+    const int32_t q = (int32_t)(row / p.num_kv_heads), s = q / p.q_len, j = q - s * p.q_len;
+    const int64_t cap = min((int64_t)p.max_blocks_per_seq * p.block_size, (int64_t)INT32_MAX);
+    const int32_t l = p.context_lens[s];
+    if ((l < 0 || l > cap) && lane == 0 && h == 0 && j == 0 && p.status) atomicOr(p.status, kDevBadLen);
+    const int32_t seen = max((int32_t)min((int64_t)max(l, 0), cap) - p.q_len + j + 1, 0);
+    const int32_t blocks = seen / p.block_size + (seen % p.block_size != 0);
+    const int32_t* list = p.selected + row * p.num_selected;
+    int32_t* out = p.tables + row * p.num_selected;
+    int32_t count = 0, last = -1;
+    bool bad = false;
+    for (int32_t i0 = 0; i0 < p.num_selected; i0 += 32) {
+        const int32_t i = i0 + lane;
+        int32_t b = i < p.num_selected ? list[i] : -1;
+        // the largest entry before this one, of those within the context (a running maximum:
+        // shifted in from below, a lane's own value leaves it unchanged)
+        int32_t top = b < blocks ? b : -1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_up_sync(0xffffffffu, top, o));
+        const int32_t below = __shfl_up_sync(0xffffffffu, top, 1);
+        const int32_t prev = lane ? max(below, last) : last;
+        const bool keep = b >= 0 && b < blocks && b > prev;
+        bad |= b >= 0 && !keep;
+        const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+        if (keep) {
+            const int32_t phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + b];
+            out[count + __popc(kept & ((1u << lane) - 1u))] =
+                phys >= 0 && phys < p.num_blocks ? phys * p.num_kv_heads + h : -1;
+        }
+        count += __popc(kept);
+        if (kept) last = __shfl_sync(0xffffffffu, b, 31 - __clz(kept));
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0 && p.status) atomicOr(p.status, kDevBadBlock);
+    if (lane == 0) p.arrive[row] = 0;
+    if (lane == 0)
+        p.lens[row] = count == 0 ? 0 : count * p.block_size - (last == blocks - 1 ? blocks * p.block_size - seen : 0);
+}
+
 
 template <class Arg>
 cudaError_t launch_pdl(dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void (*kern)(Arg), const Arg& arg) {
@@ -517,22 +711,31 @@ cudaError_t launch_key_bounds(const BoundsParams& p, BoundsType type, cudaStream
 cudaError_t launch_select_blocks(const SelectParams& p, bool bf16, cudaStream_t stream) {
     using Kern = void (*)(SelectParams);
     const bool one = p.q_len == 1, wide = p.head_size == 128;
-    const Kern kern =
-        bf16 ? (wide ? (one ? (Kern)block_scores_kernel<true, 128, 1> : (Kern)block_scores_kernel<true, 128, 4>)
-                     : (one ? (Kern)block_scores_kernel<true, 64, 1> : (Kern)block_scores_kernel<true, 64, 4>))
-             : (wide ? (one ? (Kern)block_scores_kernel<false, 128, 1> : (Kern)block_scores_kernel<false, 128, 4>)
-                     : (one ? (Kern)block_scores_kernel<false, 64, 1> : (Kern)block_scores_kernel<false, 64, 4>));
     if (p.max_blocks > p.num_selected) {
-        const int32_t groups = kScoreThreads / (2 * p.head_size / 16);
-        const int32_t heads = std::min(p.num_kv_heads, groups);
-        cudaError_t e = launch_pdl(dim3((unsigned)p.num_seqs, (unsigned)((p.max_blocks + p.chunk - 1) / p.chunk),
-                                        (unsigned)((p.num_kv_heads + heads - 1) / heads)),
-                                   dim3(kScoreThreads), 0, stream, kern, p);
+        const Kern weights = bf16 ? (wide ? (Kern)select_weights_kernel<true, 128> : (Kern)select_weights_kernel<true, 64>)
+                                  : (wide ? (Kern)select_weights_kernel<false, 128> : (Kern)select_weights_kernel<false, 64>);
+        const Kern scores = wide ? (one ? (Kern)block_scores_kernel<128, 1> : (Kern)block_scores_kernel<128, 2>)
+                                 : (one ? (Kern)block_scores_kernel<64, 1> : (Kern)block_scores_kernel<64, 2>);
+        const int64_t lanes = (int64_t)p.num_seqs * p.q_len * p.num_kv_heads * (p.head_size / 16);
+        cudaError_t e = launch_pdl(dim3((unsigned)((lanes + kWeightThreads - 1) / kWeightThreads)),
+                                   dim3(kWeightThreads), 0, stream, weights, p);
+        if (e != cudaSuccess) return e;
+        const int32_t heads = std::min(p.num_kv_heads, kScoreThreads / (p.head_size / 16));
+        // two CTAs to an SM, but none with fewer than 32 blocks of the longest contexts
+        const int64_t most = (int64_t)p.num_seqs * ((p.num_kv_heads + heads - 1) / heads) * p.max_blocks;
+        e = launch_pdl(dim3((unsigned)std::max<int64_t>(std::min<int64_t>(2 * p.sms, most / 32), 1)),
+                       dim3(kScoreThreads), 0, stream, scores, p);
         if (e != cudaSuccess) return e;
     }
     const size_t smem = 2 * sizeof(uint32_t) * (size_t)((p.max_blocks + 31) / 32);
     return launch_pdl(dim3((unsigned)(p.num_seqs * p.q_len), (unsigned)p.num_kv_heads), dim3(kSelThreads), smem,
                       stream, select_blocks_kernel, p);
+}
+
+cudaError_t launch_sparse_tables(const SparseParams& p, cudaStream_t stream) {
+    const int64_t rows = (int64_t)p.num_seqs * p.q_len * p.num_kv_heads;
+    return launch_pdl(dim3((unsigned)((rows + kTableWarps - 1) / kTableWarps)), dim3(32 * kTableWarps), 0, stream,
+                      sparse_tables_kernel, p);
 }
 
 }  // namespace pa

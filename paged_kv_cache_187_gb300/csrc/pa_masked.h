@@ -6,6 +6,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace pa {
@@ -64,25 +65,43 @@ struct SelectParams {
     int32_t block_size, num_blocks, max_context_len;
     int32_t num_selected, num_first, num_last;
     int32_t max_blocks;                     // blocks of the longest context
-    int32_t chunk;                          // blocks per CTA of the scores
+    int32_t sms;
     uint32_t* keys;                         // [S * q_len][Hkv][max_blocks] ordered scores
+    uint32_t* weights;                      // [S * q_len][Hkv][D / 16][16] pairs of 16-bit weights
     int32_t* status;
 };
 cudaError_t launch_select_blocks(const SelectParams& p, bool bf16, cudaStream_t stream);
-// Blocks per CTA of the scores, at most (their table entries sit in shared memory).
-constexpr int32_t kMaxScoreChunk = 256;
+// Blocks that a CTA of the scores takes at a time (their table entries sit in shared memory).
+constexpr int32_t kMaxScoreChunk = 512;
 // Longest row of blocks that the selection's bitmaps in shared memory hold.
 constexpr int32_t kMaxSelectBlocks = 1 << 17;
 
-// The selected blocks as a decode of its own: every (query token, kv head) becomes a sequence of
-// one kv head, over pools seen as num_blocks * num_kv_heads blocks of one kv head.
+// The selected blocks as a decode of its own: every (query token, kv head) is a row with a table of
+// its blocks, over pools seen as num_blocks * num_kv_heads blocks of one kv head.
 struct SparseParams {
     const int32_t *selected, *block_tables, *context_lens;
     int32_t max_blocks_per_seq, num_seqs, q_len, num_kv_heads, block_size, num_blocks, num_selected;
     int32_t* tables;                        // [S * q_len * Hkv][num_selected]
-    int32_t* lens;                          // [S * q_len * Hkv]
+    int32_t* lens;                          // [S * q_len * Hkv] tokens of the row
+    int32_t* arrive;                        // [S * q_len * Hkv] finished parts of the row
     int32_t* status;
 };
 cudaError_t launch_sparse_tables(const SparseParams& p, cudaStream_t stream);
+
+// What a row costs beside its tiles (its query, its first tile's wait, its output), in tiles.
+constexpr int32_t kSparseRowCost = 2;
+// Shortest share of the work worth a CTA of its own, in tiles.
+constexpr int32_t kSparseMinShare = 8;
+
+// The attention: `ctas` CTAs, or, for 0, the CTAs per SM in *per_sm and no launch.
+struct DecodeParams;
+cudaError_t launch_sparse_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
+                               const SparseParams& sp, int32_t head_size, int32_t ctas,
+                               cudaStream_t stream, int32_t* per_sm);
+cudaError_t launch_sparse_f16(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
+                              const SparseParams& sp, int32_t head_size, int32_t ctas,
+                              cudaStream_t stream, int32_t* per_sm);
+cudaError_t launch_sparse_fp8(bool q_bf16, const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
+                              const SparseParams& sp, int32_t ctas, cudaStream_t stream, int32_t* per_sm);
 
 }  // namespace pa

@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/pa.h"
@@ -172,11 +173,30 @@ pa_status pa_key_bounds(int8_t* bounds, float* bound_steps, const void* key_cach
     return ok();
 }
 
+}  // extern "C"
+
+namespace {
+
+// The weights of every row (query token and kv head; head_size 128 at most), then its scores.
+struct SelectWorkspace {
+    size_t weights, keys, total;
+};
+SelectWorkspace select_workspace(int64_t rows, int32_t blocks) {
+    SelectWorkspace L;
+    L.weights = 0;
+    L.keys = align256((size_t)rows * 2 * 128 * sizeof(int16_t));
+    L.total = L.keys + align256(sizeof(uint32_t) * (size_t)rows * blocks);
+    return L;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t pa_select_blocks_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_kv_heads,
                                        int32_t block_size, int32_t max_context_len) {
     if (num_seqs < 0 || q_len <= 0 || num_kv_heads <= 0 || block_size <= 0 || max_context_len < 0) return 0;
-    const size_t blocks = (size_t)max_context_len / block_size + 1;
-    return align256(sizeof(uint32_t) * (size_t)num_seqs * q_len * num_kv_heads * blocks);
+    return select_workspace((int64_t)num_seqs * q_len * num_kv_heads, max_context_len / block_size + 1).total;
 }
 
 pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* bounds,
@@ -214,10 +234,10 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
         return fail(PA_ERR_INVALID_ARG, "select_blocks: null pointer");
     if (!aligned16(query) || !aligned16(bounds))
         return fail(PA_ERR_INVALID_ARG, "select_blocks: buffers must be 16-byte aligned");
-    const size_t need = sizeof(uint32_t) * (size_t)num_seqs * q_len * num_kv_heads * blocks;
+    const SelectWorkspace L = select_workspace((int64_t)num_seqs * q_len * num_kv_heads, blocks);
     if (blocks > num_selected) {
-        if (!workspace || workspace_bytes < need)
-            return fail(PA_ERR_WORKSPACE, "select_blocks: workspace of %zu bytes, need %zu", workspace_bytes, need);
+        if (!workspace || workspace_bytes < L.total)
+            return fail(PA_ERR_WORKSPACE, "select_blocks: workspace of %zu bytes, need %zu", workspace_bytes, L.total);
         if (reinterpret_cast<uintptr_t>(workspace) & 255u)
             return fail(PA_ERR_INVALID_ARG, "select_blocks: workspace must be 256-byte aligned");
     }
@@ -243,10 +263,15 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
     p.num_first = num_first;
     p.num_last = num_last;
     p.max_blocks = blocks;
-    p.chunk = 64;
-    p.keys = static_cast<uint32_t*>(workspace);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "select_blocks: device");
+    p.sms = sms;
+    p.weights = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.weights);
+    p.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.keys);
     p.status = status_dev;
-    const cudaError_t e = pa::launch_select_blocks(p, dtype == PA_BF16, (cudaStream_t)stream);
+    e = pa::launch_select_blocks(p, dtype == PA_BF16, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "select_blocks launch");
     return ok();
 }
@@ -255,19 +280,64 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
 
 namespace {
 
-// The workspace of the attention over selected blocks: the rows' tables and lengths, then the
-// decode's own.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                   CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// A pool as a matrix of rows; a box is 128 bytes of a block's rows.
+pa_status encode_pool(CUtensorMap* map, const void* pool, int64_t rows, int32_t head_size, int32_t block_size,
+                      bool kv8) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const int32_t elem = kv8 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)head_size, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)head_size * elem};
+    const cuuint32_t box[2] = {128u / (cuuint32_t)elem, (cuuint32_t)block_size}, ones[2] = {1u, 1u};
+    const CUresult r = fn(map, kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                          const_cast<void*>(pool), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return PA_OK;
+}
+
+// CTAs that the workspace has room for.
+constexpr int32_t kSparseMaxCtas = 1024;
+
+// The workspace of the attention over selected blocks: the rows' tables, lengths and counters, and
+// the partial results, a slot for every step from a row to the next and from a CTA to the next.
 struct SparseWorkspace {
-    size_t tables, lens, decode, total;
+    size_t tables, lens, arrive, part_ml, part_acc, total;
 };
-SparseWorkspace sparse_workspace(int64_t rows, int32_t group, int32_t head_size, int32_t block_size,
-                                 int32_t num_selected) {
+SparseWorkspace sparse_workspace(int64_t rows, int32_t group, int32_t head_size, int32_t num_selected) {
     SparseWorkspace L;
-    L.tables = 0;
-    L.lens = align256(sizeof(int32_t) * (size_t)rows * num_selected);
-    L.decode = L.lens + align256(sizeof(int32_t) * (size_t)rows);
-    L.total = L.decode + pa_decode_auto_workspace_size((int32_t)rows, group, 1, head_size, block_size,
-                                                       num_selected * block_size);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align256(off + bytes);
+        return at;
+    };
+    L.tables = take(sizeof(int32_t) * (size_t)rows * num_selected);
+    L.lens = take(sizeof(int32_t) * (size_t)rows);
+    L.arrive = take(sizeof(int32_t) * (size_t)rows);
+    const size_t slots = (size_t)rows + kSparseMaxCtas;
+    L.part_ml = take(sizeof(float2) * slots * group);
+    L.part_acc = take(sizeof(float) * slots * group * head_size);
+    L.total = off;
     return L;
 }
 
@@ -314,7 +384,7 @@ pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* st
         return fail(PA_ERR_INVALID_ARG, "decode_sparse: null pointer");
     if (!aligned16(a.out) || !aligned16(a.query) || !aligned16(a.key_cache) || !aligned16(a.value_cache))
         return fail(PA_ERR_INVALID_ARG, "decode_sparse: device buffers must be 16-byte aligned");
-    const SparseWorkspace L = sparse_workspace(rows, group, a.head_size, a.block_size, a.num_selected);
+    const SparseWorkspace L = sparse_workspace(rows, group, a.head_size, a.num_selected);
     if (!ws || ws_bytes < L.total)
         return fail(PA_ERR_WORKSPACE, "decode_sparse: workspace of %zu bytes, need %zu", ws_bytes, L.total);
     if (reinterpret_cast<uintptr_t>(ws) & 255u)
@@ -334,18 +404,50 @@ pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* st
     p.num_selected = a.num_selected;
     p.tables = reinterpret_cast<int32_t*>(w + L.tables);
     p.lens = reinterpret_cast<int32_t*>(w + L.lens);
+    p.arrive = reinterpret_cast<int32_t*>(w + L.arrive);
     p.status = status;
-    const cudaError_t e = pa::launch_sparse_tables(p, stream);
+    // the decode's view: a sequence of one kv head per row
+    pa::DecodeParams d;
+    std::memset(&d, 0, sizeof(d));
+    d.out = a.out;
+    d.q = a.query;
+    d.num_seqs = (int32_t)rows;
+    d.num_q_heads = d.group = d.rows = group;
+    d.num_kv_heads = 1;
+    d.num_blocks = a.num_blocks * a.num_kv_heads;
+    d.block_size = a.block_size;
+    d.scale_log2 = a.scale * (a.kv8 ? a.k_scale : 1.f) * 1.4426950408889634f;
+    d.out_scale = a.kv8 ? a.v_scale : 1.f;
+    d.q_len = d.row_chunks = d.row_groups = 1;
+    d.arrive = p.arrive;
+    d.part_ml = reinterpret_cast<float2*>(w + L.part_ml);
+    d.part_acc = reinterpret_cast<float*>(w + L.part_acc);
+    d.status = status;
+    CUtensorMap km, vm;
+    pa_status st = encode_pool(&km, a.key_cache, pool_rows, a.head_size, a.block_size, a.kv8);
+    if (st == PA_OK) st = encode_pool(&vm, a.value_cache, pool_rows, a.head_size, a.block_size, a.kv8);
+    if (st != PA_OK) return st;
+    const bool bf16 = a.dtype == PA_BF16;
+    auto launch = [&](int32_t ctas, int32_t* per_sm) {
+        return a.kv8  ? pa::launch_sparse_fp8(bf16, km, vm, d, p, ctas, stream, per_sm)
+               : bf16 ? pa::launch_sparse_bf16(km, vm, d, p, a.head_size, ctas, stream, per_sm)
+                      : pa::launch_sparse_f16(km, vm, d, p, a.head_size, ctas, stream, per_sm);
+    };
+    int dev = 0, sms = 0;
+    int32_t per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = launch(0, &per_sm);
+    if (e != cudaSuccess) return cuda_fail(e, "decode_sparse: device");
+    if (per_sm <= 0) return fail(PA_ERR_CUDA, "decode_sparse: kernel cannot be resident on this device");
+    const int32_t tile_blocks = a.kv8 && a.block_size == 16 ? 2 : 1;
+    const int64_t cost = rows * ((a.num_selected + tile_blocks - 1) / tile_blocks + pa::kSparseRowCost);
+    const int32_t ctas = (int32_t)std::max<int64_t>(
+        std::min<int64_t>(std::min(per_sm * sms, kSparseMaxCtas), cost / pa::kSparseMinShare), 1);
+    e = pa::launch_sparse_tables(p, stream);
+    if (e == cudaSuccess) e = launch(ctas, nullptr);
     if (e != cudaSuccess) return cuda_fail(e, "decode_sparse launch");
-    const int32_t tokens = a.num_selected * a.block_size, blocks = a.num_blocks * a.num_kv_heads;
-    if (a.kv8)
-        return pa_decode_fp8(a.out, a.query, a.key_cache, a.value_cache, p.tables, a.num_selected, p.lens,
-                             (int32_t)rows, group, 1, a.head_size, a.block_size, blocks, tokens, a.scale,
-                             a.k_scale, a.v_scale, a.dtype, 0, 0, w + L.decode, L.total - L.decode, status,
-                             (pa_stream)stream);
-    return pa_decode_auto(a.out, a.query, a.key_cache, a.value_cache, p.tables, a.num_selected, p.lens,
-                          (int32_t)rows, group, 1, a.head_size, a.block_size, blocks, tokens, a.scale, a.dtype,
-                          w + L.decode, L.total - L.decode, status, (pa_stream)stream);
+    return ok();
 }
 
 }  // namespace
@@ -360,7 +462,7 @@ size_t pa_decode_sparse_workspace_size(int32_t num_seqs, int32_t q_len, int32_t 
         (int64_t)num_seqs * q_len * num_kv_heads > (1 << 24) || (int64_t)num_selected * block_size > (1 << 24))
         return 0;
     return sparse_workspace((int64_t)num_seqs * q_len * num_kv_heads, num_q_heads / num_kv_heads, head_size,
-                            block_size, num_selected).total;
+                            num_selected).total;
 }
 
 pa_status pa_decode_sparse(void* out, const void* query, const void* key_cache, const void* value_cache,
