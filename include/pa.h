@@ -664,8 +664,8 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
  * A row of selected ascends; -1 entries are skipped, and entries that do not ascend or lie outside
  * the context are left out and flagged PA_DEVERR_BAD_BLOCK.  A row without tokens is a zero row.
  * Other arguments, limits and accuracy as for pa_decode_auto (num_seqs * q_len * num_kv_heads at
- * most 2^24, num_selected * block_size too).  `workspace` as for pa_decode_v2, of
- * pa_decode_sparse_workspace_size bytes (0 for bad sizes). */
+ * most 2^24, num_selected * block_size too).  The present kernels need no workspace: the size is 0
+ * and `workspace` may be NULL. */
 size_t pa_decode_sparse_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
                                        int32_t num_kv_heads, int32_t head_size, int32_t block_size,
                                        int32_t num_selected);

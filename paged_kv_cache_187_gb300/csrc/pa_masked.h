@@ -76,24 +76,22 @@ constexpr int32_t kMaxScoreChunk = 512;
 // Longest row of blocks that the selection's bitmaps in shared memory hold.
 constexpr int32_t kMaxSelectBlocks = 1 << 17;
 
-// The selected blocks as a decode of its own: every (query token, kv head) is a row with a table of
-// its blocks, over pools seen as num_blocks * num_kv_heads blocks of one kv head.
+// The attention over selected blocks.  Every (query token, kv head) is a row: a sequence of one kv
+// head, over pools seen as num_blocks * num_kv_heads blocks of one kv head.
 struct SparseParams {
     const int32_t *selected, *block_tables, *context_lens;
     int32_t max_blocks_per_seq, num_seqs, q_len, num_kv_heads, block_size, num_blocks, num_selected;
-    int32_t* tables;                        // [S * q_len * Hkv][num_selected]
-    int32_t* lens;                          // [S * q_len * Hkv] tokens of the row
-    int32_t* arrive;                        // [S * q_len * Hkv] finished parts of the row
+    int32_t cluster;                        // CTAs per row
+    int32_t short_ring;                     // less of them on its way per CTA, more CTAs to an SM
     int32_t* status;
 };
-cudaError_t launch_sparse_tables(const SparseParams& p, cudaStream_t stream);
+// List entries that a CTA translates at a time.
+constexpr int32_t kSparseEntries = 512;
+// A CTA of a cluster takes at least this many tiles of its row.
+constexpr int32_t kSparseTiles = 4;
+constexpr int32_t kSparseMaxCluster = 16;
 
-// What a row costs beside its tiles (its query, its first tile's wait, its output), in tiles.
-constexpr int32_t kSparseRowCost = 2;
-// Shortest share of the work worth a CTA of its own, in tiles.
-constexpr int32_t kSparseMinShare = 8;
-
-// The attention: `ctas` CTAs, or, for 0, the CTAs per SM in *per_sm and no launch.
+// `ctas` CTAs, or, for 0, the CTAs per SM in *per_sm and no launch.
 struct DecodeParams;
 cudaError_t launch_sparse_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
                                const SparseParams& sp, int32_t head_size, int32_t ctas,

@@ -315,32 +315,6 @@ pa_status encode_pool(CUtensorMap* map, const void* pool, int64_t rows, int32_t 
     return PA_OK;
 }
 
-// CTAs that the workspace has room for.
-constexpr int32_t kSparseMaxCtas = 1024;
-
-// The workspace of the attention over selected blocks: the rows' tables, lengths and counters, and
-// the partial results, a slot for every step from a row to the next and from a CTA to the next.
-struct SparseWorkspace {
-    size_t tables, lens, arrive, part_ml, part_acc, total;
-};
-SparseWorkspace sparse_workspace(int64_t rows, int32_t group, int32_t head_size, int32_t num_selected) {
-    SparseWorkspace L;
-    size_t off = 0;
-    auto take = [&](size_t bytes) {
-        const size_t at = off;
-        off = align256(off + bytes);
-        return at;
-    };
-    L.tables = take(sizeof(int32_t) * (size_t)rows * num_selected);
-    L.lens = take(sizeof(int32_t) * (size_t)rows);
-    L.arrive = take(sizeof(int32_t) * (size_t)rows);
-    const size_t slots = (size_t)rows + kSparseMaxCtas;
-    L.part_ml = take(sizeof(float2) * slots * group);
-    L.part_acc = take(sizeof(float) * slots * group * head_size);
-    L.total = off;
-    return L;
-}
-
 struct SparseArgs {
     void* out;
     const void *query, *key_cache, *value_cache;
@@ -354,7 +328,7 @@ struct SparseArgs {
     bool kv8;
 };
 
-pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* status, cudaStream_t stream) {
+pa_status run_sparse(const SparseArgs& a, int32_t* status, cudaStream_t stream) {
     if (a.num_seqs < 0 || a.q_len <= 0 || a.num_q_heads <= 0 || a.num_kv_heads <= 0 || a.num_blocks <= 0 ||
         a.max_blocks_per_seq <= 0 || a.num_selected <= 0)
         return fail(PA_ERR_INVALID_ARG, "decode_sparse: sizes must be positive (num_seqs >= 0)");
@@ -384,12 +358,6 @@ pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* st
         return fail(PA_ERR_INVALID_ARG, "decode_sparse: null pointer");
     if (!aligned16(a.out) || !aligned16(a.query) || !aligned16(a.key_cache) || !aligned16(a.value_cache))
         return fail(PA_ERR_INVALID_ARG, "decode_sparse: device buffers must be 16-byte aligned");
-    const SparseWorkspace L = sparse_workspace(rows, group, a.head_size, a.num_selected);
-    if (!ws || ws_bytes < L.total)
-        return fail(PA_ERR_WORKSPACE, "decode_sparse: workspace of %zu bytes, need %zu", ws_bytes, L.total);
-    if (reinterpret_cast<uintptr_t>(ws) & 255u)
-        return fail(PA_ERR_INVALID_ARG, "decode_sparse: workspace must be 256-byte aligned");
-    uint8_t* w = static_cast<uint8_t*>(ws);
     pa::SparseParams p;
     std::memset(&p, 0, sizeof(p));
     p.selected = a.selected;
@@ -402,9 +370,6 @@ pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* st
     p.block_size = a.block_size;
     p.num_blocks = a.num_blocks;
     p.num_selected = a.num_selected;
-    p.tables = reinterpret_cast<int32_t*>(w + L.tables);
-    p.lens = reinterpret_cast<int32_t*>(w + L.lens);
-    p.arrive = reinterpret_cast<int32_t*>(w + L.arrive);
     p.status = status;
     // the decode's view: a sequence of one kv head per row
     pa::DecodeParams d;
@@ -419,9 +384,6 @@ pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* st
     d.scale_log2 = a.scale * (a.kv8 ? a.k_scale : 1.f) * 1.4426950408889634f;
     d.out_scale = a.kv8 ? a.v_scale : 1.f;
     d.q_len = d.row_chunks = d.row_groups = 1;
-    d.arrive = p.arrive;
-    d.part_ml = reinterpret_cast<float2*>(w + L.part_ml);
-    d.part_acc = reinterpret_cast<float*>(w + L.part_acc);
     d.status = status;
     CUtensorMap km, vm;
     pa_status st = encode_pool(&km, a.key_cache, pool_rows, a.head_size, a.block_size, a.kv8);
@@ -434,18 +396,38 @@ pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* st
                       : pa::launch_sparse_f16(km, vm, d, p, a.head_size, ctas, stream, per_sm);
     };
     int dev = 0, sms = 0;
-    int32_t per_sm = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = launch(0, &per_sm);
+    // A cluster per row, as large as leaves every CTA a few tiles and all of them a place: up to 3.4
+    // CTAs to an SM, 2.6 in clusters of 16, which need room in one part of the chip.  (us a call, 8 kv
+    // heads: 8 rows of 256 blocks 16.1 in clusters of 8 and 12.6 of 16; 32 of 64 blocks 8.7 and 12.2;
+    // 64 of 256 blocks 28.8 in clusters of 4 and 26.6 of 8; 152 of 128 30 in twos and 41 in fours.)
+    const int64_t tile_blocks = a.kv8 && a.block_size == 16 ? 2 : 1;
+    const int64_t tiles = (a.num_selected + tile_blocks - 1) / tile_blocks;
+    p.cluster = 1;
+    for (int32_t n = 2; n <= pa::kSparseMaxCluster; n *= 2)
+        if (10 * rows * n <= (int64_t)(n > 8 ? 26 : 34) * sms && tiles >= (int64_t)n * pa::kSparseTiles) p.cluster = n;
+    if (p.cluster == 1) {
+        // Whole rows: of the two rings, the one whose CTAs leave fewer places empty in their last turn
+        // (640 rows of 128 blocks, bf16: 133 us with the long ring, whose 608 places take two turns,
+        // and 99 with the short one; 384 rows 63 and 69; 1024 rows 154 and 168).
+        double best = 0.;
+        int32_t choice = 0;
+        for (int32_t kind = 0; kind < 2 && e == cudaSuccess; ++kind) {
+            int32_t per_sm = 0;
+            p.short_ring = kind;
+            e = launch(0, &per_sm);
+            const int64_t places = std::max<int64_t>((int64_t)per_sm * sms, 1), turns = (rows + places - 1) / places;
+            const double used = rows <= places ? 1. : (double)rows / (double)(turns * places);
+            if (used > best) {
+                best = used;
+                choice = kind;
+            }
+        }
+        p.short_ring = choice;
+    }
     if (e != cudaSuccess) return cuda_fail(e, "decode_sparse: device");
-    if (per_sm <= 0) return fail(PA_ERR_CUDA, "decode_sparse: kernel cannot be resident on this device");
-    const int32_t tile_blocks = a.kv8 && a.block_size == 16 ? 2 : 1;
-    const int64_t cost = rows * ((a.num_selected + tile_blocks - 1) / tile_blocks + pa::kSparseRowCost);
-    const int32_t ctas = (int32_t)std::max<int64_t>(
-        std::min<int64_t>(std::min(per_sm * sms, kSparseMaxCtas), cost / pa::kSparseMinShare), 1);
-    e = pa::launch_sparse_tables(p, stream);
-    if (e == cudaSuccess) e = launch(ctas, nullptr);
+    e = launch((int32_t)(rows * p.cluster), nullptr);
     if (e != cudaSuccess) return cuda_fail(e, "decode_sparse launch");
     return ok();
 }
@@ -454,15 +436,9 @@ pa_status run_sparse(const SparseArgs& a, void* ws, size_t ws_bytes, int32_t* st
 
 extern "C" {
 
-size_t pa_decode_sparse_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
-                                       int32_t num_kv_heads, int32_t head_size, int32_t block_size,
-                                       int32_t num_selected) {
-    if (num_seqs < 0 || q_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
-        block_size <= 0 || num_selected <= 0 || num_q_heads % num_kv_heads ||
-        (int64_t)num_seqs * q_len * num_kv_heads > (1 << 24) || (int64_t)num_selected * block_size > (1 << 24))
-        return 0;
-    return sparse_workspace((int64_t)num_seqs * q_len * num_kv_heads, num_q_heads / num_kv_heads, head_size,
-                            num_selected).total;
+// The parts of a row meet in shared memory: no call needs a workspace.
+size_t pa_decode_sparse_workspace_size(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) {
+    return 0;
 }
 
 pa_status pa_decode_sparse(void* out, const void* query, const void* key_cache, const void* value_cache,
@@ -475,7 +451,9 @@ pa_status pa_decode_sparse(void* out, const void* query, const void* key_cache, 
     const SparseArgs a{out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
                        selected, num_selected, num_seqs, q_len, num_q_heads, num_kv_heads, head_size,
                        block_size, num_blocks, scale, 1.f, 1.f, dtype, false};
-    return run_sparse(a, workspace, workspace_bytes, status_dev, (cudaStream_t)stream);
+    (void)workspace;
+    (void)workspace_bytes;
+    return run_sparse(a, status_dev, (cudaStream_t)stream);
 }
 
 pa_status pa_decode_sparse_fp8(void* out, const void* query, const void* key_cache, const void* value_cache,
@@ -489,7 +467,9 @@ pa_status pa_decode_sparse_fp8(void* out, const void* query, const void* key_cac
     const SparseArgs a{out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
                        selected, num_selected, num_seqs, q_len, num_q_heads, num_kv_heads, head_size,
                        block_size, num_blocks, scale, k_scale, v_scale, dtype, true};
-    return run_sparse(a, workspace, workspace_bytes, status_dev, (cudaStream_t)stream);
+    (void)workspace;
+    (void)workspace_bytes;
+    return run_sparse(a, status_dev, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,21 +1,30 @@
 // pa_sparse.cuh -- attention over selected blocks of the paged cache: for each query token and kv
 // head (a row) the softmax over the tokens of its selected blocks.
 //
-// The consumers are the decode's (pa_decode.cuh: tiles of one or two blocks, online softmax on
-// mma.sync for grouped heads and 8-bit caches, on CUDA cores for single ones, partial states joined
-// by the last part to finish); what differs is where the work comes from.  Rows are short and many
-// of one length, so instead of whole rows or partitions of one size, handed out as they are asked
-// for, all rows' tiles are laid end to end and cut into equal slices, one per CTA: every CTA streams
-// the same number of bytes without a pause, and a row is cut in two or three pieces at most where
-// there are more rows than CTAs.  (48 x 8 rows of 2048 tokens, 402 MB: 83 us with partitions, see
-// below for the slices.)  The slices follow from the context lengths alone, so no plan is made: each
-// CTA sums the lengths while the kernel before it still runs.
+// Rows are short (64 blocks of 16 tokens are 512 KB of K and V) and mostly of one length, and a call
+// has a few of them or some hundreds; what it costs beside the bytes is latency: launches, dependent
+// loads (list -> block table -> tiles) and the round trips where the parts of a row meet.  So there
+// is one launch and no plan, and a row belongs to a cluster of 1 to 16 CTAs: each translates its
+// piece of the list (pa_sparse_device.cuh) and streams its tiles through a ring in shared memory by
+// TMA, the consumers being the decode's (pa_decode.cuh: tiles of one or two blocks, online softmax
+// on mma.sync for grouped heads and 8-bit caches, on CUDA cores for single ones); the parts meet in
+// shared memory, where every CTA joins its share of the row's elements out of the others'.
+//
+// Measured (device time a call, calls back to back; 8 kv heads of 128, floors at the measured copy
+// bandwidth in brackets).  One sequence, 64 blocks of 16 tokens a row, 32 query heads: 7.0 us [0.6];
+// with the decode over tables that a kernel of its own made, 20.4.  48 sequences, 128 blocks: 63.5
+// [59.3], where the decode's partitions took 83, and slices of one size for every CTA, cut through
+// the rows and joined through memory, 71: CTAs with the same bytes finish up to 13 us apart, and
+// every joint is a round trip of 3-6 us.  Below the launch's 3 us and the first tile's 3 what bounds
+// it is HBM from some 300 CTAs on, and the bytes that the CTAs have on their way below that.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 
 #include "pa_decode_family.cuh"
 #include "pa_masked.h"
+#include "pa_sparse_device.cuh"
 
 namespace pa {
 
@@ -26,13 +35,108 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
 }
 
 template <class C>
+struct alignas(1024) SparseSmem {
+    // a ring of K and V tiles; once they are all consumed, the consumers' states in its place
+    union {
+        uint8_t kv[C::NSTAGE][2][C::TILE_BYTES];
+        struct {
+            float sums[C::HCAP * C::D];
+            float states[C::NCONS > 1 ? C::NCONS - 1 : 1][C::NSTATE * 32];
+        };
+    };
+    alignas(128) uint8_t q[C::HCAP * C::D * 2];
+    alignas(16) float pbuf[C::kMma ? 1 : C::NCONS][C::kMma ? 1 : C::HCAP][C::kMma ? 1 : C::BS];
+    alignas(16) float2 ml[C::HCAP];           // (reference, weight sum) of this CTA's part
+    uint64_t full[C::NSTAGE], empty[C::NSTAGE], qfull, listed;
+    uint32_t issued[C::NSTAGE], consumed[C::NSTAGE];
+    int32_t blocks[kSparseEntries + C::TB - 1];
+    int32_t tokens, q_read;
+    volatile int32_t abort;
+};
+template <class C>
+constexpr size_t sparse_smem_bytes() {
+    return sizeof(SparseSmem<C>) + 1024;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster; what was written before is seen after.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+// A consumer's state (unnormalised sums, references, weight sums) into shared memory, [head][dim].
+template <class C>
+__device__ __forceinline__ void stage_state(const MmaConsumer<C>& cons, float* ostage, float2* ml, int nrows, int lane) {
+    using M = MmaConsumer<C>;
+#pragma unroll
+    for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float v = cons.l[nt][j];
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            const int h = nt * 8 + 2 * lane + j;
+            if (lane < 4 && h < nrows) ml[h] = make_float2(cons.m[nt][j], v);
+        }
+#pragma unroll
+    for (int i = 0; i < M::KS; ++i)
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int h = nt * 8 + 2 * (lane & 3) + (r & 1);
+                ostage[h * C::D + M::out_dim(i, lane, r)] = cons.acc[i][nt][r];
+            }
+}
+template <class C>
+__device__ __forceinline__ void stage_state(const CoreConsumer<C>& cons, float* ostage, float2* ml, int nrows, int lane) {
+    constexpr int DPL = C::D / 32;
+#pragma unroll
+    for (int h = 0; h < C::HCAP; ++h) {
+        float v = cons.l[h];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        if (lane == 0 && h < nrows) ml[h] = make_float2(cons.m[h], v);
+#pragma unroll
+        for (int j = 0; j < DPL; ++j) ostage[h * C::D + lane * DPL + j] = cons.acc[h][j];
+    }
+}
+
+template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
-    sparse_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                         const DecodeParams p, const SparseParams sp) {
+    sparse_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const DecodeParams p, const SparseParams sp) {
     extern __shared__ uint8_t smem_raw[];
-    DecodeSmem<C>& sm = *reinterpret_cast<DecodeSmem<C>*>(
+    SparseSmem<C>& sm = *reinterpret_cast<SparseSmem<C>*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t parts = sp.cluster;
+    const int32_t rank = parts > 1 ? (int32_t)cluster_rank() : 0;
+    const int32_t row = (int32_t)blockIdx.x / parts;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NSTAGE; ++i) {
             mbar_init(&sm.full[i], 1);
@@ -40,208 +144,76 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             sm.issued[i] = 0;
             sm.consumed[i] = 0;
         }
-        mbar_init(&sm.xfree, 1);
-        for (int i = 0; i < C::NQ; ++i) {
-            mbar_init(&sm.qfull[i], 1);
-            mbar_init(&sm.qempty[i], C::NCONS);
-            sm.qissued[i] = 0;
-            sm.qconsumed[i] = 0;
-        }
-        sm.abort = 0;
+        mbar_init(&sm.qfull, 1);
+        mbar_init(&sm.listed, 1);
+        sm.abort = sm.q_read = 0;
         fence_barrier_init();
         prefetch_tensor_map(&kmap);
         prefetch_tensor_map(&vmap);
     }
+    if (threadIdx.x < C::HCAP) sm.ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
     __syncthreads();
+    grid_dependency_wait();
+    allow_dependent_launch();      // (what follows waits for this kernel before it writes)
+    auto timed_out = [&]() {
+        if (lane == 0) {
+            flag_error(p.status, PA_DEVERR_TIMEOUT_);
+            sm.abort = 1;
+        }
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        const int32_t Hkv = sp.num_kv_heads, QL = sp.q_len, S = sp.num_seqs;
-        const int32_t cap = (int32_t)min((int64_t)sp.max_blocks_per_seq * C::PBS, (int64_t)INT32_MAX);
-        auto len_of = [&](int32_t s) { return min(max(sp.context_lens[s], 0), cap); };
-        // tiles of a row of query token j, at most: what the context holds, up to the list's length
-        auto tiles_of = [&](int32_t len, int32_t j) {
-            const int32_t seen = max(len - QL + j + 1, 0);
-            const int32_t blocks = min(seen / C::PBS + (seen % C::PBS != 0), sp.num_selected);
-            return (blocks + C::TB - 1) / C::TB;
-        };
-        auto cost_of = [&](int32_t s) {      // of a sequence's rows
-            int64_t sum = 0;
-            if (s < S) {
-                const int32_t len = len_of(s);
-                for (int32_t j = 0; j < QL; ++j) sum += tiles_of(len, j) + kSparseRowCost;
-            }
-            return sum * Hkv;
-        };
-        // Sequences s0 .. s0 + 31, one per lane: cost, and running sum.
-        int64_t own = 0, upto = 0;
-        auto sequences = [&](int32_t s0) {
-            own = upto = cost_of(s0 + lane);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
-            return __shfl_sync(0xffffffffu, upto, 31);
-        };
-        int64_t total = 0;
-        for (int32_t s0 = 0; s0 < S; s0 += 32) total += sequences(s0);
-        const int64_t G = gridDim.x;
-        const int64_t lo = total * (int64_t)blockIdx.x / G, hi = total * ((int64_t)blockIdx.x + 1) / G;
-        auto cta_at = [&](int64_t x) { return (int32_t)(((x + 1) * G - 1) / total); };
-        // the row that `lo` is in: sequence, query token, kv head, and where its costs begin
-        int32_t s = 0, j = 0, h = 0, len = 0, T = 0;
-        int64_t base = 0;
-        {
-            int64_t before = 0;
-            for (int32_t s0 = 0; s0 < S; s0 += 32) {
-                if (S > 32) sequences(s0);
-                const uint32_t past = __ballot_sync(0xffffffffu, before + upto > lo);
-                if (past) {
-                    const int32_t l = __ffs(past) - 1;
-                    s = s0 + l;
-                    base = before + __shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, own, l);
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, upto, 31);
-            }
-            len = len_of(s);
-            for (j = 0; j < QL; ++j) {
-                T = tiles_of(len, j);
-                const int64_t c = (int64_t)(T + kSparseRowCost) * Hkv;
-                if (base + c > lo) break;
-                base += c;
-            }
-            h = (int32_t)((lo - base) / (T + kSparseRowCost));
-            base += (int64_t)h * (T + kSparseRowCost);
+        if (lane == 0) {
+            const uint32_t qbytes = (uint32_t)(p.group * C::D * 2);
+            mbar_arrive_expect_tx(&sm.qfull, qbytes);
+            bulk_load(sm.q, reinterpret_cast<const uint8_t*>(p.q) + (size_t)row * p.group * C::D * 2, qbytes,
+                      &sm.qfull);
         }
-        // what the tables kernel writes (and with it everything before it)
-        grid_dependency_wait();
-        // The next unit of this slice, in *u (seq -1: none): the row at the cursor, or one after it,
-        // with the tiles that this slice has of it.  A row belongs to the slices that hold its tiles;
-        // one without tiles to the slice where it begins.
-        auto next_unit = [&](UnitDesc& u) {
-            u.seq = -1;
-            u.kvh = u.tok0 = u.tok1 = u.row0 = u.len = 0;
-            u.pslot = -1;
-            u.pbase = 0;
-            u.nparts = 1;
-            u.nrows = p.group;
-            u.pad[0] = u.pad[1] = 0;
-            while (base < hi) {
-                const int64_t first = base + kSparseRowCost;
-                const int32_t t0 = (int32_t)min(max(lo - first, (int64_t)0), (int64_t)T);
-                const int32_t t1 = (int32_t)min(max(hi - first, (int64_t)0), (int64_t)T);
-                const bool here = t1 > t0 || (T == 0 && base >= lo);
-                if (here) {
-                    const int32_t row = (s * QL + j) * Hkv + h;
-                    u.seq = row;
-                    u.tok0 = t0 * C::BS;
-                    u.tok1 = t1 * C::BS;       // (at most: the row's tokens are not known yet)
-                    if (T > 0 && (t0 > 0 || t1 < T)) {
-                        const int32_t a = cta_at(first), b = cta_at(first + T - 1);
-                        u.nparts = b - a + 1;
-                        u.pbase = a + row;     // (slots: a CTA's and its row's number, added)
-                        u.pslot = (int32_t)blockIdx.x + row;
-                    }
-                }
-                // the cursor goes on
-                base += T + kSparseRowCost;
-                if (++h == Hkv) {
-                    h = 0;
-                    if (++j == QL) {
-                        j = 0;
-                        if (++s < S) len = len_of(s);
-                    }
-                    T = tiles_of(len, j);
-                }
-                if (here) return;
-            }
-        };
-        // Table entries b0 .. b0 + 31 of a row, one per lane; those outside the pool become a row
-        // past the tensor map (TMA reads zeros).
-        auto load_blocks = [&](int32_t row, int32_t b0, int32_t n) {
-            int32_t phys = p.num_blocks;
-            if (lane < n) {
-                phys = sp.tables[(size_t)row * sp.num_selected + b0 + lane];
-                if (phys < 0 || phys >= p.num_blocks) {
-                    flag_error(p.status, PA_DEVERR_BAD_BLOCK_);
-                    phys = p.num_blocks;
-                }
-            }
-            return phys;
-        };
-        // the row's tokens, and its first blocks here (all of them in the table are written up to
-        // the row's count; entries past it are not used)
-        auto row_len = [&](const UnitDesc& u) { return u.seq >= 0 ? sp.lens[u.seq] : 0; };
-        auto first_blocks = [&](const UnitDesc& u, int32_t n_tok) {
-            const int32_t b0 = u.tok0 / C::PBS;
-            const int32_t b1 = (min(u.tok1, n_tok) + C::PBS - 1) / C::PBS;
-            return u.seq >= 0 ? load_blocks(u.seq, b0, min(32, b1 - b0)) : 0;
-        };
-        const uint64_t policy = QL > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
-        const uint32_t qbytes = (uint32_t)(p.group * C::D * 2);
-        UnitDesc u, next;
-        next_unit(u);
-        int32_t tokens = row_len(u), phys0 = first_blocks(u, tokens);
-        uint32_t stage = 0, ephase = 1;
-        for (uint32_t it = 0;; ++it) {
-            if (warp_sees_abort(sm.abort)) u.seq = -1;
-            u.tok1 = max(min(u.tok1, tokens), u.tok0);
-            const uint32_t qs = it % C::NQ, qphase = ((it / C::NQ) & 1) ^ 1;
-            bool ok = true;
+        // this CTA's piece of the list, kSparseEntries entries at a time
+        const int32_t K = sp.num_selected;
+        const int32_t per = ((K + parts - 1) / parts + C::TB - 1) / C::TB * C::TB;
+        const int32_t e0 = min(rank * per, K), e1 = min(e0 + per, K);
+        int32_t tokens = 0;
+        auto tell = [&]() {
             if (lane == 0) {
-                ok = mbar_wait(&sm.qempty[qs], qphase);
-                if (ok) {
-                    sm.unit[qs] = u;
-                    if (u.seq < 0) {
-                        mbar_arrive(&sm.qfull[qs]);
-                    } else {
-                        mbar_arrive_expect_tx(&sm.qfull[qs], qbytes);
-                        bulk_load(sm.qbuf[qs],
-                                  reinterpret_cast<const uint8_t*>(p.q) + (size_t)u.seq * p.group * C::D * 2, qbytes,
-                                  &sm.qfull[qs]);
-                        sm.qissued[qs] += 1;
-                    }
-                }
+                sm.tokens = tokens;
+                mbar_arrive(&sm.listed);
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) {
-                if (lane == 0) {
-                    flag_error(p.status, PA_DEVERR_TIMEOUT_);
-                    sm.abort = 1;
-                }
-                break;
+        };
+        if (e1 - e0 > kSparseEntries) {      // the consumers have to know how many tokens there are
+            for (int32_t c0 = e0; c0 < e1; c0 += kSparseEntries)
+                tokens += walk_list(sp, row, c0, min(c0 + kSparseEntries, e1), 0, [](int32_t, int32_t) {}).tokens;
+            tell();
+        }
+        // (blocks that several query tokens read may stay in L2)
+        const uint64_t policy = sp.q_len > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
+        bool out = false, ok = true;
+        uint32_t stage = 0, ephase = 1;
+        int32_t have = 0;                    // blocks of a tile that the next piece completes
+        for (int32_t c0 = e0; ok && c0 < e1; c0 += kSparseEntries) {
+            const int32_t c1 = min(c0 + kSparseEntries, e1);
+            const SparseList list = walk_list(sp, row, c0, c1, p.num_blocks,
+                                              [&](int32_t i, int32_t b) { sm.blocks[have + i] = b; });
+            __syncwarp();
+            if (e1 - e0 <= kSparseEntries) {
+                tokens = list.tokens;
+                tell();
             }
-            if (u.seq < 0) {
-                if (lane == 0) allow_dependent_launch();
-                break;
-            }
-            // the unit after this one, its length and first blocks on their way meanwhile
-            next_unit(next);
-            const int32_t next_tokens = row_len(next);
-            int32_t next_phys = 0;
-            bool have_next = false;
-            const int32_t nb0 = u.tok0 / C::PBS, nb1 = (u.tok1 + C::PBS - 1) / C::PBS;
-            const int32_t ntiles = (u.tok1 - u.tok0 + C::BS - 1) / C::BS;
-            int32_t phys = phys0;
+            const int32_t n = have + list.count;
+            const int32_t ntiles = c1 == e1 ? (n + C::TB - 1) / C::TB : n / C::TB;
             for (int32_t i = 0; i < ntiles && ok; ++i) {
-                const int32_t e = (i * C::TB) & 31;
-                if (e == 0 && i > 0) phys = load_blocks(u.seq, nb0 + i * C::TB, min(32, nb1 - nb0 - i * C::TB));
-                if (i == 1) {
-                    next_phys = first_blocks(next, next_tokens);
-                    have_next = true;
-                }
-                int32_t pb[C::TB];
-#pragma unroll
-                for (int bi = 0; bi < C::TB; ++bi) pb[bi] = __shfl_sync(0xffffffffu, phys, e + bi);
                 if (lane == 0) {
                     ok = mbar_wait(&sm.empty[stage], ephase);
                     if (ok) {
                         mbar_arrive_expect_tx(&sm.full[stage], 2u * C::TILE_BYTES);
 #pragma unroll
                         for (int bi = 0; bi < C::TB; ++bi) {
-                            const int32_t y = pb[bi] * C::PBS;
+                            // (a tile's block past the list: a row past the tensor map, zeros)
+                            const int32_t e = i * C::TB + bi;
+                            const int32_t b = e < n ? sm.blocks[e] : p.num_blocks;
+                            out |= e < n && b == p.num_blocks;
+                            const int32_t y = b * C::PBS;
                             const uint32_t off = bi * C::PBS * 128;
 #pragma unroll
                             for (int hf = 0; hf < C::HALVES; ++hf) {
@@ -255,160 +227,196 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
                 if (++stage == C::NSTAGE) {
                     stage = 0;
                     ephase ^= 1;
                 }
             }
-            if (!ok) {
-                if (lane == 0) {
-                    flag_error(p.status, PA_DEVERR_TIMEOUT_);
-                    sm.abort = 1;
-                }
-                break;
-            }
-            if (!have_next) next_phys = first_blocks(next, next_tokens);
-            u = next;
-            tokens = next_tokens;
-            phys0 = next_phys;
+            // (blocks left over go to the front)
+            __syncwarp();
+            const int32_t rest = max(n - ntiles * C::TB, 0);
+            const int32_t b = lane < rest ? sm.blocks[ntiles * C::TB + lane] : 0;
+            __syncwarp();
+            if (lane < rest) sm.blocks[lane] = b;
+            have = rest;
         }
+        if (e0 >= e1) tell();
+        if (!ok) timed_out();
+        if (out) flag_error(p.status, PA_DEVERR_BAD_BLOCK_);
     } else {
-        // ------------------------------------------------------------ consumers (as the decode's)
-        grid_dependency_wait();
+        // ------------------------------------------------------------ consumers
         using Consumer = typename std::conditional<C::kMma, MmaConsumer<C>, CoreConsumer<C>>::type;
         const int c = warp - 1;
         constexpr int TS = C::NCONS;
-        auto all_agree = [&](bool v) {
-            if constexpr (C::NCONS > 1) return consumers_any(v, 32 * C::NCONS);
-            else return __any_sync(0xffffffffu, v);
-        };
-        auto timed_out = [&]() {
-            if (lane == 0) {
-                flag_error(p.status, PA_DEVERR_TIMEOUT_);
-                sm.abort = 1;
-            }
-        };
         Consumer cons;
-        uint32_t gtile = 0;   // tiles of all earlier units
-        for (uint32_t it = 0;; ++it) {
-            const uint32_t qs = it % C::NQ, qphase = (it / C::NQ) & 1;
-            bool stop = !mbar_wait_warp(&sm.qfull[qs], qphase);
-            if (stop) timed_out();
-            stop = stop || warp_sees_abort(sm.abort);
-            const UnitDesc u = sm.unit[qs];
-            if (stop || u.seq < 0) {
-                (void)all_agree(true);   // the unit barrier below, from a consumer that stops
-                break;
-            }
-            cons.load_q(sm.qbuf[qs], u.nrows, lane);
-            __syncwarp();
-            if (lane == 0) {
-                if (c == 0) sm.qconsumed[qs] += 1;
-                mbar_arrive(&sm.qempty[qs]);
-            }
-            cons.reset();
-            const int32_t b0 = u.tok0 / C::BS;
-            const int32_t ntiles = (u.tok1 + C::BS - 1) / C::BS - b0;
-            // tile k (over all units) goes to consumer k % TS; the last tile's consumer leads
-            const int gmod = (int)(gtile % (uint32_t)TS);
-            const int lead = (gmod + ntiles - 1 + TS) % TS;
-            for (int32_t t = (c - gmod + TS) % TS; t < ntiles; t += TS) {
-                const uint32_t k = gtile + (uint32_t)t;
-                const uint32_t stage = k % C::NSTAGE, fphase = (k / C::NSTAGE) & 1;
-                if (warp_sees_abort(sm.abort)) {
-                    stop = true;
-                    break;
-                }
-                if (!mbar_wait_warp(&sm.full[stage], fphase)) {
-                    timed_out();
-                    stop = true;
-                    break;
-                }
-                const int tile0 = (b0 + t) * C::BS;
-                const int valid = min(C::BS, u.tok1 - tile0);
+        bool stop = !mbar_wait_warp(&sm.qfull, 0) || !mbar_wait_warp(&sm.listed, 0);
+        cons.reset();
+        if (!stop) {
+            cons.load_q(sm.q, p.group, lane);
+            if (c == 0 && lane == 0) sm.q_read = 1;
+            const int32_t tokens = sm.tokens, ntiles = (tokens + C::BS - 1) / C::BS;
+            for (int32_t t = c; t < ntiles; t += TS) {
+                const uint32_t stage = (uint32_t)t % C::NSTAGE, fphase = ((uint32_t)t / C::NSTAGE) & 1;
+                stop = warp_sees_abort(sm.abort) || !mbar_wait_warp(&sm.full[stage], fphase);
+                if (stop) break;
+                const int valid = min(C::BS, tokens - t * C::BS);
                 if constexpr (C::kMma)
-                    cons.tile(sm.kv[stage][0], sm.kv[stage][1], valid, tile0, p.scale_log2, lane, nullptr);
+                    cons.tile(sm.kv[stage][0], sm.kv[stage][1], valid, t * C::BS, p.scale_log2, lane, nullptr);
                 else
-                    cons.tile(sm.kv[stage][0], sm.kv[stage][1], valid, tile0, p.scale_log2, lane, sm.pbuf[c]);
+                    cons.tile(sm.kv[stage][0], sm.kv[stage][1], valid, t * C::BS, p.scale_log2, lane, sm.pbuf[c]);
                 __syncwarp();
                 if (lane == 0) {
                     sm.consumed[stage] += 1;
                     mbar_arrive(&sm.empty[stage]);
                 }
             }
-            gtile += (uint32_t)ntiles;
-            if (TS > 1 && !stop && c != lead) {
-                if (it > 0 && !mbar_wait_warp(&sm.xfree, (it - 1) & 1)) {
-                    timed_out();
-                    stop = true;
-                } else {
-                    cons.export_state(sm.xbuf[(c - lead - 1 + TS) % TS], lane);
-                }
-            }
-            if (all_agree(stop)) break;   // the unit barrier (also: the states are in shared memory)
-            if (c == lead) {
-                for (int o = 0; o < TS - 1; ++o) cons.merge_state(sm.xbuf[o], lane);
-                if (TS > 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.xfree);
-                }
-                if (!warp_sees_abort(sm.abort)) cons.finish(sm.ostage, p, u, lane);
+        }
+        if (stop) timed_out();
+        // the consumers' states meet in the first one (no tile is read any more, or, after an
+        // abort, nothing of this is used)
+        if constexpr (TS > 1) {
+            stop = consumers_any(stop, 32 * TS);
+            if (c > 0 && !stop) cons.export_state(sm.states[c - 1], lane);
+            named_bar_sync(1, 32 * TS);
+        }
+        if (c == 0 && !stop) {
+            for (int o = 0; o < TS - 1; ++o) cons.merge_state(sm.states[o], lane);
+            if (parts > 1) {
+                stage_state<C>(cons, sm.sums, sm.ml, p.group, lane);
+            } else if (!warp_sees_abort(sm.abort)) {
+                UnitDesc u = {};
+                u.seq = row;
+                u.pslot = -1;
+                u.nrows = p.group;
+                cons.finish(sm.sums, p, u, lane);
             }
         }
     }
-
+    if (parts > 1) {
+        // The row's parts meet: each CTA takes every parts-th piece of eight elements.
+        __syncwarp();
+        cluster_sync();
+        const uint32_t acc0 = smem_u32(sm.sums), ml0 = smem_u32(sm.ml);
+        if (!sm.abort) {
+            for (int32_t i = (int32_t)threadIdx.x * parts + rank; i < p.group * C::D / 8; i += C::THREADS * parts) {
+                const int32_t h = i / (C::D / 8);
+                // (a running join, eight parts' values on their way together)
+                float M = -INFINITY, den = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int32_t q0 = 0; q0 < parts; q0 += 8) {
+                    float2 ml[8];
+                    float4 x[8][2];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        ml[q] = make_float2(-INFINITY, 0.f);
+                        x[q][0] = x[q][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (q0 + q < parts) {
+                            ml[q] = ld_cluster2(map_to_rank(ml0 + h * 8, q0 + q));
+                            const uint32_t a = map_to_rank(acc0 + i * 32, q0 + q);
+                            x[q][0] = ld_cluster4(a);
+                            x[q][1] = ld_cluster4(a + 16);
+                        }
+                    }
+                    float next = M;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) next = fmaxf(next, ml[q].x);
+                    const float keep = state_weight(M, next);
+                    M = next;
+                    den *= keep;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] *= keep;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float w = state_weight(ml[q].x, M);
+                        den += w * ml[q].y;
+                        y[0] += w * x[q][0].x, y[1] += w * x[q][0].y, y[2] += w * x[q][0].z, y[3] += w * x[q][0].w;
+                        y[4] += w * x[q][1].x, y[5] += w * x[q][1].y, y[6] += w * x[q][1].z, y[7] += w * x[q][1].w;
+                    }
+                }
+                const float f = den > 0.f ? p.out_scale / den : 0.f;
+                uint4 o;
+                o.x = pack2<C::kBf16>(y[0] * f, y[1] * f);
+                o.y = pack2<C::kBf16>(y[2] * f, y[3] * f);
+                o.z = pack2<C::kBf16>(y[4] * f, y[5] * f);
+                o.w = pack2<C::kBf16>(y[6] * f, y[7] * f);
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)row * p.group * C::D)[i] = o;
+            }
+        }
+        __syncwarp();
+        cluster_sync();          // (the others may still be reading here)
+    }
     // On a timeout, copies may still be landing: wait (bounded) for those never consumed.
     __syncthreads();
     if (threadIdx.x == 0 && sm.abort) {
         for (int i = 0; i < C::NSTAGE; ++i)
             if (sm.issued[i] > sm.consumed[i]) (void)mbar_wait(&sm.full[i], sm.consumed[i] & 1);
-        for (int i = 0; i < C::NQ; ++i)
-            if (sm.qissued[i] > sm.qconsumed[i]) (void)mbar_wait(&sm.qfull[i], sm.qconsumed[i] & 1);
+        if (!sm.q_read) (void)mbar_wait(&sm.qfull, 0);
     }
 }
 
-// Launches the kernel with `ctas` CTAs, or (ctas 0) tells the CTAs per SM that it can have.
+// A short ring, so that more CTAs fit an SM: about half of the decode's stages (8-bit caches: two
+// consumers and four stages; three and three took 115 us where these take 80).
+template <int NSTAGE, int NCONS>
+constexpr int short_stages() {
+    return std::max((NSTAGE / 2 + NCONS - 1) / NCONS * NCONS, 2);
+}
+
+// Launches the attention with `ctas` CTAs, or (ctas 0) tells the CTAs per SM that it can have.
 template <int D, int BS, bool BF16, bool MMA, int HCAP, bool KV8, int TB>
 cudaError_t launch_sparse_one(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
                               const SparseParams& sp, int32_t ctas, cudaStream_t stream, int32_t* per_sm) {
     constexpr int kTile = BS * TB;
     constexpr int kCons = consumers_for<MMA, kTile, KV8>();
     constexpr int kStages = stages_for<D * (KV8 ? 1 : 2) / 2, kTile, kCons>();
-    using C0 = DecodeCfg<D, kTile, BF16, MMA, HCAP, kStages, 2, kCons, KV8, false, 0, BS>;
-    using C = DecodeCfg<D, kTile, BF16, MMA, HCAP, kStages, 2, kCons, KV8, false, decode_min_ctas<C0>(), BS>;
-    constexpr size_t smem = decode_smem_bytes<C>();
-    auto kern = sparse_decode_kernel<C>;
+    using C0 = DecodeCfg<D, kTile, BF16, MMA, HCAP, kStages, 1, kCons, KV8, false, 0, BS>;
+    using C = DecodeCfg<D, kTile, BF16, MMA, HCAP, kStages, 1, kCons, KV8, false, decode_min_ctas<C0>(), BS>;
+    constexpr int kShortCons = KV8 ? 2 : kCons, kShort = KV8 ? 4 : short_stages<kStages, kCons>();
+    using CS = DecodeCfg<D, kTile, BF16, MMA, HCAP, kShort, 1, kShortCons, KV8, false, decode_min_ctas<C0>(), BS>;
+    using Kern = void (*)(CUtensorMap, CUtensorMap, DecodeParams, SparseParams);
+    const Kern kerns[2] = {sparse_kernel<C>, sparse_kernel<CS>};
+    constexpr size_t smems[2] = {sparse_smem_bytes<C>(), sparse_smem_bytes<CS>()};
+    constexpr int threads[2] = {C::THREADS, CS::THREADS};
+    const int kind = sp.short_ring ? 1 : 0;
     static PerDeviceOnce configured;
-    static std::atomic<int32_t> known[PerDeviceOnce::kMaxDevices];
+    static std::atomic<int32_t> known[2][PerDeviceOnce::kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     e = static_cast<cudaError_t>(configured.run(dev, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e1 = cudaSuccess;
+        for (int i = 0; i < 2 && e1 == cudaSuccess; ++i) {
+            e1 = cudaFuncSetAttribute(kerns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smems[i]);
+            // (clusters of 16)
+            if (e1 == cudaSuccess) e1 = cudaFuncSetAttribute(kerns[i], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        }
+        return e1;
     }));
     if (e != cudaSuccess) return e;
     if (ctas == 0) {
-        int n = dev >= 0 && dev < PerDeviceOnce::kMaxDevices ? known[dev].load() : 0;
+        const bool cached = dev >= 0 && dev < PerDeviceOnce::kMaxDevices;
+        int n = cached ? known[kind][dev].load() : 0;
         if (n == 0) {
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, C::THREADS, smem);
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kerns[kind], threads[kind], smems[kind]);
             if (e != cudaSuccess) return e;
-            if (dev >= 0 && dev < PerDeviceOnce::kMaxDevices) known[dev].store(n);
+            if (cached) known[kind][dev].store(n);
         }
         *per_sm = n;
         return cudaSuccess;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3((unsigned)threads[kind]);
+    cfg.dynamicSmemBytes = smems[kind];
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)sp.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, sp);
+    cfg.numAttrs = sp.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kerns[kind], kmap, vmap, p, sp);
 }
 
 // The instantiations of one type over 16-bit caches: single query heads on the CUDA cores, groups

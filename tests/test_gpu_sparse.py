@@ -463,3 +463,23 @@ def test_sparse_step_in_a_graph_and_on_streams(cuda_device):
         assert torch.equal(before, out)
     assert int(status) == 0
     assert bool((w1[n1:] == 0x5A).all()) and bool((w2[n2:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,bs,dtype,keep,fp8", [
+    (4, 1, 64, 16, torch.float16, 9001, False),          # a cluster's CTAs take their pieces in several goes
+    (8, 1, 128, 16, torch.bfloat16, 8999, True),         # .. whose blocks pair across the goes
+    (2, 2, 128, 32, torch.bfloat16, 1200, False),
+])
+def test_very_long_lists(cuda_device, Hq, Hkv, D, bs, dtype, keep, fp8):
+    sparse_run(sparse_case([200000, 150007, 900], 1, Hq, Hkv, D, bs, dtype, keep, 12, fp8, pick=keep))
+
+
+def test_lists_longer_than_a_go_on_every_kind_of_row(cuda_device):
+    """Whole rows of 700 entries (more rows than SMs have places), the first entries -1."""
+    b = sparse_case([12000] * 250, 1, 8, 8, 64, 16, torch.bfloat16, 700, 13, pick=650)
+    b["selected"] = torch.cat([torch.full_like(b["selected"][..., :30], -1), b["selected"]], -1).contiguous()
+    out = sparse_call(b)
+    torch.cuda.synchronize()
+    for s in (0, 17, 249):
+        one = dict(b, q=b["q"][s:s + 1], tables=b["tables"][s:s + 1], lens=[12000], selected=b["selected"][s:s + 1])
+        sparse_check(one, out[s:s + 1])

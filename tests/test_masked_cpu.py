@@ -248,9 +248,6 @@ def _sparse(lib, fp8=False, **kw):
     (dict(out=0), INVALID, "null"),
     (dict(q=MIS), INVALID, "aligned"),
     (dict(vc=MIS), INVALID, "aligned"),
-    (dict(ws=0), WORKSPACE, "workspace"),
-    (dict(wb=10), WORKSPACE, "workspace"),
-    (dict(ws=A + 16), INVALID, "256-byte"),
 ])
 def test_sparse_refusals(lib, fp8, kw, code, word):
     assert _sparse(lib, fp8, **kw) == code
@@ -262,12 +259,8 @@ def test_sparse_fp8_refusals_empty_calls_and_sizes(lib, pa):
         assert _sparse(lib, True, **kw) == INVALID and "k_scale" in _err(lib)
     assert _sparse(lib, True, D=64) == UNSUPPORTED
     assert _sparse(lib, S=0, out=0, q=0, kc=0, vc=0, bt=0, lens=0, sel=0, ws=0, wb=0) == OK
-    size = pa.pa_decode_sparse_workspace_size
-    assert size(3, 1, 8, 2, 128, 16, 8) > 0 and size(3, 2, 8, 2, 128, 16, 8) > size(3, 1, 8, 2, 128, 16, 8)
-    for bad in ((-1, 1, 8, 2, 128, 16, 8), (3, 0, 8, 2, 128, 16, 8), (3, 1, 9, 2, 128, 16, 8),
-                (3, 1, 8, 0, 128, 16, 8), (3, 1, 8, 2, 128, 16, 0), (1 << 24, 9, 8, 2, 128, 16, 8),
-                (1, 1, 8, 2, 128, 16, 1 << 22)):
-        assert size(*bad) == 0
+    # (the parts of a row meet in shared memory)
+    assert pa.pa_decode_sparse_workspace_size(3, 1, 8, 2, 128, 16, 8) == 0
 
 
 def test_binding_refuses_before_the_library(pa, monkeypatch):
