@@ -19,30 +19,57 @@ __device__ __forceinline__ int32_t exponent_of(float x) {
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float power_of_two(int32_t e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// 16 bytes of K as floats.
+// Pairs of 16-bit values (8-bit caches: widened to fp16): the larger and smaller ones (of a number
+// and NaN: the number), and x * 0 + acc, which is NaN from the first infinity or NaN on.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (BF16) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t odd2(uint32_t acc, uint32_t x) {
+    uint32_t r;
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    return r;
+}
+
+// 16 bytes of K as pairs.
 template <BoundsType T>
-__device__ __forceinline__ void widen(const uint4& x, float (&v)[T == BoundsType::kFp8 ? 16 : 8]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ void pairs(const uint4& x, uint32_t (&v)[T == BoundsType::kFp8 ? 8 : 4]) {
     if constexpr (T == BoundsType::kFp8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t lo, hi;
-            e4m3x4_to_f16x2x2(w[i], lo, hi);
-            unpack2<false>(lo, v[4 * i], v[4 * i + 1]);
-            unpack2<false>(hi, v[4 * i + 2], v[4 * i + 3]);
-        }
+        e4m3x4_to_f16x2x2(x.x, v[0], v[1]);
+        e4m3x4_to_f16x2x2(x.y, v[2], v[3]);
+        e4m3x4_to_f16x2x2(x.z, v[4], v[5]);
+        e4m3x4_to_f16x2x2(x.w, v[6], v[7]);
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack2<T == BoundsType::kBf16>(w[i], v[2 * i], v[2 * i + 1]);
+        v[0] = x.x;
+        v[1] = x.y;
+        v[2] = x.z;
+        v[3] = x.w;
     }
 }
 
 constexpr int kBoundsWarps = 4;
+// Blocks of a sequence and kv head that a warp takes, one after another.
+constexpr int kBoundsRun = 4;
 
-// A warp per (block, kv head): its lanes read the block's rows, 16 bytes each and several rows
-// at once, and keep the largest and smallest value of their dims; the halves of the warp join by
-// shuffles.  The step is a power of two, so that x / step and its rounding are exact in fp32.
-// Bound by HBM for prompts (one read of K, 1/16 of it written), by latency for a step.
+// A warp per kv head and run of blocks: its lanes read a block's rows, 16 bytes each and several
+// rows at once, and keep the largest and smallest value of their dims; the halves of the warp join
+// by shuffles.  The step is a power of two, so that x / step and its rounding are exact in fp32.
+// Bound by HBM for prompts (one read of K, 1/16 of it written), by latency for a step.  A run, since
+// what comes before a block's rows (lengths, then table entries) is as long as the rows' own wait:
+// 58 K tokens of new prompts, 8 heads of 128 (125 MB): 22.2 us, 5.6 TB/s; a block at a time 23.2; 26.7 before
+// the values were compared in pairs of 16 bits.
 template <BoundsType T, int D, int BS>
 __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const BoundsParams p) {
     constexpr int kElem = T == BoundsType::kFp8 ? 1 : 2;
@@ -53,10 +80,11 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Bou
     grid_dependency_wait();
     allow_dependent_launch();
     const int32_t lane = threadIdx.x & 31;
+    const int32_t runs = (p.slots + kBoundsRun - 1) / kBoundsRun;
     const int64_t unit = (int64_t)blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
     const int32_t h = (int32_t)(unit % p.num_kv_heads);
     const int64_t at = unit / p.num_kv_heads;
-    const int32_t s = (int32_t)(at / p.slots), j = (int32_t)(at - (int64_t)s * p.slots);
+    const int32_t s = (int32_t)(at / runs), run = (int32_t)(at - (int64_t)s * runs);
     if (s >= p.num_seqs) return;
     const int64_t cap = min((int64_t)p.max_blocks_per_seq * BS, (int64_t)INT32_MAX);
     int32_t n = p.max_new_tokens;
@@ -67,82 +95,107 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Bou
         bad |= n < 0 || n > p.max_new_tokens;
         n = min(max(n, 0), p.max_new_tokens);
     }
-    if (bad && j == 0 && h == 0 && lane == 0 && p.status) atomicOr(p.status, kDevBadLen);
+    if (bad && run == 0 && h == 0 && lane == 0 && p.status) atomicOr(p.status, kDevBadLen);
     const int32_t len = (int32_t)min((int64_t)max(l, 0), cap);
-    const int32_t block = max(len - n, 0) / BS + j;   // the j-th block that holds a new token
-    const int32_t valid = min(len - block * BS, BS);
-    if (n == 0 || valid <= 0) return;
-    const int32_t phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + block];
-    if (phys < 0 || phys >= p.num_blocks) {
-        if (h == 0 && lane == 0 && p.status) atomicOr(p.status, kDevBadBlock);
-        return;
-    }
-    const int64_t place = (int64_t)phys * p.num_kv_heads + h;
-    const uint4* rows = static_cast<const uint4*>(p.key_cache) + place * BS * kLanes;
-    uint4 x[kLoads];
+    // this run's blocks: of those that hold a new token
+    const int32_t first = max(len - n, 0) / BS + run * kBoundsRun;
+    const int32_t count = n == 0 ? 0 : min((len - first * BS + BS - 1) / BS, kBoundsRun);
+    int32_t entry = 0;                                // lane i: block i's place in the pool
+    if (lane < count) entry = p.block_tables[(size_t)s * p.max_blocks_per_seq + first + lane];
+    for (int32_t i = 0; i < count; ++i) {
+        const int32_t block = first + i, valid = min(len - block * BS, BS);
+        const int32_t phys = __shfl_sync(0xffffffffu, entry, i);
+        if (phys < 0 || phys >= p.num_blocks) {
+            if (h == 0 && lane == 0 && p.status) atomicOr(p.status, kDevBadBlock);
+            continue;
+        }
+        const int64_t place = (int64_t)phys * p.num_kv_heads + h;
+        const uint4* rows = static_cast<const uint4*>(p.key_cache) + place * BS * kLanes;
+        uint4 x[kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-        if (i * kRows + lane / kLanes < valid) x[i] = rows[i * 32 + lane];
-    float hi[kDims], lo[kDims];
-    bool nan = false;
+        for (int i = 0; i < kLoads; ++i)
+            if (i * kRows + lane / kLanes < valid) x[i] = rows[i * 32 + lane];
+        constexpr bool kBf16 = T == BoundsType::kBf16;
+        constexpr uint32_t kInf = kBf16 ? 0x7F807F80u : 0x7C007C00u, kSign = 0x80008000u;
+        uint32_t top[kDims / 2], bottom[kDims / 2], odd = 0;
 #pragma unroll
-    for (int d = 0; d < kDims; ++d) {
-        hi[d] = -INFINITY;
-        lo[d] = INFINITY;
-    }
+        for (int d = 0; d < kDims / 2; ++d) {
+            top[d] = kInf | kSign;
+            bottom[d] = kInf;
+        }
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        if (i * kRows + lane / kLanes < valid) {
-            float v[kDims];
-            widen<T>(x[i], v);
+        for (int i = 0; i < kLoads; ++i) {
+            if (i * kRows + lane / kLanes < valid) {
+                uint32_t v[kDims / 2];
+                pairs<T>(x[i], v);
 #pragma unroll
-            for (int d = 0; d < kDims; ++d) {
-                nan |= v[d] != v[d];
-                hi[d] = fmaxf(hi[d], v[d]);
-                lo[d] = fminf(lo[d], v[d]);
+                for (int d = 0; d < kDims / 2; ++d) {
+                    odd = odd2<kBf16>(odd, v[d]);
+                    top[d] = max2<kBf16>(top[d], v[d]);
+                    bottom[d] = min2<kBf16>(bottom[d], v[d]);
+                }
             }
         }
-    }
 #pragma unroll
-    for (int o = kLanes; o < 32; o <<= 1)
+        for (int o = kLanes; o < 32; o <<= 1)
+#pragma unroll
+            for (int d = 0; d < kDims / 2; ++d) {
+                top[d] = max2<kBf16>(top[d], __shfl_xor_sync(0xffffffffu, top[d], o));
+                bottom[d] = min2<kBf16>(bottom[d], __shfl_xor_sync(0xffffffffu, bottom[d], o));
+            }
+        // (rare) an infinity, or NaN?
+        bool nan = false;
+        if (__any_sync(0xffffffffu, odd != 0)) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (i * kRows + lane / kLanes < valid) {
+                    uint32_t v[kDims / 2];
+                    pairs<T>(x[i], v);
+#pragma unroll
+                    for (int d = 0; d < kDims / 2; ++d)
+                        nan |= (v[d] & 0x7FFFu) > (kInf & 0xFFFFu) || ((v[d] >> 16) & 0x7FFFu) > (kInf & 0xFFFFu);
+                }
+        }
+        float hi[kDims], lo[kDims];
+#pragma unroll
+        for (int d = 0; d < kDims / 2; ++d) {
+            unpack2<kBf16>(top[d], hi[2 * d], hi[2 * d + 1]);
+            unpack2<kBf16>(bottom[d], lo[2 * d], lo[2 * d + 1]);
+        }
+        nan = __any_sync(0xffffffffu, nan);
+        // (a dim of NaN alone stays at -inf, inf: it counts as 0; an infinity as the largest number)
+        constexpr float kMost = T == BoundsType::kBf16 ? 3.38953139e38f : 65504.f;
+        float most = 0.f;
 #pragma unroll
         for (int d = 0; d < kDims; ++d) {
-            hi[d] = fmaxf(hi[d], __shfl_xor_sync(0xffffffffu, hi[d], o));
-            lo[d] = fminf(lo[d], __shfl_xor_sync(0xffffffffu, lo[d], o));
+            if (hi[d] < lo[d]) hi[d] = lo[d] = 0.f;
+            most = fmaxf(most, fmaxf(fabsf(hi[d]), fabsf(lo[d])));
         }
-    nan = __any_sync(0xffffffffu, nan);
-    // (a dim of NaN alone stays at -inf, inf: it counts as 0; an infinity as the largest number)
-    constexpr float kMost = T == BoundsType::kBf16 ? 3.38953139e38f : 65504.f;
-    float most = 0.f;
 #pragma unroll
-    for (int d = 0; d < kDims; ++d) {
-        if (hi[d] < lo[d]) hi[d] = lo[d] = 0.f;
-        most = fmaxf(most, fmaxf(fabsf(hi[d]), fabsf(lo[d])));
-    }
+        for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const int32_t e = min(exponent_of(fminf(most, kMost)), 96) - 6;
+        const float inv = power_of_two(-e);
+        // row groups 0 and 1 write the upper and the lower bounds
+        int8_t* out = p.bounds + place * 2 * D;
+        const int32_t part = lane / kLanes;
+        if (part < 2) {
+            uint32_t w[kDims / 4];
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const int32_t e = min(exponent_of(fminf(most, kMost)), 96) - 6;
-    const float inv = power_of_two(-e);
-    // row groups 0 and 1 write the upper and the lower bounds
-    int8_t* out = p.bounds + place * 2 * D;
-    const int32_t part = lane / kLanes;
-    if (part < 2) {
-        uint32_t w[kDims / 4];
+            for (int k = 0; k < kDims / 4; ++k) {
+                w[k] = 0;
 #pragma unroll
-        for (int k = 0; k < kDims / 4; ++k) {
-            w[k] = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const float y = part ? lo[4 * k + b] : hi[4 * k + b];
-                const int32_t q = __float2int_rn(fminf(fmaxf(y * inv, -127.f), 127.f));
-                w[k] |= ((uint32_t)q & 0xFFu) << (8 * b);
+                for (int b = 0; b < 4; ++b) {
+                    const float y = part ? lo[4 * k + b] : hi[4 * k + b];
+                    const int32_t q = __float2int_rn(fminf(fmaxf(y * inv, -127.f), 127.f));
+                    w[k] |= ((uint32_t)q & 0xFFu) << (8 * b);
+                }
             }
+            int8_t* dst = out + part * D + (lane % kLanes) * kDims;
+            if constexpr (kDims == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
         }
-        int8_t* dst = out + part * D + (lane % kLanes) * kDims;
-        if constexpr (kDims == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        if (lane == 0) p.steps[place] = nan ? __int_as_float(0x7fc00000) : power_of_two(e);
     }
-    if (lane == 0) p.steps[place] = nan ? __int_as_float(0x7fc00000) : power_of_two(e);
 }
 
 // ------------------------------------------------------------------ selection
@@ -641,7 +694,7 @@ cudaError_t launch_bounds_of(const BoundsParams& p, cudaStream_t stream) {
     const Kern kern = p.head_size == 128
                           ? (p.block_size == 16 ? (Kern)key_bounds_kernel<T, 128, 16> : (Kern)key_bounds_kernel<T, 128, 32>)
                           : (p.block_size == 16 ? (Kern)key_bounds_kernel<T, 64, 16> : (Kern)key_bounds_kernel<T, 64, 32>);
-    const int64_t units = (int64_t)p.num_seqs * p.slots * p.num_kv_heads;
+    const int64_t units = (int64_t)p.num_seqs * ((p.slots + kBoundsRun - 1) / kBoundsRun) * p.num_kv_heads;
     return launch_pdl(dim3((unsigned)((units + kBoundsWarps - 1) / kBoundsWarps)), dim3(32 * kBoundsWarps), 0, stream,
                       kern, p);
 }
