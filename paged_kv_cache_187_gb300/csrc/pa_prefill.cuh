@@ -507,11 +507,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // row tile: the last one whose units begin at or before `at`
                         int32_t a = here;
                         if (it == 0) {
+                            // (32 places looked at together: a round trip through L2 or two, where
+                            // halving took one per bit, 0.6 us each)
                             int32_t b = (int32_t)(hdr.total_units / (uint32_t)Hkv);
                             while (b - a > 1) {
-                                const int32_t m = (a + b) >> 1;
-                                if (p.before[m] * Hkv <= at) a = m;
-                                else b = m;
+                                const int32_t step = (b - a + 31) / 32;
+                                const int32_t m = min(a + lane * step, b);
+                                const bool le = m < b && p.before[m] * Hkv <= at;
+                                const int32_t k = 31 - __clz(__ballot_sync(0xffffffffu, lane == 0 || le));
+                                a += k * step;
+                                b = min(a + step, b);
                             }
                         } else if (p.before[a + 1] * Hkv <= at) {
                             ++a;
@@ -1380,10 +1385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < dims / 16; ++h) {
                         float o[16];
                         load_o(h, o);
+                        if (mine) {      // (a row that holds no token is not read again either)
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) p.part_acc[cell(at, dim0 + 16 * h + c)] = o[c];
+                            for (int c = 0; c < 16; ++c) p.part_acc[cell(at, dim0 + 16 * h + c)] = o[c];
+                        }
                     }
-                    if (half == 0 && !(both && si)) p.part_ml[at + row] = make_float2(ref, sum);
+                    if (mine && half == 0 && !(both && si)) p.part_ml[at + row] = make_float2(ref, sum);
                 }
                 release();
                 if (takes_part) {
@@ -1401,14 +1408,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     named_bar_sync(bar, kStreamThreads);
                     if (sm.last_part[si]) {
                         __threadfence();
-                        float M = -INFINITY;
+                        // (three at a time, each a round trip through L2; a row of no token: none)
+                        const int32_t parts = mine ? u.nparts : 0;
+                        float M = -INFINITY, den = 0.f;
 #pragma unroll 1
-                        for (int q = 0; q < u.nparts; ++q) M = fmaxf(M, __ldcg(&p.part_ml[place(q) + row]).x);
-                        float den = 0.f;
+                        for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-                        for (int q = 0; q < u.nparts; ++q) {
-                            const float2 ml = __ldcg(&p.part_ml[place(q) + row]);
-                            den += state_weight(ml.x, M) * ml.y;
+                            for (int q = 0; q < parts; q += 3) {
+                                float2 ml[3];
+#pragma unroll
+                                for (int t = 0; t < 3; ++t)
+                                    ml[t] = q + t < parts ? __ldcg(&p.part_ml[place(q + t) + row])
+                                                          : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                                for (int t = 0; t < 3; ++t) {
+                                    if (pass == 0) M = fmaxf(M, ml[t].x);
+                                    else if (q + t < parts) den += state_weight(ml[t].x, M) * ml[t].y;
+                                }
+                            }
                         }
                         const float f = den == 0.f ? 0.f : p.out_scale / den;
                         // (three partitions' values are on their way together: one at a time, joining six of them
