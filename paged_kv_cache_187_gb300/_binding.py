@@ -13,6 +13,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 from . import build as _build
 
@@ -161,7 +162,6 @@ def raw():
 
 # --------------------------------------------------------------------------- helpers
 def _dt(t) -> int:
-    import torch
     if t.dtype == torch.float16:
         return PA_F16
     if t.dtype == torch.bfloat16:
@@ -180,14 +180,12 @@ def _dev(t, name, dtype=None):
 
 
 def _opt_dev(t, name):
-    import torch
     if t is None:
         return None
     return _dev(t, name, torch.int32)
 
 
 def _stream(stream):
-    import torch
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
@@ -197,7 +195,6 @@ def _stream(stream):
 def pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, status=None,
                          stream=None):
     """key/value [T, Hkv, D]; key_cache/value_cache [NB, Hkv, bs, D]; slot_mapping [T] int32."""
-    import torch
     T, Hkv, D = key.shape
     NB, Hkv2, bs, D2 = key_cache.shape
     if value.shape != key.shape or value_cache.shape != key_cache.shape or (Hkv2, D2) != (Hkv, D):
@@ -215,7 +212,6 @@ def pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, statu
 
 
 def _decode_common(out, query, key_cache, value_cache, block_tables, context_lens):
-    import torch
     S, Hq, D = query.shape
     NB, Hkv, bs, D2 = key_cache.shape
     if out.shape != query.shape or value_cache.shape != key_cache.shape or D2 != D:
@@ -315,7 +311,6 @@ def pa_decode_auto(out, query, key_cache, value_cache, block_tables, context_len
 
 def _u8(t, name):
     """An fp8 E4M3 pool: a uint8 (or float8_e4m3fn) CUDA tensor."""
-    import torch
     if t.dtype not in (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8)):
         raise TypeError(f"{name} must be uint8 / float8_e4m3fn (fp8 E4M3 bytes), got {t.dtype}")
     return _dev(t, name)
@@ -324,7 +319,6 @@ def _u8(t, name):
 def pa_reshape_and_cache_fp8(key, value, key_cache, value_cache, slot_mapping, k_scale: float,
                              v_scale: float, status=None, stream=None):
     """Quantising scatter: key/value [T, Hkv, D] fp16/bf16 -> fp8 E4M3 pools [NB, Hkv, bs, D]."""
-    import torch
     T, Hkv, D = key.shape
     NB, Hkv2, bs, D2 = key_cache.shape
     if value.shape != key.shape or value_cache.shape != key_cache.shape or (Hkv2, D2) != (Hkv, D):
@@ -346,7 +340,6 @@ def pa_decode_fp8(out, query, key_cache, value_cache, block_tables, context_lens
                   variant: str = "auto", partition_size: int = 0, workspace=None, status=None,
                   stream=None):
     """Paged decode over fp8 E4M3 pools; query/out fp16 or bf16 [S, Hq, D]."""
-    import torch
     S, Hq, D = query.shape
     NB, Hkv, bs, D2 = key_cache.shape
     if out.shape != query.shape or value_cache.shape != key_cache.shape or D2 != D:
@@ -375,7 +368,6 @@ def pa_decode_mq(out, query, key_cache, value_cache, block_tables, context_lens,
                  workspace=None, status=None, stream=None):
     """Multi-query paged decode: query/out [S, q_len, Hq, D]; new token j of a sequence of
     length L attends to tokens t < L - q_len + j + 1."""
-    import torch
     S, QL, Hq, D = query.shape
     NB, Hkv, bs, D2 = key_cache.shape
     if out.shape != query.shape or value_cache.shape != key_cache.shape or D2 != D:
@@ -394,7 +386,6 @@ def pa_decode_mq(out, query, key_cache, value_cache, block_tables, context_lens,
 def pa_decode_step(out, query, key, value, key_cache, value_cache, slot_mapping, block_tables,
                    context_lens, max_context_len: int, scale: float, workspace=None, status=None,
                    stream=None):
-    import torch
     S, Hq, D = query.shape
     NB, Hkv, bs, D2 = key_cache.shape
     if key.shape != (S, Hkv, D) or value.shape != key.shape or slot_mapping.shape != (S,):
@@ -439,7 +430,6 @@ def pa_decode_step_host(out_host, query_host, key_host, value_host, slot_mapping
                         status=None, stream=None):
     """One decode step from host buffers (pinned CPU tensors): H2D of the inputs,
     reshape_and_cache + decode, D2H of out, all enqueued on the stream (no wait)."""
-    import torch
     S, Hq, D = query_host.shape
     NB, Hkv, bs, D2 = key_cache.shape
     if key_host.shape != (S, Hkv, D) or value_host.shape != key_host.shape or D2 != D:
@@ -501,7 +491,6 @@ def pa_advance_step(context_lens, slot_mapping, block_tables, block_size: int, n
                     input_positions=None, input_tokens=None, sampled_token_ids=None,
                     status=None, stream=None):
     """Device-side move of every sequence to its next token (multi-step decode loop)."""
-    import torch
     S = int(context_lens.shape[0])
     if slot_mapping.shape != (S,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("advance_step: context_lens / slot_mapping [S], block_tables [S, max]")
@@ -518,7 +507,6 @@ def pa_advance_step(context_lens, slot_mapping, block_tables, block_size: int, n
 def pa_copy_blocks(key_cache, value_cache, block_pairs, status=None, stream=None):
     """Device copy of whole blocks old -> new for each row (old, new) of block_pairs
     (int32 [n, 2] on the device), in both pools."""
-    import torch
     NB, Hkv, bs, D = key_cache.shape
     if value_cache.shape != key_cache.shape or block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
         raise ValueError("copy_blocks: pools [NB, Hkv, bs, D] and pairs [n, 2] expected")
@@ -535,6 +523,10 @@ def pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, h
                                               head_size, max_context_len))
 
 
+_current_device, _current_stream = (getattr(torch._C, "_cuda_getDevice", None),
+                                    getattr(torch._C, "_cuda_getCurrentRawStream", None))
+
+
 class _Call:
     """The device and stream of one call, and its tensors' addresses.  The library launches on
     the current device, so every tensor has to live there."""
@@ -542,13 +534,11 @@ class _Call:
     __slots__ = ("dev",)
 
     def __init__(self):
-        import torch
-        self.dev = torch._C._cuda_getDevice()
+        self.dev = _current_device()
 
     def stream(self, stream):
         if stream is None:
-            import torch
-            return torch._C._cuda_getCurrentRawStream(self.dev)
+            return _current_stream(self.dev)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
     def here(self, t, name):
@@ -559,17 +549,26 @@ class _Call:
                              f"{self.dev}")
 
     def ptr(self, t, name, dtype):
-        if t.get_device() != self.dev:
+        if t.get_device() != self.dev or t.dtype is not dtype or not t.is_contiguous():
             self.here(t, name)
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
+    def pools(self, tensors, shape, dtype):
+        """The addresses of layers' pools, which have one shape and type."""
+        dev, got = self.dev, array.array("Q")
+        for t in tensors:
+            if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+                if t.shape != shape:
+                    raise ValueError("the pools must have one shape and type")
+                self.ptr(t, "pool", dtype)
+            got.append(t.data_ptr())
+        return got
+
     def pool8(self, t, name):
         """An fp8 E4M3 pool: a uint8 or float8_e4m3fn tensor."""
-        import torch
         if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
             raise TypeError(f"{name} must be uint8 / float8_e4m3fn (fp8 E4M3 bytes), got {t.dtype}")
         return self.ptr(t, name, t.dtype)
@@ -590,7 +589,6 @@ class _Call:
 
 def _prefill(fn, pool, scales, out, query, key_cache, value_cache, block_tables, context_lens,
              query_starts, max_context_len, scale, workspace, status, stream, *tree_mask):
-    import torch
     i32 = torch.int32
     c = _Call()
     T, Hq, D = query.shape
@@ -647,7 +645,6 @@ def pa_prefill_fp8(out, query, key_cache, value_cache, block_tables, context_len
 
 def _rope(fn, fp8, scales, query_out, query, key, value, key_cache, value_cache, slot_mapping,
           positions, inv_freq, pair_axes, interleaved, status, stream):
-    import torch
     c = _Call()
     T, Hq, D = query.shape
     Hkv = key.shape[1]
@@ -706,7 +703,6 @@ def pa_move_blocks(key_caches, value_caches, block_pairs, block_tables=None, sta
     """Moves block `from` to block `to` for each row (from, to) of block_pairs (int32 [n, 2]
     on the device, ascending `from`) in every layer's pools (lists of [NB, Hkv, bs, D]
     tensors), and rewrites block_tables (int32 [rows, max_blocks] on the device)."""
-    import torch
     c = _Call()
     L = len(key_caches)
     if L == 0 or len(value_caches) != L:
@@ -768,7 +764,6 @@ def pa_tree_accept(accepted, num_accepted, next_tokens, new_lens, draft_tokens, 
     """The path of each tree that the model's choices accept: accepted int32 [S, max_accepted],
     num_accepted int32 [S], next_tokens int64 [S], new_lens int32 [S] (may be context_lens), from
     draft_tokens / target_tokens int64 [T] and tree_mask int32 [T, words]."""
-    import torch
     i32, i64 = torch.int32, torch.int64
     c = _Call()
     T, S = draft_tokens.shape[0], context_lens.shape[0]
@@ -793,7 +788,6 @@ def pa_move_tokens(key_caches, value_caches, block_tables, new_lens, accepted, n
     """Moves the rows of the accepted tokens together in every layer's pools (lists of
     [NB, Hkv, bs, D] tensors): position b + accepted[s][j] to b + j, b = new_lens[s] -
     num_accepted[s]."""
-    import torch
     i32 = torch.int32
     c = _Call()
     L = len(key_caches)
@@ -810,11 +804,7 @@ def pa_move_tokens(key_caches, value_caches, block_tables, new_lens, accepted, n
     dt = PA_FP8_E4M3 if k0.element_size() == 1 else _dt(k0)
     if dt == PA_FP8_E4M3:
         c.pool8(k0, "pool")
-    pools = array.array("Q")
-    for t in (*key_caches, *value_caches):
-        if t.shape != shape:
-            raise ValueError("move_tokens: the pools must have one shape and type")
-        pools.append(c.ptr(t, "pool", pt))
+    pools = c.pools((*key_caches, *value_caches), shape, pt)
     base = pools.buffer_info()[0]
     _check(_lib.pa_move_tokens(
         base, base + 8 * L, L, c.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
@@ -828,7 +818,6 @@ def pa_key_bounds(bounds, bound_steps, key_cache, block_tables, context_lens, ma
     """Bounds of the keys of the blocks that hold each sequence's last tokens: max_new_tokens each,
     or query_starts[s + 1] - query_starts[s] of them.  bounds int8 [NB, Hkv, 2, D] (largest, then
     smallest), bound_steps fp32 [NB, Hkv]."""
-    import torch
     i32 = torch.int32
     c = _Call()
     NB, Hkv, bs, D = key_cache.shape
@@ -871,7 +860,6 @@ def pa_select_blocks(selected, query, bounds, bound_steps, block_tables, context
                      stream=None):
     """The blocks that each query token and kv head reads: selected int32 [S, q_len, Hkv, n] (or
     [S, Hkv, n]), ascending, then -1; query [S, q_len, Hq, D] (or [S, Hq, D])."""
-    import torch
     i32 = torch.int32
     c = _Call()
     S, QL, Hq, D = _rows4(query, "query")
@@ -901,7 +889,6 @@ def pa_decode_sparse_workspace_size(num_seqs, q_len, num_q_heads, num_kv_heads, 
 
 def _sparse(fn, pool, scales, out, query, key_cache, value_cache, block_tables, context_lens, selected,
             scale, workspace, status, stream):
-    import torch
     i32 = torch.int32
     c = _Call()
     S, QL, Hq, D = _rows4(query, "query")
@@ -947,7 +934,6 @@ def pa_decode_sparse_fp8(out, query, key_cache, value_cache, block_tables, conte
 
 def pa_selftest_wait_timeout(status, limit_us: int, stream=None):
     """Runs the bounded-wait self-test kernel; sets PA_DEVERR_TIMEOUT in `status`."""
-    import torch
     _check(_lib.pa_selftest_wait_timeout(_dev(status, "status", torch.int32), int(limit_us),
                                          _stream(stream)))
 
