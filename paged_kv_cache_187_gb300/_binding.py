@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -527,6 +528,11 @@ _current_device, _current_stream = (getattr(torch._C, "_cuda_getDevice", None),
                                     getattr(torch._C, "_cuda_getCurrentRawStream", None))
 
 
+_shape_of, _dtype_of = operator.attrgetter("shape"), operator.attrgetter("dtype")
+_is_contiguous, _device_of, _address_of = (torch.Tensor.is_contiguous, torch.Tensor.get_device,
+                                           torch.Tensor.data_ptr)
+
+
 class _Call:
     """The device and stream of one call, and its tensors' addresses.  The library launches on
     the current device, so every tensor has to live there."""
@@ -558,14 +564,14 @@ class _Call:
 
     def pools(self, tensors, shape, dtype):
         """The addresses of layers' pools, which have one shape and type."""
-        dev, got = self.dev, array.array("Q")
-        for t in tensors:
-            if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-                if t.shape != shape:
-                    raise ValueError("the pools must have one shape and type")
+        n = len(tensors)
+        if list(map(_shape_of, tensors)).count(shape) != n:
+            raise ValueError("the pools must have one shape and type")
+        if (list(map(_dtype_of, tensors)).count(dtype) != n or not all(map(_is_contiguous, tensors))
+                or list(map(_device_of, tensors)).count(self.dev) != n):
+            for t in tensors:
                 self.ptr(t, "pool", dtype)
-            got.append(t.data_ptr())
-        return got
+        return array.array("Q", map(_address_of, tensors))
 
     def pool8(self, t, name):
         """An fp8 E4M3 pool: a uint8 or float8_e4m3fn tensor."""

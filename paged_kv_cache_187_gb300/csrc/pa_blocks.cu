@@ -219,23 +219,29 @@ __device__ __forceinline__ int32_t blocks_of(const SelectParams& p, int32_t len,
 //     P = sum_j max(p_j, 0), N = sum_j min(p_j, 0),
 // however many heads.  D / 16 lanes take a (query token, kv head), 16 dims each, and write its
 // weights, 16 bits each: P of 16 dims, then N, lane by lane.
-constexpr int kWeightThreads = 128;
+
+// What takes the queries of a group, the largest of magnitude `most`, to whole numbers of at most 64
+// (an infinity counts as the largest number, which comes to 64 as well).
+template <bool BF16>
+__device__ __forceinline__ float weight_scale(float most) {
+    constexpr float kBig = BF16 ? 3.38953139e38f : 65504.f;
+    return power_of_two(5 - exponent_of(fminf(most, kBig)));
+}
+__device__ __forceinline__ int32_t weight_of(float v, float scale) {
+    return __float2int_rn(fminf(fmaxf(v * scale, -64.f), 64.f));
+}
+
+// The weights of dims 16 c .. of a row's group of queries (`q`: the row's queries, dims 16 c on), by
+// D / 16 lanes together.
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kWeightThreads) select_weights_kernel(const SelectParams p) {
+__device__ __forceinline__ void group_weights(const uint4* q, int32_t group, uint32_t (&w)[16]) {
     constexpr int kLanes = D / 16;
-    grid_dependency_wait();
-    allow_dependent_launch();      // (after the wait: the scores read all but the weights early)
-    const int64_t row = ((int64_t)blockIdx.x * kWeightThreads + threadIdx.x) / kLanes;   // token and head
-    const int32_t c = threadIdx.x % kLanes;
-    const int64_t rows = (int64_t)p.num_seqs * p.q_len * p.num_kv_heads;
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) +
-                                                    min(row, rows - 1) * p.group * D + c * 16);
     // four heads' rows at once (those past the group: the last one's again, not counted)
     uint4 x[4][2];
     auto load = [&](int32_t g0) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int32_t g = min(g0 + k, p.group - 1);
+            const int32_t g = min(g0 + k, group - 1);
             x[k][0] = q[g * (D / 8)];
             x[k][1] = q[g * (D / 8) + 1];
         }
@@ -252,37 +258,49 @@ __global__ void __launch_bounds__(kWeightThreads) select_weights_kernel(const Se
         }
     };
     float most = 0.f;
-    for (int32_t g0 = 0; g0 < p.group; g0 += 4) {
+    for (int32_t g0 = 0; g0 < group; g0 += 4) {
         load(g0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) each(k, [&](int, float v) { most = fmaxf(most, fabsf(v)); });
     }
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    // (an infinity counts as the largest number, which comes to 64 as well)
-    constexpr float kBig = BF16 ? 3.38953139e38f : 65504.f;
-    const float inv = power_of_two(5 - exponent_of(fminf(most, kBig)));
+    const float inv = weight_scale<BF16>(most);
     int32_t up[16], down[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) up[i] = down[i] = 0;
-    for (int32_t g0 = 0; g0 < p.group; g0 += 4) {
-        if (p.group > 4) load(g0);
+    for (int32_t g0 = 0; g0 < group; g0 += 4) {
+        if (group > 4) load(g0);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (g0 + k < p.group)
+            if (g0 + k < group)
                 each(k, [&](int i, float v) {
-                    const int32_t z = __float2int_rn(fminf(fmaxf(v * inv, -64.f), 64.f));
+                    const int32_t z = weight_of(v, inv);
                     up[i] += max(z, 0);
                     down[i] += min(z, 0);
                 });
     }
-    if (row >= rows) return;
-    uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         w[i] = (uint32_t)((up[2 * i] & 0xFFFF) | (up[2 * i + 1] << 16));
         w[8 + i] = (uint32_t)((down[2 * i] & 0xFFFF) | (down[2 * i + 1] << 16));
     }
+}
+
+constexpr int kWeightThreads = 128;
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kWeightThreads) select_weights_kernel(const SelectParams p) {
+    constexpr int kLanes = D / 16;
+    grid_dependency_wait();
+    allow_dependent_launch();      // (after the wait: the scores read all but the weights early)
+    const int64_t row = ((int64_t)blockIdx.x * kWeightThreads + threadIdx.x) / kLanes;   // token and head
+    const int32_t c = threadIdx.x % kLanes;
+    const int64_t rows = (int64_t)p.num_seqs * p.q_len * p.num_kv_heads;
+    uint32_t w[16];
+    group_weights<BF16, D>(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) +
+                                                          min(row, rows - 1) * p.group * D + c * 16),
+                           p.group, w);
+    if (row >= rows) return;
     uint4* out = reinterpret_cast<uint4*>(p.weights + (row * kLanes + c) * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
@@ -290,6 +308,55 @@ __global__ void __launch_bounds__(kWeightThreads) select_weights_kernel(const Se
 
 constexpr int kScoreThreads = 256;
 constexpr int kScoreBatch = 4;            // records that a lane has on their way
+
+// Four records of a lane, 16 dims each: upper and lower bounds; the step of the one whose score the
+// lane ends up with (0: a block outside the pool).
+struct ScoreBatch {
+    uint4 x[kScoreBatch][2];
+    float step;
+};
+
+// Which of four records a lane ends up with.
+template <int D>
+__device__ __forceinline__ int32_t record_of(int32_t c) {
+    return (c / (D / 64)) & 3;
+}
+
+// The scores of four records against weights P (wp) and N (wn), D / 16 lanes together (every lane of
+// the warp comes here), in an order that unsigned numbers keep: record record_of(c)'s in lane c.
+template <int D>
+__device__ __forceinline__ uint32_t score_batch(const ScoreBatch& y, const int32_t (&wp)[8], const int32_t (&wn)[8],
+                                                int32_t c) {
+    int32_t dot[kScoreBatch];
+#pragma unroll
+    for (int k = 0; k < kScoreBatch; ++k) {
+        int32_t a = 0, b = 0;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const uint4 &v = y.x[k][0], &z = y.x[k][1];
+            const int32_t hi = (int32_t)(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w);
+            const int32_t lo = (int32_t)(m == 0 ? z.x : m == 1 ? z.y : m == 2 ? z.z : z.w);
+            a = __dp2a_lo(wp[2 * m], hi, a);
+            b = __dp2a_hi(wp[2 * m + 1], hi, b);
+            a = __dp2a_lo(wn[2 * m], lo, a);
+            b = __dp2a_hi(wn[2 * m + 1], lo, b);
+        }
+        dot[k] = a + b;
+    }
+    // the lanes' sums: half of the lanes go on with records 2, 3, then with the odd one
+    constexpr int kHalf = D / 32, kQuarter = D / 64;
+    const bool top = c & kHalf, odd = c & kQuarter;
+    int32_t a = top ? dot[2] : dot[0], b = top ? dot[3] : dot[1];
+    a += __shfl_xor_sync(0xffffffffu, top ? dot[0] : dot[2], kHalf);
+    b += __shfl_xor_sync(0xffffffffu, top ? dot[1] : dot[3], kHalf);
+    int32_t d = odd ? b : a;
+    d += __shfl_xor_sync(0xffffffffu, odd ? a : b, kQuarter);
+#pragma unroll
+    for (int o = kQuarter / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    const float f = (float)d * y.step;
+    const uint32_t bits = __float_as_uint(f);
+    return f != f ? 0xffffffffu : (bits >> 31) ? ~bits : bits | 0x80000000u;
+}
 
 // Blocks of a sequence with scores: the last query token's, without the first and last ones.
 __device__ __forceinline__ int32_t scored_of(const SelectParams& p, int32_t s) {
@@ -367,15 +434,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const Se
         const bool mine = sub < subs && h < p.num_kv_heads;
         const int32_t head = mine ? h : 0;
         // the record whose score this lane ends up with, of four
-        const int32_t u = (c / (kLanes / 4)) & 3;
+        const int32_t u = record_of<D>(c);
         const int8_t* const at = p.bounds + c * 16;
-        // Four records of this lane, from place `first` on, on their way (past the end: the last
-        // one again).
-        struct Batch {
-            uint4 x[kScoreBatch][2];
-            float step;
-        };
-        auto fetch = [&](int32_t first, Batch& t) {
+        // four records of this lane, from place `first` on (past the end: the last one again)
+        auto fetch = [&](int32_t first, ScoreBatch& t) {
             int32_t rec[kScoreBatch];
 #pragma unroll
             for (int k = 0; k < kScoreBatch; ++k) rec[k] = rec_s[min(first + k * subs, n - 1)];
@@ -390,7 +452,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const Se
             if (r < 0) t.step = 0.f;
         };
         const int32_t stride = kScoreBatch * subs;
-        Batch one, two;
+        ScoreBatch one, two;
         fetch(sub, one);
         if (!waited) {
             grid_dependency_wait();
@@ -412,42 +474,13 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const Se
             }
             uint32_t* const keys =
                 p.keys + (((size_t)s * p.q_len + j0) * p.num_kv_heads + head) * p.max_blocks + b0;
-            auto score = [&](int32_t first, const Batch& y) {
+            auto score = [&](int32_t first, const ScoreBatch& y) {
                 const int32_t i = first + u * subs;
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
-                    int32_t dot[kScoreBatch];
-#pragma unroll
-                    for (int k = 0; k < kScoreBatch; ++k) {
-                        int32_t a = 0, b = 0;
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const uint4 &v = y.x[k][0], &z = y.x[k][1];
-                            const int32_t hi = (int32_t)(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w);
-                            const int32_t lo = (int32_t)(m == 0 ? z.x : m == 1 ? z.y : m == 2 ? z.z : z.w);
-                            a = __dp2a_lo(wp[t][2 * m], hi, a);
-                            b = __dp2a_hi(wp[t][2 * m + 1], hi, b);
-                            a = __dp2a_lo(wn[t][2 * m], lo, a);
-                            b = __dp2a_hi(wn[t][2 * m + 1], lo, b);
-                        }
-                        dot[k] = a + b;
-                    }
-                    // the lanes' sums: half of the lanes go on with records 2, 3, then with the odd one
-                    constexpr int kHalf = kLanes / 2, kQuarter = kLanes / 4;
-                    const bool top = c & kHalf, odd = c & kQuarter;
-                    int32_t a = top ? dot[2] : dot[0], b = top ? dot[3] : dot[1];
-                    a += __shfl_xor_sync(0xffffffffu, top ? dot[0] : dot[2], kHalf);
-                    b += __shfl_xor_sync(0xffffffffu, top ? dot[1] : dot[3], kHalf);
-                    int32_t d = odd ? b : a;
-                    d += __shfl_xor_sync(0xffffffffu, odd ? a : b, kQuarter);
-#pragma unroll
-                    for (int o = kQuarter / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                    if (mine && c % kQuarter == 0 && i < n && j0 + t < p.q_len) {
-                        const float f = (float)d * y.step;
-                        const uint32_t bits = __float_as_uint(f);
-                        keys[(size_t)t * p.num_kv_heads * p.max_blocks + i] =
-                            f != f ? 0xffffffffu : (bits >> 31) ? ~bits : bits | 0x80000000u;
-                    }
+                    const uint32_t key = score_batch<D>(y, wp[t], wn[t], c);
+                    if (mine && c % (kLanes / 4) == 0 && i < n && j0 + t < p.q_len)
+                        keys[(size_t)t * p.num_kv_heads * p.max_blocks + i] = key;
                 }
             };
             // (a warp's groups go through the steps together: its shuffles need every lane)
@@ -498,44 +531,39 @@ __device__ __forceinline__ int32_t scan_cta(int32_t x, int32_t* buf, int32_t* to
     return before;
 }
 
-// CTA (query token, kv head): the `want` largest of its row's scores.  A histogram over the
-// scores' own range (2048 bins, so that the counts spread) finds the bin that holds the smallest
-// of them; what is in that bin is ranked one against the other, or, where that is more than there
-// are threads, the range is narrowed to the bin and divided again, until one value is left, of
-// which the first blocks are taken.  What is taken is a bit per block, which puts the list in
-// order.  Bound by latency: the passes over at most 16 keys a thread and the scans between them.
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectParams p) {
-    extern __shared__ uint32_t sel_smem[];
-    __shared__ int32_t buf[32];
-    __shared__ __align__(16) int32_t hist[kSelBins];
-    __shared__ uint32_t range[2];             // the scores' least and greatest
-    __shared__ int32_t found[2];              // the bin, and the scores above it
-    __shared__ int32_t gathered;
+// The `want` largest of a row's scores, by one CTA.  A histogram over the scores' own range (2048
+// bins, so that the counts spread) finds the bin that holds the smallest of them; what is in that
+// bin is ranked one against the other, or, where that is more than there are threads, the range is
+// narrowed to the bin and divided again, until one value is left, of which the first blocks are
+// taken.  What is taken is a bit per block, which puts the list in order.  Bound by latency: the
+// passes over at most 16 keys a thread and the scans between them.
+struct SelectSmem {
+    int32_t buf[32];
+    alignas(16) int32_t hist[kSelBins];
+    uint32_t range[2];             // the scores' least and greatest
+    int32_t found[2];              // the bin, and the scores above it
+    int32_t gathered;
     static_assert(2 * kSelThreads <= kSelBins, "the candidates take the histogram's place");
+};
+
+// Before select_row, and a barrier.
+__device__ __forceinline__ void select_clear(SelectSmem& sm) {
+    for (int32_t i = threadIdx.x; i < kSelBins; i += kSelThreads) sm.hist[i] = 0;
+    if (threadIdx.x == 0) {
+        sm.range[0] = 0xffffffffu;
+        sm.range[1] = 0u;
+        sm.gathered = 0;
+    }
+}
+
+// keys[i]: block i's score, of the blocks from num_first on and before the last num_last of the
+// row's `blocks`; `bits`: two bits of shared memory per block.
+__device__ __forceinline__ void select_row(const SelectParams& p, int32_t blocks, const uint32_t* keys,
+                                           uint32_t* bits_smem, SelectSmem& sm, int32_t* out) {
     const int32_t tid = threadIdx.x, lane = tid & 31;
-    // (where scores come first, the kernel that writes the weights has waited for all before it)
-    if (p.max_blocks <= p.num_selected) grid_dependency_wait();
-    const int64_t row = (int64_t)blockIdx.x * p.num_kv_heads + blockIdx.y;
-    const int32_t s = (int32_t)(blockIdx.x / p.q_len), j = (int32_t)(blockIdx.x % p.q_len);
-    const int32_t blocks = blocks_of(p, context_of(p, s, false), j);
-    for (int32_t i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-    if (tid == 0) {
-        range[0] = 0xffffffffu;
-        range[1] = 0u;
-        gathered = 0;
-    }
-    __syncthreads();
-    grid_dependency_wait();
-    allow_dependent_launch();
-    int32_t* out = p.selected + row * p.num_selected;
-    if (blocks <= p.num_selected) {
-        for (int32_t i = tid; i < p.num_selected; i += kSelThreads) out[i] = i < blocks ? i : -1;
-        return;
-    }
     const int32_t words = (blocks + 31) / 32;
-    uint32_t* const take = sel_smem;
-    uint32_t* const tie = sel_smem + (p.max_blocks + 31) / 32;
-    const uint32_t* keys = p.keys + row * p.max_blocks;
+    uint32_t* const take = bits_smem;
+    uint32_t* const tie = bits_smem + (p.max_blocks + 31) / 32;
     const int32_t m0 = p.num_first, m1 = blocks - p.num_last;    // scored blocks: m0 .. m1 - 1
     int32_t want = p.num_selected - p.num_first - p.num_last;
     const int32_t rounds = (blocks + kSelThreads - 1) / kSelThreads;
@@ -563,12 +591,12 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) {
-        atomicMin(&range[0], lo);
-        atomicMax(&range[1], hi);
+        atomicMin(&sm.range[0], lo);
+        atomicMax(&sm.range[1], hi);
     }
     __syncthreads();
-    lo = range[0];
-    hi = range[1];
+    lo = sm.range[0];
+    hi = sm.range[1];
     // Narrow lo .. hi until all of it is taken (`all`), few enough of it are left to be ranked
     // (`rank`), or one value is; `want` of it are taken.
     bool all = want == 0, rank = false;
@@ -576,11 +604,11 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     for (bool again = false; !all && !rank && lo < hi; again = true) {
         const int32_t shift = max(0, 21 - __clz(hi - lo));
         if (again) {
-            for (int32_t i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+            for (int32_t i = tid; i < kSelBins; i += kSelThreads) sm.hist[i] = 0;
             __syncthreads();
         }
         each([&](int32_t, uint32_t k) {
-            if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1);
+            if (k >= lo && k <= hi) atomicAdd(&sm.hist[(k - lo) >> shift], 1);
         });
         __syncthreads();
         // bins from the top: thread t has the bins that end at kSelBins - 1 - 4 t
@@ -588,23 +616,23 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
         int32_t mine = 0, n[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            n[k] = hist[kSelBins - 1 - (tid * kPer + k)];
+            n[k] = sm.hist[kSelBins - 1 - (tid * kPer + k)];
             mine += n[k];
         }
-        int32_t total, above = scan_cta(mine, buf, &total);
+        int32_t total, above = scan_cta(mine, sm.buf, &total);
         if (above < want && want <= above + mine) {
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 if (above < want && want <= above + n[k]) {
-                    found[0] = kSelBins - 1 - (tid * kPer + k);
-                    found[1] = above;
+                    sm.found[0] = kSelBins - 1 - (tid * kPer + k);
+                    sm.found[1] = above;
                 }
                 above += n[k];
             }
         }
         __syncthreads();
-        const int32_t bin = found[0], here = hist[bin];
-        want -= found[1];
+        const int32_t bin = sm.found[0], here = sm.hist[bin];
+        want -= sm.found[1];
         all = here == want;
         rank = !all && here <= kSelThreads;
         lo += (uint32_t)bin << shift;
@@ -613,7 +641,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     }
     // the bits: everything above the range, and the range itself if all of it is taken; what is
     // to be ranked goes to a list, what is equal to bits of its own
-    uint2* const cand = reinterpret_cast<uint2*>(hist);
+    uint2* const cand = reinterpret_cast<uint2*>(sm.hist);
     auto mark = [&](int32_t i, uint32_t k, bool scored) {
         const bool here = scored && want > 0 && k >= lo && k <= hi;
         const bool in = i < blocks && (!scored || (want > 0 && k > hi) || (here && all));
@@ -623,7 +651,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
             const uint32_t e = __ballot_sync(0xffffffffu, here);
             if (lane == 0 && (i >> 5) < words) tie[i >> 5] = e;
         } else if (here && rank) {
-            cand[atomicAdd(&gathered, 1)] = make_uint2(k, (uint32_t)i);
+            cand[atomicAdd(&sm.gathered, 1)] = make_uint2(k, (uint32_t)i);
         }
     };
 #pragma unroll
@@ -640,7 +668,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     }
     __syncthreads();
     if (rank) {
-        const int32_t n = gathered;
+        const int32_t n = sm.gathered;
         if (tid < n) {
             const uint2 me = cand[tid];
             int32_t better = 0;
@@ -660,17 +688,159 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
         int32_t total;
         if (!all && !rank) {
             uint32_t e = w < words ? tie[w] : 0u;
-            const int32_t before = ties + scan_cta(__popc(e), buf, &total);
+            const int32_t before = ties + scan_cta(__popc(e), sm.buf, &total);
             ties += total;
             for (int32_t left = want - before; e && left > 0; --left) {
                 bits |= e & (0u - e);
                 e &= e - 1u;
             }
         }
-        int32_t to = at + scan_cta(__popc(bits), buf, &total);
+        int32_t to = at + scan_cta(__popc(bits), sm.buf, &total);
         at += total;
         for (; bits; bits &= bits - 1u) out[to++] = 32 * w + __ffs(bits) - 1;
     }
+}
+
+// CTA (query token, kv head): the selection from scores in memory.
+__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectParams p) {
+    extern __shared__ uint32_t sel_smem[];
+    __shared__ SelectSmem sm;
+    // (the kernel that writes the weights has waited for all that comes before this call)
+    const int64_t row = (int64_t)blockIdx.x * p.num_kv_heads + blockIdx.y;
+    const int32_t s = (int32_t)(blockIdx.x / p.q_len), j = (int32_t)(blockIdx.x % p.q_len);
+    const int32_t blocks = blocks_of(p, context_of(p, s, false), j);
+    select_clear(sm);
+    __syncthreads();
+    grid_dependency_wait();
+    allow_dependent_launch();
+    int32_t* out = p.selected + row * p.num_selected;
+    if (blocks <= p.num_selected) {
+        for (int32_t i = threadIdx.x; i < p.num_selected; i += kSelThreads) out[i] = i < blocks ? i : -1;
+        return;
+    }
+    select_row(p, blocks, p.keys + row * p.max_blocks, sel_smem, sm, out);
+}
+
+// Short contexts: the same in one launch, CTA (query token, kv head).  The first warp takes the
+// weights, four dims to a lane, while the others' first records come; D / 16 lanes score four blocks
+// at a time into shared memory.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kSelThreads) select_short_kernel(const SelectParams p) {
+    constexpr int kLanes = D / 16, kGroups = kSelThreads / kLanes;
+    extern __shared__ uint32_t sel_smem[];      // two bits per block, then the scores
+    __shared__ SelectSmem sm;
+    __shared__ __align__(16) uint32_t weights[kLanes][16];
+    select_clear(sm);
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int32_t tid = threadIdx.x, lane = tid & 31, c = tid % kLanes, grp = tid / kLanes, h = blockIdx.y;
+    const int64_t row = (int64_t)blockIdx.x * p.num_kv_heads + h;
+    const int32_t s = (int32_t)(blockIdx.x / p.q_len), j = (int32_t)(blockIdx.x % p.q_len);
+    // (the first blocks' table entries, the queries and the length are on their way together; an
+    // entry past the context is not used)
+    const int32_t first = p.num_first, u = record_of<D>(c);
+    const int32_t* const table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+    int32_t phys[kScoreBatch];
+    auto entries = [&](int32_t i0) {
+#pragma unroll
+        for (int k = 0; k < kScoreBatch; ++k)
+            phys[k] = table[min(first + i0 + k * kGroups + grp, p.max_blocks_per_seq - 1)];
+    };
+    auto fetch = [&](ScoreBatch& y) {           // (a block outside the pool: the first one's, times 0)
+#pragma unroll
+        for (int k = 0; k < kScoreBatch; ++k) {
+            const bool out_of = phys[k] < 0 || phys[k] >= p.num_blocks;
+            const size_t rec = (size_t)(out_of ? 0 : phys[k]) * p.num_kv_heads + h;
+            const int8_t* src = p.bounds + rec * 2 * D + c * 16;
+            y.x[k][0] = __ldg(reinterpret_cast<const uint4*>(src));
+            y.x[k][1] = __ldg(reinterpret_cast<const uint4*>(src + D));
+            if (k == u) {
+                y.step = __ldg(p.steps + rec);
+                if (out_of) y.step = 0.f;
+            }
+        }
+    };
+    entries(0);
+    const int32_t blocks = blocks_of(p, context_of(p, s, tid == 0 && h == 0 && j == 0), j);
+    int32_t* out = p.selected + row * p.num_selected;
+    if (blocks <= p.num_selected) {
+        for (int32_t i = tid; i < p.num_selected; i += kSelThreads) out[i] = i < blocks ? i : -1;
+        return;
+    }
+    const int32_t n = blocks - p.num_first - p.num_last;
+    ScoreBatch y;
+    fetch(y);
+    if (tid < 32) {
+        // dims 4 lane .. of the group's heads, four heads at a time
+        const bool here = 4 * lane < D;
+        const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.query) + row * p.group * D) +
+                         (here ? lane : 0);
+        float v[4][4], most = 0.f;
+        auto load = [&](int32_t g0) {
+            uint2 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = q[min(g0 + k, p.group - 1) * (D / 4)];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                unpack2<BF16>(x[k].x, v[k][0], v[k][1]);
+                unpack2<BF16>(x[k].y, v[k][2], v[k][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[k][i] = v[k][i] == v[k][i] ? v[k][i] : 0.f;      // (NaN: 0)
+            }
+        };
+        for (int32_t g0 = 0; g0 < p.group; g0 += 4) {
+            load(g0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(v[k][i]));
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const float inv = weight_scale<BF16>(most);
+        int32_t up[4] = {0, 0, 0, 0}, down[4] = {0, 0, 0, 0};
+        for (int32_t g0 = 0; g0 < p.group; g0 += 4) {
+            if (p.group > 4) load(g0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t z = g0 + k < p.group ? weight_of(v[k][i], inv) : 0;
+                    up[i] += max(z, 0);
+                    down[i] += min(z, 0);
+                }
+        }
+        if (here) {
+            uint32_t* const w = &weights[lane / 4][2 * (lane & 3)];
+            w[0] = (uint32_t)((up[0] & 0xFFFF) | (up[1] << 16));
+            w[1] = (uint32_t)((up[2] & 0xFFFF) | (up[3] << 16));
+            w[8] = (uint32_t)((down[0] & 0xFFFF) | (down[1] << 16));
+            w[9] = (uint32_t)((down[2] & 0xFFFF) | (down[3] << 16));
+        }
+    }
+    __syncthreads();
+    int32_t wp[8], wn[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int4 a = reinterpret_cast<const int4*>(weights[c])[i], b = reinterpret_cast<const int4*>(weights[c])[2 + i];
+        wp[4 * i] = a.x, wp[4 * i + 1] = a.y, wp[4 * i + 2] = a.z, wp[4 * i + 3] = a.w;
+        wn[4 * i] = b.x, wn[4 * i + 1] = b.y, wn[4 * i + 2] = b.z, wn[4 * i + 3] = b.w;
+    }
+    uint32_t* const keys = sel_smem + 2 * ((p.max_blocks + 31) / 32);
+    bool bad = false;
+    for (int32_t i0 = 0; i0 < n; i0 += kScoreBatch * kGroups) {
+        if (i0 > 0) fetch(y);
+#pragma unroll
+        for (int k = 0; k < kScoreBatch; ++k)
+            bad |= (phys[k] < 0 || phys[k] >= p.num_blocks) && i0 + k * kGroups + grp < n;
+        entries(i0 + kScoreBatch * kGroups);
+        const uint32_t key = score_batch<D>(y, wp, wn, c);
+        const int32_t i = i0 + u * kGroups + grp;
+        if (c % (kLanes / 4) == 0 && i < n) keys[first + i] = key;
+    }
+    if (bad && p.status) atomicOr(p.status, kDevBadBlock);
+    __syncthreads();
+    select_row(p, blocks, keys, sel_smem, sm, out);
 }
 
 template <class Arg>
@@ -711,26 +881,30 @@ cudaError_t launch_key_bounds(const BoundsParams& p, BoundsType type, cudaStream
 
 cudaError_t launch_select_blocks(const SelectParams& p, bool bf16, cudaStream_t stream) {
     using Kern = void (*)(SelectParams);
-    const bool one = p.q_len == 1, wide = p.head_size == 128;
-    if (p.max_blocks > p.num_selected) {
-        const Kern weights = bf16 ? (wide ? (Kern)select_weights_kernel<true, 128> : (Kern)select_weights_kernel<true, 64>)
-                                  : (wide ? (Kern)select_weights_kernel<false, 128> : (Kern)select_weights_kernel<false, 64>);
-        const Kern scores = wide ? (one ? (Kern)block_scores_kernel<128, 1> : (Kern)block_scores_kernel<128, 2>)
-                                 : (one ? (Kern)block_scores_kernel<64, 1> : (Kern)block_scores_kernel<64, 2>);
-        const int64_t lanes = (int64_t)p.num_seqs * p.q_len * p.num_kv_heads * (p.head_size / 16);
-        cudaError_t e = launch_pdl(dim3((unsigned)((lanes + kWeightThreads - 1) / kWeightThreads)),
-                                   dim3(kWeightThreads), 0, stream, weights, p);
-        if (e != cudaSuccess) return e;
-        const int32_t heads = std::min(p.num_kv_heads, kScoreThreads / (p.head_size / 16));
-        // two CTAs to an SM, but none with fewer than 32 blocks of the longest contexts
-        const int64_t most = (int64_t)p.num_seqs * ((p.num_kv_heads + heads - 1) / heads) * p.max_blocks;
-        e = launch_pdl(dim3((unsigned)std::max<int64_t>(std::min<int64_t>(2 * p.sms, most / 32), 1)),
-                       dim3(kScoreThreads), 0, stream, scores, p);
-        if (e != cudaSuccess) return e;
+    const bool wide = p.head_size == 128;
+    const dim3 rows((unsigned)(p.num_seqs * p.q_len), (unsigned)p.num_kv_heads);
+    const size_t bits = 2 * sizeof(uint32_t) * (size_t)((p.max_blocks + 31) / 32);
+    if (!p.keys) {
+        const Kern kern = bf16 ? (wide ? (Kern)select_short_kernel<true, 128> : (Kern)select_short_kernel<true, 64>)
+                               : (wide ? (Kern)select_short_kernel<false, 128> : (Kern)select_short_kernel<false, 64>);
+        return launch_pdl(rows, dim3(kSelThreads), bits + sizeof(uint32_t) * (size_t)p.max_blocks, stream, kern, p);
     }
-    const size_t smem = 2 * sizeof(uint32_t) * (size_t)((p.max_blocks + 31) / 32);
-    return launch_pdl(dim3((unsigned)(p.num_seqs * p.q_len), (unsigned)p.num_kv_heads), dim3(kSelThreads), smem,
-                      stream, select_blocks_kernel, p);
+    const bool one = p.q_len == 1;
+    const Kern weights = bf16 ? (wide ? (Kern)select_weights_kernel<true, 128> : (Kern)select_weights_kernel<true, 64>)
+                              : (wide ? (Kern)select_weights_kernel<false, 128> : (Kern)select_weights_kernel<false, 64>);
+    const Kern scores = wide ? (one ? (Kern)block_scores_kernel<128, 1> : (Kern)block_scores_kernel<128, 2>)
+                             : (one ? (Kern)block_scores_kernel<64, 1> : (Kern)block_scores_kernel<64, 2>);
+    const int64_t lanes = (int64_t)p.num_seqs * p.q_len * p.num_kv_heads * (p.head_size / 16);
+    cudaError_t e = launch_pdl(dim3((unsigned)((lanes + kWeightThreads - 1) / kWeightThreads)), dim3(kWeightThreads), 0,
+                               stream, weights, p);
+    if (e != cudaSuccess) return e;
+    const int32_t heads = std::min(p.num_kv_heads, kScoreThreads / (p.head_size / 16));
+    // two CTAs to an SM, but none with fewer than 32 blocks of the longest contexts
+    const int64_t most = (int64_t)p.num_seqs * ((p.num_kv_heads + heads - 1) / heads) * p.max_blocks;
+    e = launch_pdl(dim3((unsigned)std::max<int64_t>(std::min<int64_t>(2 * p.sms, most / 32), 1)), dim3(kScoreThreads), 0,
+                   stream, scores, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(rows, dim3(kSelThreads), bits, stream, select_blocks_kernel, p);
 }
 
 }  // namespace pa

@@ -268,8 +268,16 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "select_blocks: device");
     p.sms = sms;
-    p.weights = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.weights);
-    p.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.keys);
+    // One launch, a CTA per row, where an SM has one row of a thousand blocks at most (1 sequence of 200
+    // / 1000 / 2000 blocks, 8 kv heads: 7.4 / 10 / 13 us, in three launches 9.6 / 9.9 / 10.4; 19
+    // sequences 7.8 / 11.3 / 17.3 and 12.9 / 14 / 18.6; 32, whose rows come in two turns, 14.1 and 13.7
+    // at 200; every launch is 2 us of host time too).
+    const bool one_launch = blocks <= num_selected ||
+                            (blocks <= 1024 && (int64_t)num_seqs * q_len * num_kv_heads <= sms);
+    if (!one_launch) {
+        p.weights = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.weights);
+        p.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.keys);
+    }
     p.status = status_dev;
     e = pa::launch_select_blocks(p, dtype == PA_BF16, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "select_blocks launch");

@@ -187,6 +187,15 @@ def test_selection(cuda_device, q_len, Hq, Hkv, D, bs, dtype, keep, first, last)
     select_check(b, out, keep, first, last)
 
 
+@pytest.mark.parametrize("seqs", [2, 40])
+@pytest.mark.parametrize("q_len,Hq,Hkv,D,dtype", [(1, 16, 4, 128, torch.bfloat16), (2, 14, 2, 64, torch.float16)])
+def test_one_launch_and_three_select_alike(cuda_device, seqs, q_len, Hq, Hkv, D, dtype):
+    """Few rows of short contexts take one launch, more rows or longer contexts three."""
+    for blocks in (1024, 1025, 300):
+        b = select_case([blocks * 16 - 5 - 7 * (i % 3) for i in range(seqs)], q_len, Hq, Hkv, D, 16, dtype, blocks)
+        select_check(dict(b, lens=b["lens"][:3]), select_call(b, 37, 2, 3), 37, 2, 3)
+
+
 @pytest.mark.parametrize("values", [1, 2, 5])
 def test_equal_scores_go_to_the_lowest_block(cuda_device, values):
     b = select_case([400, 5000, 9000, 20000, 1024], 1, 8, 2, 64, 16, torch.bfloat16, 3, values=values)
