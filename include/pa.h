@@ -591,8 +591,9 @@ pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_a
  * flagged PA_DEVERR_BAD_LEN.  key_caches / value_caches as for pa_move_blocks (PA_F16, PA_BF16 or
  * PA_FP8_E4M3, rows of a multiple of 16 bytes).  The blocks that new tokens sit in must not be
  * shared between sequences (pa_alloc_reserve_batch sees to that).  On the host: reserve the blocks
- * of the whole tree with pa_alloc_reserve_batch, take the slots from pa_alloc_slots, and append the
- * accepted tokens alone.  One launch per 64 layers. */
+ * of the whole tree with pa_alloc_reserve_batch, take the slots from the tables (position t's is
+ * table[t / block_size] * block_size + t % block_size), and append the accepted tokens alone.  One
+ * launch per 64 layers. */
 pa_status pa_move_tokens(void* const* key_caches, void* const* value_caches, int32_t num_layers,
                          const int32_t* block_tables, int32_t max_blocks_per_seq,
                          const int32_t* new_lens, const int32_t* accepted, int32_t max_accepted,
@@ -664,7 +665,7 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
  * A row of selected ascends; -1 entries are skipped, and entries that do not ascend or lie outside
  * the context are left out and flagged PA_DEVERR_BAD_BLOCK.  A row without tokens is a zero row.
  * Other arguments, limits and accuracy as for pa_decode_auto (num_seqs * q_len * num_kv_heads at
- * most 2^24, num_selected * block_size too).  The present kernels need no workspace: the size is 0
+ * most 2^24, num_selected at most 65536).  The present kernels need no workspace: the size is 0
  * and `workspace` may be NULL. */
 size_t pa_decode_sparse_workspace_size(int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
                                        int32_t num_kv_heads, int32_t head_size, int32_t block_size,

@@ -42,7 +42,9 @@ struct PfHeader {
     uint32_t cut;
     uint32_t shares;
     int64_t cost;           // all units'
-    uint32_t pad[58];
+    uint32_t lines;         // entries of `before`: row tiles, or pairs of them
+    uint32_t pairs;         // cut 1, trees: the lines are pairs of row tiles (see prefill_plan_kernel)
+    uint32_t pad[56];
 };
 
 struct PrefillParams {
@@ -63,8 +65,8 @@ struct PrefillParams {
     PfHeader* hdr;
     int4* seqs;                // [num_seqs] (q_start, q_len, len, first row tile)
     int32_t* seq_of;           // [row tiles] the sequence
-    int32_t* order;            // [row tiles] longest first
-    int64_t* before;           // [row tiles + 1] cost of the row tiles before, one kv head
+    int32_t* order;            // [row tiles] longest first; for pairs, the pair's first row tile
+    int64_t* before;           // [row tiles + 1] cost of the row tiles (pairs) before, one kv head
     int32_t* arrive;           // [CTAs][2 streams] finished partitions of the unit that a
                                // share leaves unfinished
     float2* part_ml;           // [CTAs][2][2 streams][128] (reference, weight sum): a share

@@ -150,6 +150,47 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
         __syncthreads();
     }
     const bool cut = longest > 1 && (whole - kPfCutCost) * shares > all;
+    // Trees of more than one row tile behind long contexts: two row tiles of a sequence read the same
+    // K and V, and laid end to end they would read it far apart in time, from memory both times.  So
+    // two neighbouring CTAs take the shares of a pair of row tiles, each its own, and keep in step:
+    // the second read comes from L2.  (A row tile left over leaves a CTA idle meanwhile; pairs are
+    // taken where that costs no more than a tenth.)  4 trees of 50-63 tokens, 8 heads to a kv head,
+    // behind 56-60 K: 370 us end to end, 330 in pairs; 415 and 362 at the power cap.
+    long long paired = 0;
+    int32_t lines = row_tiles;
+    auto pair_cost = [&](int32_t i) {          // of the pair that begins at row tile i, 0: none does
+        if (i >= row_tiles) return 0;
+        const int32_t s = p.seq_of[i];
+        if ((i - seq_at(s).w) & 1) return 0;
+        const bool two = i + 1 < row_tiles && p.seq_of[i + 1] == s;
+        return min(tiles_of(two ? i + 1 : i, s) + kPfItemCost, 1 << 21);
+    };
+    if (cut && p.tree_mask && p.grid > 1) {
+        __syncthreads();                       // seq_of
+        for (int32_t base = 0; base < row_tiles; base += kPlanThreads) {
+            int32_t sum;
+            (void)block_scan(pair_cost(base + tid), buf, &sum);
+            paired += sum;
+        }
+    }
+    const bool pairs = paired > 0 && 20 * paired <= 11 * cost;
+    if (pairs) {
+        long long before = 0;
+        lines = 0;
+        for (int32_t base = 0; base < row_tiles; base += kPlanThreads) {
+            const int32_t i = base + tid, n = pair_cost(i);
+            int32_t sum, count;
+            const int32_t at = block_scan(n, buf, &sum);
+            const int32_t place = lines + block_scan(n > 0 ? 1 : 0, buf, &count);
+            if (n > 0) {
+                p.before[place] = before + at;
+                p.order[place] = i;
+            }
+            before += sum;
+            lines += count;
+        }
+        if (tid == 0) p.before[lines] = before;
+    }
     if (!cut) {
         for (int32_t i = tid; i < row_tiles; i += kPlanThreads)
             p.order[atomicAdd(&first[bucket(tiles_at(i))], 1)] = i;
@@ -160,8 +201,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
         p.hdr->counter = 0;
         p.hdr->total_units = (uint32_t)units;
         p.hdr->cut = cut ? 1 : 0;
-        p.hdr->shares = (uint32_t)shares;
-        p.hdr->cost = all;
+        const long long cost2 = paired * p.num_kv_heads, units2 = (long long)lines * p.num_kv_heads;
+        p.hdr->shares = (uint32_t)(pairs ? max(1ll, min(p.grid / 2ll, max(units2, cost2 / kPfMinShare))) : shares);
+        p.hdr->cost = pairs ? cost2 : all;
+        p.hdr->lines = (uint32_t)lines;
+        p.hdr->pairs = pairs ? 1 : 0;
     }
 }
 

@@ -85,6 +85,8 @@ struct SparseParams {
     int32_t short_ring;                     // less of them on its way per CTA, more CTAs to an SM
     int32_t* status;
 };
+// List entries of a row, at most (a piece of a list is read up to its own place for every 512 of them).
+constexpr int32_t kSparseMaxSelected = 1 << 16;
 // List entries that a CTA translates at a time.
 constexpr int32_t kSparseEntries = 512;
 // A CTA of a cluster takes at least this many tiles of its row.

@@ -359,8 +359,8 @@ pa_status run_sparse(const SparseArgs& a, int32_t* status, cudaStream_t stream) 
         return fail(PA_ERR_UNSUPPORTED, "decode_sparse: pool has more than 2^31 rows");
     const int64_t rows = (int64_t)a.num_seqs * a.q_len * a.num_kv_heads;
     if (rows > (1 << 24)) return fail(PA_ERR_UNSUPPORTED, "decode_sparse: more than 2^24 (token, kv head) rows");
-    if ((int64_t)a.num_selected * a.block_size > (1 << 24))
-        return fail(PA_ERR_UNSUPPORTED, "decode_sparse: more than 2^24 selected tokens a row");
+    if (a.num_selected > pa::kSparseMaxSelected)
+        return fail(PA_ERR_UNSUPPORTED, "decode_sparse: num_selected %d > %d", a.num_selected, pa::kSparseMaxSelected);
     if (a.num_seqs == 0) return ok();
     if (!a.out || !a.query || !a.key_cache || !a.value_cache || !a.block_tables || !a.context_lens || !a.selected)
         return fail(PA_ERR_INVALID_ARG, "decode_sparse: null pointer");

@@ -107,7 +107,8 @@ struct Unit {
     int32_t single;       // the unit has rows for one stream only
     int32_t fix0;         // tiles at or past this one (within the item) are fixed
     int32_t nparts, part; // the unit's partitions, and which of them this is
-    int32_t first;        // the share (CTA) that holds partition 0
+    int32_t first;        // the CTA that holds partition 0 (trees: twice that, + 1 if the next
+                          // partition is two CTAs on and not one)
 };
 
 template <class C>
@@ -468,12 +469,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hdr.total_units = (uint32_t)(all * Hkv);
             }
             const int64_t shares = hdr.shares;
+            // (pairs of row tiles: neighbouring CTAs have the same share, each its own row tile)
+            const bool pairs = C::kTree && hdr.cut && hdr.pairs;
             // cut 0: the unit to take next; cut 1: the cost at which this share goes on, and
             // where it ends
-            int32_t w = (int32_t)blockIdx.x;
+            int32_t w = (int32_t)blockIdx.x >> (pairs ? 1 : 0);
             auto share_at = [&](int64_t b) { return b * hdr.cost / shares; };
             int64_t at = 0, end = 0;
             int32_t here = 0;
+            bool found = false;    // `here` is the line of this share's unit
             if (hdr.cut && w < (int32_t)hdr.shares) {
                 at = share_at(w);
                 end = share_at(w + 1);
@@ -506,10 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (at < end) do {
                         // row tile: the last one whose units begin at or before `at`
                         int32_t a = here;
-                        if (it == 0) {
+                        if (C::kTree && !found) {
+                            found = true;
                             // (32 places looked at together: a round trip through L2 or two, where
-                            // halving took one per bit, 0.6 us each)
-                            int32_t b = (int32_t)(hdr.total_units / (uint32_t)Hkv);
+                            // halving takes one per bit, 0.6 us each)
+                            int32_t b = (int32_t)hdr.lines;
                             while (b - a > 1) {
                                 const int32_t step = (b - a + 31) / 32;
                                 const int32_t m = min(a + lane * step, b);
@@ -517,6 +522,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const int32_t k = 31 - __clz(__ballot_sync(0xffffffffu, lane == 0 || le));
                                 a += k * step;
                                 b = min(a + step, b);
+                            }
+                        } else if (!C::kTree && it == 0) {
+                            int32_t b = (int32_t)(hdr.total_units / (uint32_t)Hkv);
+                            while (b - a > 1) {
+                                const int32_t m = (a + b) >> 1;
+                                if (p.before[m] * Hkv <= at) a = m;
+                                else b = m;
                             }
                         } else if (p.before[a + 1] * Hkv <= at) {
                             ++a;
@@ -535,14 +547,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int64_t lo = ((body + 1) * shares + hdr.cost - 1) / hdr.cost;
                         const int64_t hi = ((begin + len) * shares - 1) / hdr.cost;
                         rt = a;
+                        if (pairs) {
+                            rt = p.order[a] + (int32_t)(blockIdx.x & 1);
+                            // (a row tile left over is its pair's only one: on to the next unit)
+                            if ((blockIdx.x & 1) && (rt >= (int32_t)(hdr.total_units / (uint32_t)Hkv) ||
+                                                     p.seq_of[rt] != p.seq_of[rt - 1])) {
+                                rt = -1;
+                                at = min(begin + len, end);
+                                continue;
+                            }
+                        }
                         u.kvh = kvh;
                         u.nparts = (int32_t)max(hi - lo + 1, (int64_t)0) + 1;
                         u.first = (int32_t)(u.nparts > 1 ? lo - 1 : w);
                         u.part = w - u.first;
+                        if (C::kTree)
+                            u.first = pairs ? 2 * (2 * u.first + (int32_t)(blockIdx.x & 1)) + 1 : 2 * u.first;
                         tile0 = at > body ? (int32_t)(at - body) : 0;
                         tile1 = end < begin + len ? (int32_t)(end - body) : kNoToken;
                         at = min(begin + len, end);
-                    } while (false);
+                    } while (C::kTree && rt < 0 && at < end);
                 }
                 if (rt >= 0) {
                     int4 q;
@@ -1375,8 +1399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // rows of one stream only are its first stream's, whoever works on them.)
                 const int sj = u.single ? 0 : si;
                 const bool takes_part = both || !u.single || si == 0;
+                const int32_t first_cta = C::kTree ? u.first >> 1 : u.first;
                 auto place = [&](int part) {
-                    return ((size_t)(2 * (u.first + part) + (part == 0)) * 2 + sj) * kPfRows;
+                    const int32_t cta = C::kTree ? first_cta + (1 + (u.first & 1)) * part : u.first + part;
+                    return ((size_t)(2 * cta + (part == 0)) * 2 + sj) * kPfRows;
                 };
                 auto cell = [&](size_t at, int d) { return at * D + (size_t)d * kPfRows + row; };
                 if (takes_part) {
@@ -1385,12 +1411,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < dims / 16; ++h) {
                         float o[16];
                         load_o(h, o);
-                        if (mine) {      // (a row that holds no token is not read again either)
+                        if (!C::kTree || mine) {      // (a row that holds no token is not read again either)
 #pragma unroll
                             for (int c = 0; c < 16; ++c) p.part_acc[cell(at, dim0 + 16 * h + c)] = o[c];
                         }
                     }
-                    if (mine && half == 0 && !(both && si)) p.part_ml[at + row] = make_float2(ref, sum);
+                    if ((!C::kTree || mine) && half == 0 && !(both && si)) p.part_ml[at + row] = make_float2(ref, sum);
                 }
                 release();
                 if (takes_part) {
@@ -1403,28 +1429,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int32_t worth = u.single && !both ? 2 : 1;
                         const int32_t full = u.single ? 2 * u.nparts : u.nparts;
                         sm.last_seq[si] = u.seq;
-                        sm.last_part[si] = atomicAdd(&p.arrive[2 * u.first + sj], worth) == full - worth;
+                        sm.last_part[si] = atomicAdd(&p.arrive[2 * first_cta + sj], worth) == full - worth;
                     }
                     named_bar_sync(bar, kStreamThreads);
                     if (sm.last_part[si]) {
                         __threadfence();
-                        // (three at a time, each a round trip through L2; a row of no token: none)
-                        const int32_t parts = mine ? u.nparts : 0;
                         float M = -INFINITY, den = 0.f;
+                        if constexpr (C::kTree) {
+                            // (three at a time, each a round trip through L2; a row of no token: none)
+                            const int32_t parts = mine ? u.nparts : 0;
 #pragma unroll 1
-                        for (int pass = 0; pass < 2; ++pass) {
+                            for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-                            for (int q = 0; q < parts; q += 3) {
-                                float2 ml[3];
+                                for (int q = 0; q < parts; q += 3) {
+                                    float2 ml[3];
 #pragma unroll
-                                for (int t = 0; t < 3; ++t)
-                                    ml[t] = q + t < parts ? __ldcg(&p.part_ml[place(q + t) + row])
-                                                          : make_float2(-INFINITY, 0.f);
+                                    for (int t = 0; t < 3; ++t)
+                                        ml[t] = q + t < parts ? __ldcg(&p.part_ml[place(q + t) + row])
+                                                              : make_float2(-INFINITY, 0.f);
 #pragma unroll
-                                for (int t = 0; t < 3; ++t) {
-                                    if (pass == 0) M = fmaxf(M, ml[t].x);
-                                    else if (q + t < parts) den += state_weight(ml[t].x, M) * ml[t].y;
+                                    for (int t = 0; t < 3; ++t) {
+                                        if (pass == 0) M = fmaxf(M, ml[t].x);
+                                        else if (q + t < parts) den += state_weight(ml[t].x, M) * ml[t].y;
+                                    }
                                 }
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int q = 0; q < u.nparts; ++q) M = fmaxf(M, __ldcg(&p.part_ml[place(q) + row]).x);
+#pragma unroll 1
+                            for (int q = 0; q < u.nparts; ++q) {
+                                const float2 ml = __ldcg(&p.part_ml[place(q) + row]);
+                                den += state_weight(ml.x, M) * ml.y;
                             }
                         }
                         const float f = den == 0.f ? 0.f : p.out_scale / den;

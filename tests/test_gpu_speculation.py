@@ -1,0 +1,164 @@
+"""GPU: the tree and sparse operators in a row, as a server uses them: drafts decoded over selected
+blocks, the drafted tree's tokens written with their rotary positions, verified over the whole cache,
+the accepted path committed in every layer, the touched blocks bounded anew -- several rounds, after
+which the cache has to hold what appending the accepted tokens alone would have put there."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import chunk_reference as R
+import masked_reference as M
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("prompts,rounds", [([500, 33, 1300], 4), ([1], 3)])
+def test_rounds_of_speculation(cuda_device, prompts, rounds, fp8):
+    import paged_kv_cache_187_gb300 as pa
+    Hq, Hkv, D, bs, layers, dtype, dev = 16, 4, 128, 16, 2, torch.bfloat16, "cuda"
+    S, width, mcl, keep, vocab = len(prompts), 100, 1600, 12, 3
+    NB = S * width + 10
+    ks, vs = (0.03, 0.02) if fp8 else (1.0, 1.0)
+    g, r = torch.Generator(device=dev).manual_seed(5), random.Random(3)
+    scale = D ** -0.5
+    alloc = pa.PagedAllocator(NB, bs, 9)
+    cdt = torch.uint8 if fp8 else dtype
+    keys, values = ([torch.full((NB, Hkv, bs, D), 0, dtype=cdt, device=dev) for _ in range(layers)] for _ in range(2))
+    bounds = [torch.zeros((NB, Hkv, 2, D), dtype=torch.int8, device=dev) for _ in range(layers)]
+    steps = [torch.zeros((NB, Hkv), device=dev) for _ in range(layers)]
+    freq = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().to(dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    held = [[] for _ in range(S)]         # per sequence and layer: the rows that have to be in the cache
+
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32, device=dev)
+
+    def write(l, q, k, v, slots, pos):
+        out = torch.empty_like(q)
+        if fp8:
+            pa.pa_rope_and_cache_fp8(out, q, k, v, keys[l], values[l], slots, pos[None], freq, ks, vs, status=status)
+        else:
+            pa.pa_rope_and_cache(out, q, k, v, keys[l], values[l], slots, pos[None], freq, status=status)
+        return out
+
+    def rows(l, slots):
+        b, o = slots.long() // bs, slots.long() % bs
+        return [(keys[l][x, :, y].clone(), values[l][x, :, y].clone()) for x, y in zip(b, o)]
+
+    # the prompts
+    starts = np.concatenate([[0], np.cumsum(prompts)])
+    slots = []
+    for s, n in enumerate(prompts):
+        alloc.pa_alloc_add_seq(s, n)
+        slots += alloc.pa_alloc_slots(s, 0, n).tolist()
+    ids = list(range(S))
+    slots_d = i32(slots)
+    pos = torch.cat([torch.arange(n, device=dev) for n in prompts])
+    for l in range(layers):
+        q, k, v = (torch.randn((int(starts[-1]), h, D), generator=g, device=dev).to(dtype) for h in (Hq, Hkv, Hkv))
+        write(l, q, k, v, slots_d, pos)
+        got = rows(l, slots_d)
+        for s in range(S):
+            held[s].append(got[starts[s]:starts[s + 1]])
+    tables = torch.from_numpy(alloc.pa_alloc_block_tables(ids, width)).to(dev)
+    lens = torch.from_numpy(alloc.pa_alloc_context_lens(ids)).to(dev)
+    for l in range(layers):
+        pa.pa_key_bounds(bounds[l], steps[l], keys[l], tables, lens, max(prompts), query_starts=i32(starts.tolist()),
+                         status=status)
+    ws = torch.empty(max(pa.pa_select_blocks_workspace_size(S, 1, Hkv, bs, mcl), 256), dtype=torch.uint8, device=dev)
+    moved = 0
+    for _ in range(rounds):
+        length = alloc.pa_alloc_context_lens(ids)
+        # a draft step over selected blocks, every layer
+        for l in range(layers):
+            q = torch.randn((S, Hq, D), generator=g, device=dev).to(dtype)
+            sel = torch.empty((S, Hkv, keep), dtype=torch.int32, device=dev)
+            pa.pa_select_blocks(sel, q, bounds[l], steps[l], tables, lens, bs, mcl, 1, 3, workspace=ws, status=status)
+            out = torch.zeros_like(q)
+            if fp8:
+                pa.pa_decode_sparse_fp8(out, q, keys[l], values[l], tables, lens, sel, scale, ks, vs, status=status)
+            else:
+                pa.pa_decode_sparse(out, q, keys[l], values[l], tables, lens, sel, scale, status=status)
+            for s in range(S):
+                L, n_blocks = int(length[s]), -(-int(length[s]) // bs)
+                k, v = M.gather(keys[l], tables[s], L, ks), M.gather(values[l], tables[s], L, vs)
+                seen = torch.zeros((1, Hkv, n_blocks * bs), dtype=torch.bool, device=dev)
+                for h in range(Hkv):
+                    picked = [x for x in sel[s, h].tolist() if x >= 0]
+                    assert len(picked) == min(keep, n_blocks) and picked == sorted(set(picked))
+                    assert 0 in picked and n_blocks - 1 in picked
+                    for x in picked:
+                        seen[0, h, x * bs:(x + 1) * bs] = True
+                want, tol = M.attend(q[s:s + 1], k, v, seen[..., :L], scale, dtype, 2.0 ** -11 if fp8 else 2.0 ** -16,
+                                     2.0 ** -24)
+                assert ((out[s:s + 1].double() - want).abs() <= tol).all()
+        # the trees: written behind the contexts, verified, committed
+        sizes = [r.randint(1, 40) for _ in range(S)]
+        T = sum(sizes)
+        parents = [[-1] + [r.randrange(max(0, i - 5), i) for i in range(1, n)] for n in sizes]
+        sees = [M.paths(p) for p in parents]
+        mask = M.masks(sees, 2, dev)
+        starts = np.concatenate([[0], np.cumsum(sizes)])
+        starts_d = i32(starts.tolist())
+        slots, depth = [], []
+        for s, n in enumerate(sizes):
+            alloc.pa_alloc_reserve_batch([s], n)
+            table = alloc.pa_alloc_block_tables([s], width)[0]
+            slots += [int(table[t // bs]) * bs + t % bs for t in range(int(length[s]), int(length[s]) + n)]
+            depth += [int(length[s]) + int(m.sum()) - 1 for m in sees[s]]
+        tables = torch.from_numpy(alloc.pa_alloc_block_tables(ids, width)).to(dev)
+        with_tree = i32([int(length[s]) + sizes[s] for s in range(S)])
+        slots_d, pos = i32(slots), torch.tensor(depth, dtype=torch.int64, device=dev)
+        tws = torch.empty(pa.pa_decode_tree_workspace_size(T, S, Hq, Hkv, D, mcl), dtype=torch.uint8, device=dev)
+        tree_rows = []
+        for l in range(layers):
+            q, k, v = (torch.randn((T, h, D), generator=g, device=dev).to(dtype) for h in (Hq, Hkv, Hkv))
+            q = write(l, q, k, v, slots_d, pos)
+            tree_rows.append(rows(l, slots_d))
+            out = torch.zeros_like(q)
+            args = (out, q, keys[l], values[l], tables, with_tree, starts_d, mask, mcl, scale)
+            if fp8:
+                pa.pa_decode_tree_fp8(*args, ks, vs, workspace=tws, status=status)
+            else:
+                pa.pa_decode_tree(*args, workspace=tws, status=status)
+            want, tol = M.tree(q, keys[l], values[l], tables, with_tree.tolist(), starts, sees, scale, ks, vs)
+            assert ((out.double() - want).abs() <= tol).all()
+        draft, target = ([r.randrange(vocab) for _ in range(T)] for _ in range(2))
+        accepted = torch.zeros((S, 8), dtype=torch.int32, device=dev)
+        count = torch.zeros(S, dtype=torch.int32, device=dev)
+        follow = torch.zeros(S, dtype=torch.int64, device=dev)
+        lens = with_tree.clone()
+        pa.pa_tree_accept(accepted, count, follow, lens, torch.tensor(draft, device=dev), torch.tensor(target, device=dev),
+                          mask, starts_d, lens, status=status)
+        pa.pa_move_tokens(keys, values, tables, lens, accepted, count, status=status)
+        # (the host appends the accepted tokens, into the blocks that it reserved)
+        for s in range(S):
+            a = int(starts[s])
+            path, token = M.accept(parents[s], draft[a:a + sizes[s]], target[a:a + sizes[s]], 8)
+            assert accepted[s, :len(path)].tolist() == path and int(follow[s]) == token
+            moved += sum(i != j for j, i in enumerate(path))
+            for _ in path:
+                alloc.pa_alloc_append(s)
+            for l in range(layers):
+                held[s][l] = held[s][l] + [tree_rows[l][a + i] for i in path]
+        assert lens.tolist() == alloc.pa_alloc_context_lens(ids).tolist()
+        for l in range(layers):
+            pa.pa_key_bounds(bounds[l], steps[l], keys[l], tables, lens, 8, status=status)
+    assert moved > 0 or S == 1
+    assert int(status) == 0
+    largest = 448.0 if fp8 else 3.3895313892515355e38
+    for s in range(S):
+        L = int(lens[s])
+        for l in range(layers):
+            assert len(held[s][l]) == L
+            block, offset = tables[s, torch.arange(L, device=dev) // bs].long(), torch.arange(L, device=dev) % bs
+            assert torch.equal(keys[l][block, :, offset], torch.stack([k for k, _ in held[s][l]]))
+            assert torch.equal(values[l][block, :, offset], torch.stack([v for _, v in held[s][l]]))
+            for b in range(-(-L // bs)):
+                at = int(tables[s, b])
+                hi, lo, step = M.bounds(R.cache_values(keys[l][at, 1, :min(bs, L - b * bs)]), largest)
+                assert torch.equal(bounds[l][at, 1, 0].double(), hi) and torch.equal(bounds[l][at, 1, 1].double(), lo)
+                assert float(steps[l][at, 1]) == step

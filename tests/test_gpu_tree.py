@@ -464,3 +464,19 @@ def test_accept_and_move_in_a_graph(cuda_device):
             assert accepted[s, :len(path)].tolist() == path and int(follow[s]) == token
         want = moves_reference(fresh, tables.cpu(), new, accepted.cpu(), count, bs)
         assert all(torch.equal(p, w) for p, w in zip(pools, want))
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,bs,dtype,fp8", [
+    # two row tiles (and four, and three with one left over) of a sequence, taken in pairs
+    ([(60, 9001), (50, 7000), (64, 12000)], 16, 2, 128, 16, torch.bfloat16, False),
+    ([(55, 20000)], 8, 1, 128, 32, torch.float16, False),
+    ([(120, 9001), (97, 8000)], 16, 2, 128, 16, torch.bfloat16, False),
+    ([(33, 9001), (64, 300), (34, 15000), (0, 40), (64, 64)], 16, 2, 64, 16, torch.float16, False),
+    ([(60, 9001), (50, 7000)], 16, 2, 128, 16, torch.float16, True),
+    ([(400, 8000), (300, 9000)], 4, 1, 128, 16, torch.bfloat16, False),
+    # too many left over for pairs
+    ([(60, 9001), (5, 7000), (9, 12000), (31, 8000)], 16, 2, 128, 16, torch.bfloat16, False),
+])
+def test_row_tiles_in_pairs(cuda_device, seqs, Hq, Hkv, D, bs, dtype, fp8):
+    b = make(seqs, Hq, Hkv, D, bs, dtype, 41 + Hq, fp8)
+    run(b, trees(b, "paths", 19))

@@ -242,7 +242,7 @@ def _sparse(lib, fp8=False, **kw):
     (dict(Hq=34), UNSUPPORTED, "group"),
     (dict(NB=1 << 27), UNSUPPORTED, "rows"),
     (dict(S=1 << 20, QL=64), UNSUPPORTED, "rows"),
-    (dict(n=1 << 21), UNSUPPORTED, "tokens"),
+    (dict(n=(1 << 16) + 1), UNSUPPORTED, "num_selected"),
     (dict(scale=float("inf")), INVALID, "scale"),
     (dict(sel=0), INVALID, "null"),
     (dict(out=0), INVALID, "null"),
