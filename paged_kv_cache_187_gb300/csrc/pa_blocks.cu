@@ -12,6 +12,16 @@ namespace pa {
 
 namespace {
 
+// 16 bytes that no other thread reads, kept out of L1: bounds of 58 K tokens of new prompts 21.2 us
+// and a selection over 20 contexts of 60-126 K tokens 48.1 us; through L1 22.3 and 51.7.
+__device__ __forceinline__ uint4 ld_once(const void* at) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(at));
+    return v;
+}
+
 // floor(log2 x), -100 at least, of x >= 0 (not NaN).
 __device__ __forceinline__ int32_t exponent_of(float x) {
     return max((int32_t)(__float_as_uint(x) >> 23) - 127, -100);
@@ -68,8 +78,8 @@ constexpr int kBoundsRun = 4;
 // by shuffles.  The step is a power of two, so that x / step and its rounding are exact in fp32.
 // Bound by HBM for prompts (one read of K, 1/16 of it written), by latency for a step.  A run, since
 // what comes before a block's rows (lengths, then table entries) is as long as the rows' own wait:
-// 58 K tokens of new prompts, 8 heads of 128 (125 MB): 22.2 us, 5.6 TB/s; a block at a time 23.2; 26.7 before
-// the values were compared in pairs of 16 bits.
+// 58 K tokens of new prompts, 8 heads of 128 (125 MB): 21.2 us, 5.9 TB/s (through L1, where the rest was
+// measured, 22.3; a block at a time 23.2, 16 blocks 40; 26.7 with values compared one by one in fp32).
 template <BoundsType T, int D, int BS>
 __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const BoundsParams p) {
     constexpr int kElem = T == BoundsType::kFp8 ? 1 : 2;
@@ -99,7 +109,7 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Bou
     const int32_t len = (int32_t)min((int64_t)max(l, 0), cap);
     // this run's blocks: of those that hold a new token
     const int32_t first = max(len - n, 0) / BS + run * kBoundsRun;
-    const int32_t count = n == 0 ? 0 : min((len - first * BS + BS - 1) / BS, kBoundsRun);
+    const int32_t count = n == 0 ? 0 : min(len / BS + (len % BS != 0) - first, kBoundsRun);
     int32_t entry = 0;                                // lane i: block i's place in the pool
     if (lane < count) entry = p.block_tables[(size_t)s * p.max_blocks_per_seq + first + lane];
     for (int32_t i = 0; i < count; ++i) {
@@ -114,7 +124,7 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) key_bounds_kernel(const Bou
         uint4 x[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            if (i * kRows + lane / kLanes < valid) x[i] = rows[i * 32 + lane];
+            if (i * kRows + lane / kLanes < valid) x[i] = ld_once(rows + i * 32 + lane);
         constexpr bool kBf16 = T == BoundsType::kBf16;
         constexpr uint32_t kInf = kBf16 ? 0x7F807F80u : 0x7C007C00u, kSign = 0x80008000u;
         uint32_t top[kDims / 2], bottom[kDims / 2], odd = 0;
@@ -366,12 +376,12 @@ __device__ __forceinline__ int32_t scored_of(const SelectParams& p, int32_t s) {
 
 // Scores of the sequences' blocks, laid end to end (and once more for each further turn of kv
 // heads, as many at a time as the CTA has groups of lanes) and cut into equal slices, one per CTA:
-// contexts of any lengths keep all CTAs busy to the end.  (20 contexts of 60-126 K tokens: 43 us,
-// with a CTA per piece of 64 blocks of a sequence 51.)  A lane has 16 dims of a head: their weights
-// in registers, and 16 bytes of upper and of lower bounds of four records on their way; D / 16 lanes
-// share a record.  Whole-number products, exact sums (below 2^24), one exact product with the
-// block's step.  All that the weights do not come with is read before the kernel that writes them
-// has finished.  Bound by HBM: 2 D + 4 bytes per block and kv head.
+// contexts of any lengths keep all CTAs busy to the end.  (20 contexts of 60-126 K tokens, the whole
+// selection: 48 us; with a CTA per piece of 64 blocks of a sequence 8 more.)  A lane has 16 dims of a
+// head: their weights in registers, and 16 bytes of upper and of lower bounds of four records on
+// their way; D / 16 lanes share a record.  Whole-number products, exact sums (below 2^24), one exact
+// product with the block's step.  All that the weights do not come with is read before the kernel
+// that writes them has finished.  Bound by HBM: 2 D + 4 bytes per block and kv head.
 template <int D, int QT>
 __global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const SelectParams p) {
     constexpr int kLanes = D / 16;                           // lanes per record
@@ -444,8 +454,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const Se
 #pragma unroll
             for (int k = 0; k < kScoreBatch; ++k) {
                 const int8_t* src = at + (size_t)(uint32_t)(max(rec[k], 0) + head) * (2 * D);
-                t.x[k][0] = __ldg(reinterpret_cast<const uint4*>(src));
-                t.x[k][1] = __ldg(reinterpret_cast<const uint4*>(src + D));
+                t.x[k][0] = ld_once(src);
+                t.x[k][1] = ld_once(src + D);
             }
             const int32_t r = u == 0 ? rec[0] : u == 1 ? rec[1] : u == 2 ? rec[2] : rec[3];
             t.step = __ldg(p.steps + (size_t)(uint32_t)(max(r, 0) + head));
@@ -499,6 +509,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const Se
         for (int32_t s = tid; s < p.num_seqs; s += kScoreThreads) (void)context_of(p, s, true);   // reports
 }
 
+// (1024, with half the keys each: the selection over 20 contexts of 60-126 K tokens 2.5 us more)
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelRegs = 16;              // keys of a thread that stay in registers
