@@ -363,7 +363,7 @@ __device__ __forceinline__ uint32_t score_batch(const ScoreBatch& y, const int32
     d += __shfl_xor_sync(0xffffffffu, odd ? a : b, kQuarter);
 #pragma unroll
     for (int o = kQuarter / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    const float f = (float)d * y.step;
+    const float f = fmaf((float)d, y.step, 0.f);      // (0, not -0, where the step is 0)
     const uint32_t bits = __float_as_uint(f);
     return f != f ? 0xffffffffu : (bits >> 31) ? ~bits : bits | 0x80000000u;
 }
@@ -898,7 +898,9 @@ cudaError_t launch_select_blocks(const SelectParams& p, bool bf16, cudaStream_t 
     if (!p.keys) {
         const Kern kern = bf16 ? (wide ? (Kern)select_short_kernel<true, 128> : (Kern)select_short_kernel<true, 64>)
                                : (wide ? (Kern)select_short_kernel<false, 128> : (Kern)select_short_kernel<false, 64>);
-        return launch_pdl(rows, dim3(kSelThreads), bits + sizeof(uint32_t) * (size_t)p.max_blocks, stream, kern, p);
+        // (lists with room for every block need no scores)
+        const size_t smem = p.max_blocks > p.num_selected ? bits + sizeof(uint32_t) * (size_t)p.max_blocks : 0;
+        return launch_pdl(rows, dim3(kSelThreads), smem, stream, kern, p);
     }
     const bool one = p.q_len == 1;
     const Kern weights = bf16 ? (wide ? (Kern)select_weights_kernel<true, 128> : (Kern)select_weights_kernel<true, 64>)

@@ -224,6 +224,8 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
         return fail(PA_ERR_UNSUPPORTED, "select_blocks: query group %d > 16", num_q_heads / num_kv_heads);
     if (num_kv_heads > kMaxGridY) return fail(PA_ERR_UNSUPPORTED, "select_blocks: too many heads");
     if ((int64_t)num_seqs * q_len > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "select_blocks: too many rows");
+    if ((int64_t)num_blocks * num_kv_heads > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "select_blocks: pool of more than 2^31 blocks of one kv head");
     const int64_t context = std::min<int64_t>(max_context_len, (int64_t)max_blocks_per_seq * block_size);
     const int32_t blocks = (int32_t)((context + block_size - 1) / block_size);
     if (blocks > pa::kMaxSelectBlocks)

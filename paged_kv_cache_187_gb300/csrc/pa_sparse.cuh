@@ -160,6 +160,17 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
             sm.abort = 1;
         }
     };
+    // Elements 8 i .. of the row's outputs, of their sums and the sum of the weights (0: nothing is
+    // seen; NaN: some score is)
+    auto store_eight = [&](int32_t i, float den, const float (&y)[8]) {
+        const float f = den == 0.f ? 0.f : p.out_scale / den;
+        uint4 o;
+        o.x = pack2<C::kBf16>(y[0] * f, y[1] * f);
+        o.y = pack2<C::kBf16>(y[2] * f, y[3] * f);
+        o.z = pack2<C::kBf16>(y[4] * f, y[5] * f);
+        o.w = pack2<C::kBf16>(y[6] * f, y[7] * f);
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)row * p.group * C::D)[i] = o;
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -283,14 +294,14 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
         }
         if (c == 0 && !stop) {
             for (int o = 0; o < TS - 1; ++o) cons.merge_state(sm.states[o], lane);
-            if (parts > 1) {
-                stage_state<C>(cons, sm.sums, sm.ml, p.group, lane);
-            } else if (!warp_sees_abort(sm.abort)) {
-                UnitDesc u = {};
-                u.seq = row;
-                u.pslot = -1;
-                u.nrows = p.group;
-                cons.finish(sm.sums, p, u, lane);
+            stage_state<C>(cons, sm.sums, sm.ml, p.group, lane);
+            __syncwarp();
+            if (parts == 1 && !warp_sees_abort(sm.abort)) {
+                for (int32_t i = lane; i < p.group * C::D / 8; i += 32) {
+                    const float4* x = reinterpret_cast<const float4*>(sm.sums + 8 * i);
+                    const float4 a = x[0], b = x[1];
+                    store_eight(i, sm.ml[i / (C::D / 8)].y, {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+                }
             }
         }
     }
@@ -335,13 +346,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
                         y[4] += w * x[q][1].x, y[5] += w * x[q][1].y, y[6] += w * x[q][1].z, y[7] += w * x[q][1].w;
                     }
                 }
-                const float f = den > 0.f ? p.out_scale / den : 0.f;
-                uint4 o;
-                o.x = pack2<C::kBf16>(y[0] * f, y[1] * f);
-                o.y = pack2<C::kBf16>(y[2] * f, y[3] * f);
-                o.z = pack2<C::kBf16>(y[4] * f, y[5] * f);
-                o.w = pack2<C::kBf16>(y[6] * f, y[7] * f);
-                reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)row * p.group * C::D)[i] = o;
+                store_eight(i, den, y);
             }
         }
         __syncwarp();

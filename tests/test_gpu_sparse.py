@@ -492,3 +492,85 @@ def test_lists_longer_than_a_go_on_every_kind_of_row(cuda_device):
     for s in (0, 17, 249):
         one = dict(b, q=b["q"][s:s + 1], tables=b["tables"][s:s + 1], lens=[12000], selected=b["selected"][s:s + 1])
         sparse_check(one, out[s:s + 1])
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,dtype", [
+    ([700], 8, 2, 128, torch.bfloat16),                 # a cluster per row
+    ([700, 90] * 60, 8, 4, 128, torch.float16),         # a CTA
+    ([700], 2, 2, 64, torch.float16),                   # single heads, a cluster
+    ([700, 90] * 160, 2, 2, 64, torch.bfloat16),
+])
+def test_nan_keys_and_values_that_a_row_sees(cuda_device, lens, Hq, Hkv, D, dtype):
+    b = sparse_case(lens, 1, Hq, Hkv, D, 16, dtype, 40, 31, pick=40)
+    good = sparse_call(b)
+    assert bool(torch.isfinite(good).all())
+    first = [int(b["tables"][0, int(b["selected"][0, 0, h, 3])]) for h in range(2)]
+    b["kc"][first[0], 0, 5] = math.nan                  # kv head 0: all of it
+    b["vc"][first[1], 1, 7, 11] = math.nan              # kv head 1: dim 11
+    out = sparse_call(b)
+    g = Hq // Hkv
+    want = torch.zeros(good.shape, dtype=torch.bool, device="cuda")
+    want[0, 0, :g] = True
+    want[0, 0, g:2 * g, 11] = True
+    assert torch.equal(torch.isnan(out), want)
+    assert torch.equal(out[~want], good[~want])
+
+
+def test_lists_with_room_for_every_block_of_a_long_context(cuda_device):
+    b = select_case([16 * 20000 + 3, 16 * 131072, 5], 1, 2, 1, 64, 16, torch.float16, 5)
+    keep = 131072
+    out = select_call(b, keep, 3, 4)
+    for s, L in enumerate(b["lens"]):
+        n = -(-L // 16)
+        assert torch.equal(out[s, 0, 0, :n], torch.arange(n, dtype=torch.int32, device="cuda"))
+        assert bool((out[s, 0, 0, n:] == -1).all())
+    select_check(dict(b, lens=b["lens"][:1]), select_call(b, 131071, 3, 4), 131071, 3, 4)
+
+
+@pytest.mark.parametrize("seqs", [1, 40])
+def test_a_block_outside_the_pool_scores_zero(cuda_device, seqs):
+    """Not -0, whatever stands in the pool's first block."""
+    b = select_case([16 * 50] * seqs, 1, 8, 4, 64, 16, torch.bfloat16, 5)
+    b["q"].abs_()
+    b["bounds"].zero_()
+    b["bounds"][0] = -5
+    for at, block in ((3, -1), (17, b["bounds"].shape[0]), (30, 1 << 30)):
+        b["tables"][:, at] = block
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = select_call(b, 25, 1, 2, status=status)
+    assert int(status) == 2
+    for s in range(seqs):
+        worst = [i for i, x in enumerate(b["tables"][s].tolist()) if x == 0]
+        want = [i for i in range(48) if i not in worst][:23] + [48, 49]
+        if worst and worst[0] in (0, 48, 49):
+            want = list(range(23)) + [48, 49]
+        for h in range(4):
+            assert out[s, 0, h].tolist() == want, (s, h)
+
+
+def test_two_host_threads_and_streams_at_once(cuda_device):
+    import threading
+    jobs = []
+    for i, (lens, keep) in enumerate((([900, 4000], 40), ([300] * 50, 9))):
+        sel = select_case(lens, 1, 8, 2, 128, 16, torch.bfloat16, i)
+        att = sparse_case(lens, 1, 8, 2, 128, 16, torch.bfloat16, keep, i)
+        jobs.append((sel, att, keep, select_call(sel, keep, 1, 2), sparse_call(att)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(sel, att, keep, chosen, alone):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(60):
+                a = select_call(sel, keep, 1, 2, stream=stream)
+                b = sparse_call(att, stream=stream)
+                stream.synchronize()
+                if not torch.equal(a, chosen) or not torch.equal(b, alone):
+                    wrong.append(keep)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

@@ -162,3 +162,56 @@ def test_rounds_of_speculation(cuda_device, prompts, rounds, fp8):
                 hi, lo, step = M.bounds(R.cache_values(keys[l][at, 1, :min(bs, L - b * bs)]), largest)
                 assert torch.equal(bounds[l][at, 1, 0].double(), hi) and torch.equal(bounds[l][at, 1, 1].double(), lo)
                 assert float(steps[l][at, 1]) == step
+
+
+FIRST_CALLS = """
+import torch
+import test_gpu_sparse as S
+import test_gpu_tree as T
+import paged_kv_cache_187_gb300 as pa
+lens = [900, 40]
+att = S.sparse_case(lens, 1, 8, 2, 128, 16, torch.bfloat16, 40, 1)
+sel = S.select_case(lens, 1, 8, 2, 128, 16, torch.bfloat16, 1)
+far = S.select_case([40000], 1, 8, 2, 128, 16, torch.bfloat16, 1)
+tree = T.make([(12, 90), (5, 700)], 8, 2, 128, 16, torch.bfloat16, 2)
+sees = T.trees(tree, "paths", 1)
+mask = T.M.masks(sees, 1, "cuda")
+out, o = torch.zeros_like(tree["q"]), torch.zeros_like(att["q"])
+ws, ws2 = T.workspace(tree, 700), torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+a, f = (torch.zeros((len(x["lens"]), 1, 2, 40), dtype=torch.int32, device="cuda") for x in (sel, far))
+ids = torch.zeros(17, dtype=torch.int64, device="cuda")
+moved = tree["kc"].clone(), tree["vc"].clone()
+i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")
+path, count, follow, new = i32(2, 4), i32(2), torch.zeros(2, dtype=torch.int64, device="cuda"), i32(2)
+bounds, steps = torch.zeros((tree["kc"].shape[0], 2, 2, 128), dtype=torch.int8, device="cuda"), torch.zeros(
+    (tree["kc"].shape[0], 2), device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    S.sparse_call(att, out=o, ws=ws2)
+    S.select_call(sel, 40, 1, 2, out=a, ws=ws2)
+    S.select_call(far, 40, 1, 2, out=f, ws=ws2)
+    T.call(tree, mask, out, ws=ws, mcl=700)
+    pa.pa_tree_accept(path, count, follow, new, ids, ids, mask, tree["starts_d"], tree["lens_d"])
+    pa.pa_move_tokens([moved[0]], [moved[1]], tree["tables"], new, path, count)
+    pa.pa_key_bounds(bounds, steps, tree["kc"], tree["tables"], tree["lens_d"], 700)
+graph.replay()
+torch.cuda.synchronize()
+S.sparse_check(att, o)
+S.select_check(sel, a, 40, 1, 2)
+S.select_check(far, f, 40, 1, 2)
+T.check(tree, sees, out)
+assert int(count.min()) >= 1 and int(new[0]) == 90 - 12 + int(count[0])
+assert bool(steps.any())
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture(cuda_device):
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], env=env, cwd=here, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-3000:]

@@ -480,3 +480,35 @@ def test_accept_and_move_in_a_graph(cuda_device):
 def test_row_tiles_in_pairs(cuda_device, seqs, Hq, Hkv, D, bs, dtype, fp8):
     b = make(seqs, Hq, Hkv, D, bs, dtype, 41 + Hq, fp8)
     run(b, trees(b, "paths", 19))
+
+
+@pytest.mark.parametrize("seqs,kind", [([(2000, 2000), (3, 900)], "chain"), ([(1700, 2600)], "any"),
+                                       ([(2048, 2050), (2047, 4000)], "paths")])
+def test_large_trees(cuda_device, seqs, kind):
+    b = make(seqs, 4, 2, 64, 16, torch.float16, 12)
+    run(b, trees(b, kind, 3))
+
+
+def test_two_graphs_share_a_workspace(cuda_device):
+    """One whose contexts are cut, one without a plan, replayed in turn."""
+    import paged_kv_cache_187_gb300 as pa
+    cases = [make([(40, 9000), (64, 7000)], 8, 2, 128, 16, torch.bfloat16, 6), make([(9, 300)], 8, 2, 128, 16, torch.bfloat16, 7)]
+    need = max(pa.pa_decode_tree_workspace_size(b["q"].shape[0], len(b["lens"]), 8, 2, 128, max(b["lens"])) for b in cases)
+    ws = torch.full((need,), 0x5A, dtype=torch.uint8, device="cuda")
+    side, graphs, sees, outs = torch.cuda.Stream(), [], [], []
+    for b in cases:
+        sees.append(trees(b, "paths", 5))
+        mask, out = M.masks(sees[-1], 2, "cuda"), torch.zeros_like(b["q"])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call(b, mask, out, ws=ws)
+        graphs.append((graph, mask))
+        outs.append(out)
+    for turn in range(3):
+        for i, b in enumerate(cases):
+            outs[i].fill_(7.0)
+            graphs[i][0].replay()
+        torch.cuda.synchronize()
+        for i, b in enumerate(cases):
+            check(b, sees[i], outs[i])

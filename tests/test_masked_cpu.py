@@ -195,6 +195,7 @@ def _select(lib, **kw):
     (dict(Hq=70000, Hkv=70000), UNSUPPORTED, "heads"),
     (dict(S=1 << 20, QL=1 << 12), UNSUPPORTED, "rows"),
     (dict(mcl=1 << 30, maxb=1 << 27), UNSUPPORTED, "contexts"),
+    (dict(NB=1 << 30), UNSUPPORTED, "pool"),
     (dict(sel=0), INVALID, "null"),
     (dict(st=0), INVALID, "null"),
     (dict(q=MIS), INVALID, "aligned"),
