@@ -590,10 +590,10 @@ pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_a
  * pool PA_DEVERR_BAD_BLOCK; num_accepted or new_lens out of range: the sequence is left out and
  * flagged PA_DEVERR_BAD_LEN.  key_caches / value_caches as for pa_move_blocks (PA_F16, PA_BF16 or
  * PA_FP8_E4M3, rows of a multiple of 16 bytes).  The blocks that new tokens sit in must not be
- * shared between sequences (pa_alloc_reserve_batch sees to that).  On the host: reserve the blocks
- * of the whole tree with pa_alloc_reserve_batch, take the slots from the tables (position t's is
- * table[t / block_size] * block_size + t % block_size), and append the accepted tokens alone.  One
- * launch per 64 layers. */
+ * shared between sequences (pa_alloc_reserve_batch sees to that), nor a pool named twice.  On the
+ * host: reserve the blocks of the whole tree with pa_alloc_reserve_batch, take the slots from the
+ * tables (position t's is table[t / block_size] * block_size + t % block_size), and append the
+ * accepted tokens alone.  One launch per 64 layers. */
 pa_status pa_move_tokens(void* const* key_caches, void* const* value_caches, int32_t num_layers,
                          const int32_t* block_tables, int32_t max_blocks_per_seq,
                          const int32_t* new_lens, const int32_t* accepted, int32_t max_accepted,

@@ -164,6 +164,55 @@ def test_rounds_of_speculation(cuda_device, prompts, rounds, fp8):
                 assert float(steps[l][at, 1]) == step
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pools_past_four_gigabytes(cuda_device, fp8):
+    """The same blocks at the end of large pools and in small ones: the same bits."""
+    import paged_kv_cache_187_gb300 as pa
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Hkv, D, bs, used, NB = 8, 128, 16, 60, (400_000 if fp8 else 200_000)
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    lens, n = torch.tensor([470, 350], dtype=torch.int32, device="cuda"), 20
+    small = [torch.randn((used, Hkv, bs, D), generator=g, device="cuda") for _ in range(2)]
+    small = [x.to(torch.float8_e4m3fn).view(dtype) if fp8 else x.to(dtype) for x in small]
+    large = [torch.empty((NB, Hkv, bs, D), dtype=dtype, device="cuda") for _ in range(2)]
+    where = torch.arange(used, device="cuda") * 7 + NB - 7 * used
+    for x, y in zip(large, small):
+        x[where] = y
+    tables = torch.randperm(used, generator=g, device="cuda").to(torch.int32)[:2 * 30].view(2, 30)
+    far = where[tables.long()].to(torch.int32)
+    q = torch.randn((2 * n, 16, D), generator=g, device="cuda").to(torch.bfloat16)
+    starts = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    mask = torch.randint(-2 ** 31, 2 ** 31, (2 * n, 1), generator=g, device="cuda").to(torch.int32)
+    path = torch.tensor([[0, 2, 5, 6], [0, 1, 4, -1]], dtype=torch.int32, device="cuda")
+    count = torch.tensor([4, 3], dtype=torch.int32, device="cuda")
+    new = lens - n + count
+    got = []
+    for (kc, vc), table in ((small, tables), (large, far)):
+        bounds = torch.zeros((kc.shape[0], Hkv, 2, D), dtype=torch.int8, device="cuda")
+        steps = torch.zeros((kc.shape[0], Hkv), device="cuda")
+        pa.pa_key_bounds(bounds, steps, kc, table, lens, int(lens.max()))
+        chosen = torch.zeros((2, Hkv, 9), dtype=torch.int32, device="cuda")
+        ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+        pa.pa_select_blocks(chosen, q[::n].contiguous(), bounds, steps, table, lens, bs, 470, 1, 2, workspace=ws)
+        near, tree = torch.zeros_like(q[::n].contiguous()), torch.zeros_like(q)
+        args = (near, q[::n].contiguous(), kc, vc, table, lens, chosen, 0.1)
+        if fp8:
+            pa.pa_decode_sparse_fp8(*args, 0.5, 0.5)
+            pa.pa_decode_tree_fp8(tree, q, kc, vc, table, lens, starts, mask, 470, 0.1, 0.5, 0.5, workspace=ws)
+        else:
+            pa.pa_decode_sparse(*args)
+            pa.pa_decode_tree(tree, q, kc, vc, table, lens, starts, mask, 470, 0.1, workspace=ws)
+        pa.pa_move_tokens([kc], [vc], table, new, path, count)
+        torch.cuda.synchronize()
+        at = table[:, :30].long()
+        got.append((bounds[at], steps[at], chosen, near, tree, kc[at], vc[at]))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bool(got[0][3].any()) and bool(got[0][4].any())
+
+
 FIRST_CALLS = """
 import torch
 import test_gpu_sparse as S
