@@ -72,20 +72,34 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const Accep
 }
 
 constexpr int kMoveThreads = 128;
-constexpr int kMoveBatch = 8;        // rows that a thread has on their way
+constexpr int kMoveBatch = 4;        // rows that a thread has on their way
+constexpr int kMoveCtas = 12;        // CTAs to an SM
 constexpr int kMovePath = 64;        // path entries whose places sit in shared memory at a time
+static_assert(kMovePath <= kMoveThreads, "a thread per entry");
 
 // CTA (s, y): sequence s in pool y (2 * layer, + 1 for V).  A thread has one 16-byte column of
 // one kv head's rows and takes the path's rows in order, a batch's loads before its stores: a
 // row is only ever overwritten after it was read, since path[j] >= j and ascending.  Bound by
 // HBM at many layers (a row is 256 bytes per head, at scattered places), else by the chain
-// count -> path -> tables -> rows.
-__global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const __grid_constant__ MoveTokensParams p) {
+// lengths -> tables -> rows.  (64 sequences, 64 pools of 8 heads of 256 bytes: 14.5 us, 4.4 TB/s;
+// eight rows at a time, whose registers leave room for 6 CTAs, 17.2; two pools to a CTA 15.8, four
+// 18.5.)
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) move_tokens_kernel(const __grid_constant__ MoveTokensParams p) {
     __shared__ int64_t from_s[kMovePath], to_s[kMovePath];   // row of head 0; -1: nothing to move
     grid_dependency_wait();
     const int32_t s = blockIdx.x, tid = threadIdx.x;
     const bool report = p.report && blockIdx.y == 0 && p.status;
-    int32_t n = p.num_accepted[s];
+    // (the path's first entries are on their way with the lengths)
+    const int32_t* path = p.accepted + (size_t)s * p.max_accepted;
+    int32_t node = 0, before = -1;
+    auto entry = [&](int32_t j) {
+        if (j < p.max_accepted) {
+            node = path[j];
+            if (j > 0) before = path[j - 1];
+        }
+    };
+    if (tid < kMovePath) entry(tid);
+    const int32_t n = p.num_accepted[s];
     const int64_t base = (int64_t)p.new_lens[s] - n;
     if (n < 0 || n > p.max_accepted || base < 0) {
         if (report && tid == 0) atomicOr(p.status, kDevBadLen);
@@ -93,7 +107,6 @@ __global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const __grid_
     }
     const int32_t layer = blockIdx.y >> 1;
     const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size;
-    const int32_t* path = p.accepted + (size_t)s * p.max_accepted;
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
     uint4* const pool = layer < p.num_layers
                             ? static_cast<uint4*>((blockIdx.y & 1) ? p.value[layer] : p.key[layer])
@@ -107,10 +120,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_tokens_kernel(const __grid_
     for (int32_t j0 = 0; j0 < n; j0 += kMovePath) {
         const int32_t m = min(n - j0, kMovePath);
         if (j0 > 0) __syncthreads();
-        for (int32_t i = tid; i < m; i += kMoveThreads) {
-            const int32_t j = j0 + i, node = path[j];
+        if (tid < m) {
+            const int32_t i = tid, j = j0 + i;
+            if (j0 > 0) entry(j);
             int64_t from = -1, to = -1;
-            if (node < j || (j > 0 && path[j - 1] >= node)) {
+            if (node < j || (j > 0 && before >= node)) {
                 if (report) atomicOr(p.status, kDevBadSlot);
             } else if (base + node >= cap) {
                 if (report) atomicOr(p.status, kDevBadLen);
