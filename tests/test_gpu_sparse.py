@@ -575,3 +575,12 @@ def test_two_host_threads_and_streams_at_once(cuda_device):
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
+@pytest.mark.parametrize("lens,Hq,dtype,fp8", [([700, 33], 8, torch.bfloat16, False), ([300] * 100, 2, torch.float16, False),
+                                               ([700, 33], 8, torch.float16, True)])
+def test_scales(cuda_device, lens, Hq, dtype, fp8, scale):
+    b = sparse_case(lens, 1, Hq, 2, 128, 16, dtype, 20, 33, fp8=fp8)
+    b["scale"] = scale
+    sparse_check(b, sparse_call(b))

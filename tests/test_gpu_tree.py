@@ -512,3 +512,10 @@ def test_two_graphs_share_a_workspace(cuda_device):
         torch.cuda.synchronize()
         for i, b in enumerate(cases):
             check(b, sees[i], outs[i])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
+def test_scales(cuda_device, scale):
+    b = make([(20, 300), (5, 5), (33, 2000)], 8, 2, 128, 16, torch.bfloat16, 21)
+    b["scale"] = scale
+    run(b, trees(b, "any", 4))
