@@ -665,7 +665,8 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
  * A row of selected ascends; -1 entries are skipped, and entries that do not ascend or lie outside
  * the context are left out and flagged PA_DEVERR_BAD_BLOCK.  A row without tokens is a zero row; a
  * NaN score that it sees makes it NaN, a NaN value that element of it (an infinite one: infinite or
- * NaN).
+ * NaN).  A token with a score of -inf has no weight, and a row of such tokens alone is a zero row; a
+ * score of +inf makes the row NaN.
  * Other arguments, limits and accuracy as for pa_decode_auto (num_seqs * q_len * num_kv_heads at
  * most 2^24, num_selected at most 65536).  The present kernels need no workspace: the size is 0
  * and `workspace` may be NULL. */

@@ -120,7 +120,7 @@ struct UnitDesc {
 };
 
 template <int D_, int BS_, bool BF16_, bool MMA_, int HCAP_, int NSTAGE_, int NQ_, int NCONS_,
-          bool KV8_ = false, bool MQ_ = false, int MINB_ = 0, int PBS_ = BS_>
+          bool KV8_ = false, bool MQ_ = false, int MINB_ = 0, int PBS_ = BS_, bool LOW_ = MQ_>
 struct DecodeCfg {
     static constexpr int D = D_;
     // Tokens per tile (what a consumer takes at a time), and the pool's block size: a tile
@@ -132,6 +132,7 @@ struct DecodeCfg {
     static constexpr bool kKv8 = KV8_;             // K/V cache in fp8 E4M3 (else = query type)
     static constexpr bool kMma = MMA_;
     static constexpr bool kMq = MQ_;               // several causal query tokens per sequence
+    static constexpr bool kLow = LOW_;             // -inf may be all that a row has seen so far
     static constexpr int HCAP = HCAP_;             // query rows per unit the kernel holds
     static constexpr int NT = MMA_ ? HCAP_ / 8 : 0;  // mma n-tiles of 8 heads
     static constexpr int NSTAGE = NSTAGE_;
@@ -447,9 +448,9 @@ struct MmaConsumer {
                 mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
                 mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
                 const float mn = fmaxf(m[nt][j], mx[j]);
-                // A multi-query column may have seen no token yet (all masked so far):
+                // A column may have seen nothing but -inf yet (multi-query: all masked so far):
                 // exponentiate against 0 then, so that its weights and rescale are 0, not NaN.
-                mref[j] = (C::kMq && mn == -INFINITY) ? 0.f : mn;
+                mref[j] = (C::kLow && mn == -INFINITY) ? 0.f : mn;
                 alpha[j] = fast_exp2(m[nt][j] - mref[j]);
                 m[nt][j] = mn;
             }
@@ -871,12 +872,13 @@ struct CoreConsumer {
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const float mn = fmaxf(m[h], mx);
-            const float alpha = fast_exp2(m[h] - mn);
+            const float mref = (C::kLow && mn == -INFINITY) ? 0.f : mn;
+            const float alpha = fast_exp2(m[h] - mref);
             m[h] = mn;
             float ps = 0.f;
 #pragma unroll
             for (int tc = 0; tc < NC8; ++tc) {
-                const float e = fast_exp2(lg[h][tc] - mn);
+                const float e = fast_exp2(lg[h][tc] - mref);
                 ps += e;
                 if ((lane & 3) == 0) pbuf[h][tc * 8 + (lane >> 2)] = e;
             }

@@ -7,8 +7,9 @@
 // is one launch and no plan, and a row belongs to a cluster of 1 to 16 CTAs: each translates its
 // piece of the list (pa_sparse_device.cuh) and streams its tiles through a ring in shared memory by
 // TMA, the consumers being the decode's (pa_decode.cuh: tiles of one or two blocks, online softmax
-// on mma.sync for grouped heads and 8-bit caches, on CUDA cores for single ones); the parts meet in
-// shared memory, where every CTA joins its share of the row's elements out of the others'.
+// on mma.sync for grouped heads and 8-bit caches, on CUDA cores for single ones; a tile or a CTA's
+// whole part may hold scores of -inf alone, from infinite keys, whose weights are 0: kLow); the parts
+// meet in shared memory, where every CTA joins its share of the row's elements out of the others'.
 //
 // Measured (device time a call, calls back to back; 8 kv heads of 128, floors at the measured copy
 // bandwidth in brackets).  One sequence, 64 blocks of 16 tokens a row, 32 query heads: 7.1 us [0.6];
@@ -376,9 +377,9 @@ cudaError_t launch_sparse_one(const CUtensorMap& kmap, const CUtensorMap& vmap, 
     constexpr int kCons = consumers_for<MMA, kTile, KV8>();
     constexpr int kStages = stages_for<D * (KV8 ? 1 : 2) / 2, kTile, kCons>();
     using C0 = DecodeCfg<D, kTile, BF16, MMA, HCAP, kStages, 1, kCons, KV8, false, 0, BS>;
-    using C = DecodeCfg<D, kTile, BF16, MMA, HCAP, kStages, 1, kCons, KV8, false, decode_min_ctas<C0>(), BS>;
+    using C = DecodeCfg<D, kTile, BF16, MMA, HCAP, kStages, 1, kCons, KV8, false, decode_min_ctas<C0>(), BS, true>;
     constexpr int kShortCons = KV8 ? 2 : kCons, kShort = KV8 ? 4 : short_stages<kStages, kCons>();
-    using CS = DecodeCfg<D, kTile, BF16, MMA, HCAP, kShort, 1, kShortCons, KV8, false, decode_min_ctas<C0>(), BS>;
+    using CS = DecodeCfg<D, kTile, BF16, MMA, HCAP, kShort, 1, kShortCons, KV8, false, decode_min_ctas<C0>(), BS, true>;
     using Kern = void (*)(CUtensorMap, CUtensorMap, DecodeParams, SparseParams);
     const Kern kerns[2] = {sparse_kernel<C>, sparse_kernel<CS>};
     constexpr size_t smems[2] = {sparse_smem_bytes<C>(), sparse_smem_bytes<CS>()};
