@@ -14,9 +14,29 @@ import operator
 import os
 
 import numpy as np
-import torch
 
 from . import build as _build
+
+
+class _Torch:
+    """Stands for torch until a call takes something of it: the allocator and raw() need none."""
+
+    def __getattr__(self, name):
+        _with_torch()
+        return getattr(torch, name)
+
+
+torch = _Torch()
+
+
+def _with_torch():
+    """Puts torch, and what the calls take of it, in place of the stand-ins."""
+    import torch as module
+    global torch, _current_device, _current_stream, _is_contiguous, _device_of, _address_of
+    torch, tensor = module, module.Tensor
+    _current_device = getattr(module._C, "_cuda_getDevice", None)
+    _current_stream = getattr(module._C, "_cuda_getCurrentRawStream", None)
+    _is_contiguous, _device_of, _address_of = tensor.is_contiguous, tensor.get_device, tensor.data_ptr
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
@@ -524,13 +544,19 @@ def pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, h
                                               head_size, max_context_len))
 
 
-_current_device, _current_stream = (getattr(torch._C, "_cuda_getDevice", None),
-                                    getattr(torch._C, "_cuda_getCurrentRawStream", None))
+def _current_device():
+    _with_torch()
+    return _current_device()
+
+
+def _current_stream(device):
+    _with_torch()
+    return _current_stream(device)
 
 
 _shape_of, _dtype_of = operator.attrgetter("shape"), operator.attrgetter("dtype")
-_is_contiguous, _device_of, _address_of = (torch.Tensor.is_contiguous, torch.Tensor.get_device,
-                                           torch.Tensor.data_ptr)
+_is_contiguous, _device_of, _address_of = map(operator.methodcaller,
+                                              ("is_contiguous", "get_device", "data_ptr"))
 
 
 class _Call:

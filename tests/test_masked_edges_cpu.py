@@ -1,0 +1,68 @@
+"""CPU-only: the binding's and the library's edges around the tree and sparse operators."""
+import os
+import subprocess
+import sys
+import textwrap
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def pa():
+    from paged_kv_cache_187_gb300 import build
+    build.build()
+    import paged_kv_cache_187_gb300 as pkg
+    return pkg
+
+
+def test_the_allocator_and_the_raw_library_need_no_torch(pa):
+    code = """
+        import sys
+        sys.modules["torch"] = None          # importing it raises
+        import numpy as np
+        import paged_kv_cache_187_gb300 as pa
+        assert pa.raw().pa_version() > 0
+        alloc = pa.PagedAllocator(10, 16, 3)
+        alloc.pa_alloc_add_seq(1, 40)
+        alloc.pa_alloc_append(1)
+        assert alloc.num_free == 7
+        assert pa.pa_decode_tree_workspace_size(100, 3, 8, 2, 128, 900) > 0
+        assert pa.pa_select_blocks_workspace_size(3, 1, 2, 16, 900) > 0
+        try:
+            pa.pa_key_bounds(*[np.zeros((1, 2, 3, 4))] * 5, 1)
+        except ImportError:
+            pass
+        else:
+            raise AssertionError("a call with tensors")
+    """
+    subprocess.run([sys.executable, "-c", textwrap.dedent(code)], cwd=ROOT, check=True)
+
+
+def test_torch_is_looked_up_at_the_first_call_with_tensors(pa):
+    code = """
+        import paged_kv_cache_187_gb300._binding as B, sys
+        assert "torch" not in sys.modules and type(B.torch) is B._Torch
+        assert B.torch.float16.itemsize == 2
+        import torch
+        assert B.torch is torch and B._address_of is torch.Tensor.data_ptr
+        t = torch.zeros((2, 3))
+        c = B._Call.__new__(B._Call)
+        c.dev = -1                            # (the device of the host's tensors)
+        assert list(c.pools((t, t), t.shape, t.dtype)) == [t.data_ptr()] * 2
+    """
+    subprocess.run([sys.executable, "-c", textwrap.dedent(code)], cwd=ROOT, check=True)
+
+
+def test_pools_before_torch_is_looked_up(pa):
+    code = """
+        import torch
+        import paged_kv_cache_187_gb300._binding as B
+        assert type(B.torch) is B._Torch
+        t = torch.zeros((2, 3))
+        c = B._Call.__new__(B._Call)
+        c.dev = -1
+        assert list(c.pools((t, t), t.shape, t.dtype)) == [t.data_ptr()] * 2
+    """
+    subprocess.run([sys.executable, "-c", textwrap.dedent(code)], cwd=ROOT, check=True)
