@@ -623,14 +623,15 @@ def _prefill(fn, pool, scales, out, query, key_cache, value_cache, block_tables,
              query_starts, max_context_len, scale, workspace, status, stream, *tree_mask):
     i32 = torch.int32
     c = _Call()
+    who = "decode_tree" if tree_mask else "prefill"
     T, Hq, D = query.shape
     NB, Hkv, bs, D2 = key_cache.shape
     S = context_lens.shape[0]
     if out.shape != query.shape or value_cache.shape != key_cache.shape or D2 != D:
-        raise ValueError("prefill: inconsistent shapes")
+        raise ValueError(f"{who}: inconsistent shapes")
     if (context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S
             or query_starts.dim() != 1 or query_starts.shape[0] != S + 1):
-        raise ValueError("prefill: block_tables [S, max_blocks], context_lens [S] and "
+        raise ValueError(f"{who}: block_tables [S, max_blocks], context_lens [S] and "
                          "query_starts [S + 1] expected")
     tree = ()
     if tree_mask:

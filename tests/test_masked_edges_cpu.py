@@ -5,6 +5,7 @@ import sys
 import textwrap
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -66,3 +67,23 @@ def test_pools_before_torch_is_looked_up(pa):
         assert list(c.pools((t, t), t.shape, t.dtype)) == [t.data_ptr()] * 2
     """
     subprocess.run([sys.executable, "-c", textwrap.dedent(code)], cwd=ROOT, check=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("wrong", [dict(out=(5, 4, 32)), dict(lens=(1, 1)), dict(starts=(3,)), dict(mask=(4, 1))])
+def test_shape_errors_name_the_tree(pa, monkeypatch, fp8, wrong):
+    import paged_kv_cache_187_gb300._binding as B
+
+    class Here(B._Call):       # a machine without a GPU has no current device
+        def __init__(self):
+            self.dev = 0
+
+    monkeypatch.setattr(B, "_Call", Here)
+    shapes = dict(out=(5, 4, 64), q=(5, 4, 64), k=(9, 2, 16, 64), v=(9, 2, 16, 64), tables=(1, 4), lens=(1,),
+                  starts=(2,), mask=(5, 1))
+    args = [torch.zeros(x) for x in {**shapes, **wrong}.values()]
+    with pytest.raises(ValueError, match="^decode_tree: "):
+        (pa.pa_decode_tree_fp8 if fp8 else pa.pa_decode_tree)(*args, 64, 0.1, *([0.5, 0.5] if fp8 else []))
+    if "mask" not in wrong:
+        with pytest.raises(ValueError, match="^prefill: "):
+            (pa.pa_prefill_fp8 if fp8 else pa.pa_prefill)(*args[:-1], 64, 0.1, *([0.5, 0.5] if fp8 else []))
