@@ -643,7 +643,8 @@ pa_status pa_key_bounds(int8_t* bounds, float* bound_steps, const void* key_cach
  *   selected  int32 [num_seqs][q_len][num_kv_heads][num_selected]: block indices within the
  *             sequence, ascending, then -1
  *   query     [num_seqs][q_len][num_q_heads][head_size], fp16 or bf16 (dtype)
- * head_size 64 or 128, block_size 16 or 32, groups up to 16, contexts of up to 2^17 blocks; lengths
+ * head_size 64 or 128, block_size 16 or 32, groups up to 16, contexts of up to 2^17 blocks,
+ * num_selected up to 2^30 (a list of more than 2^16 is longer than pa_decode_sparse takes); lengths
  * past max_context_len or the table's row are clamped and flagged PA_DEVERR_BAD_LEN.  `workspace`
  * (device, 256-byte aligned, of pa_select_blocks_workspace_size bytes) needs no initialisation and
  * is dead after the call. */

@@ -38,6 +38,9 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int32_t kMaxGridY = 65535;
 
+// Entries of a list (blocks, an accepted path) at most: kernels step past its end in 32 bits.
+constexpr int32_t kMaxList = 1 << 30;
+
 }  // namespace
 
 extern "C" {
@@ -213,6 +216,8 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
     if (num_first < 0 || num_last < 0 || (int64_t)num_first + num_last > num_selected)
         return fail(PA_ERR_INVALID_ARG, "select_blocks: num_first %d and num_last %d of %d blocks", num_first,
                     num_last, num_selected);
+    if (num_selected > kMaxList)
+        return fail(PA_ERR_UNSUPPORTED, "select_blocks: num_selected %d > %d", num_selected, kMaxList);
     if (dtype != PA_F16 && dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "select_blocks: dtype");
     if (head_size != 64 && head_size != 128)
         return fail(PA_ERR_UNSUPPORTED, "select_blocks: head_size %d (64 or 128)", head_size);

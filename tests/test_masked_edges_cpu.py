@@ -7,6 +7,8 @@ import textwrap
 import pytest
 import torch
 
+from test_masked_cpu import UNSUPPORTED, _accept, _err, _move, _select
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -87,3 +89,11 @@ def test_shape_errors_name_the_tree(pa, monkeypatch, fp8, wrong):
     if "mask" not in wrong:
         with pytest.raises(ValueError, match="^prefill: "):
             (pa.pa_prefill_fp8 if fp8 else pa.pa_prefill)(*args[:-1], 64, 0.1, *([0.5, 0.5] if fp8 else []))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(first=2 ** 31 - 12), dict(first=0, last=2 ** 30)])
+@pytest.mark.parametrize("n", [2 ** 30 + 1, 2 ** 31 - 1])
+def test_lists_of_blocks_past_32_bit_steps_are_refused(pa, n, kw):
+    kw = {k: min(x, n) for k, x in {**dict(first=1, last=0), **kw}.items()}
+    assert _select(pa.raw(), n=n, **kw) == UNSUPPORTED
+    assert "num_selected" in _err(pa.raw())
