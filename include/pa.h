@@ -572,7 +572,7 @@ pa_status pa_decode_tree_fp8(void* out, const void* query, const void* key_cache
  *   new_lens      int32 [num_seqs]: context_lens[s] - C + num_accepted[s]; may be context_lens
  *   draft_tokens, target_tokens  int64 [num_tokens]: each new token's id, and the id that the
  *                 model chooses after it
- * mask_words is at most 64 here.  Another rule of acceptance (sampling) can fill accepted,
+ * mask_words is at most 64 here, max_accepted 2^30.  Another rule of acceptance (sampling) can fill accepted,
  * num_accepted and new_lens itself.  Bad query_starts, or a context shorter than its tree, are
  * clamped and flagged PA_DEVERR_BAD_LEN. */
 pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_accepted,

@@ -54,6 +54,8 @@ pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_a
         return fail(PA_ERR_INVALID_ARG, "tree_accept: sizes must be positive (num_tokens, num_seqs >= 0)");
     if (mask_words > pa::kMaxTreeWords)
         return fail(PA_ERR_UNSUPPORTED, "tree_accept: mask_words %d > %d", mask_words, pa::kMaxTreeWords);
+    if (max_accepted > kMaxList)
+        return fail(PA_ERR_UNSUPPORTED, "tree_accept: max_accepted %d > %d", max_accepted, kMaxList);
     if (num_seqs == 0) return ok();
     if (!accepted || !num_accepted || !next_tokens || !new_lens || !query_starts || !context_lens ||
         (num_tokens > 0 && (!draft_tokens || !target_tokens || !tree_mask)))

@@ -97,3 +97,9 @@ def test_lists_of_blocks_past_32_bit_steps_are_refused(pa, n, kw):
     kw = {k: min(x, n) for k, x in {**dict(first=1, last=0), **kw}.items()}
     assert _select(pa.raw(), n=n, **kw) == UNSUPPORTED
     assert "num_selected" in _err(pa.raw())
+
+
+@pytest.mark.parametrize("most", [2 ** 30 + 1, 2 ** 31 - 1])
+def test_paths_past_32_bit_steps_are_refused_by_the_accept(pa, most):
+    assert _accept(pa.raw(), most=most) == UNSUPPORTED
+    assert "max_accepted" in _err(pa.raw())
