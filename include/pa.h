@@ -589,7 +589,7 @@ pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_a
  * PA_DEVERR_BAD_SLOT, one past the block table's row PA_DEVERR_BAD_LEN, one in a block outside the
  * pool PA_DEVERR_BAD_BLOCK; num_accepted or new_lens out of range: the sequence is left out and
  * flagged PA_DEVERR_BAD_LEN.  key_caches / value_caches as for pa_move_blocks (PA_F16, PA_BF16 or
- * PA_FP8_E4M3, rows of a multiple of 16 bytes).  The blocks that new tokens sit in must not be
+ * PA_FP8_E4M3, rows of a multiple of 16 bytes); max_accepted is at most 2^30.  The blocks that new tokens sit in must not be
  * shared between sequences (pa_alloc_reserve_batch sees to that), nor a pool named twice.  On the
  * host: reserve the blocks of the whole tree with pa_alloc_reserve_batch, take the slots from the
  * tables (position t's is table[t / block_size] * block_size + t % block_size), and append the

@@ -38,7 +38,8 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int32_t kMaxGridY = 65535;
 
-// Entries of a list (blocks, an accepted path) at most: kernels step past its end in 32 bits.
+// Entries of a list (blocks, an accepted path, a token's row) at most: kernels step past its end in
+// 32 bits.
 constexpr int32_t kMaxList = 1 << 30;
 
 }  // namespace
@@ -94,7 +95,9 @@ pa_status pa_move_tokens(void* const* key_caches, void* const* value_caches, int
         return fail(PA_ERR_UNSUPPORTED, "move_tokens: dtype");
     const int64_t row = (int64_t)head_size * (dtype == PA_FP8_E4M3 ? 1 : 2);
     if (row % 16) return fail(PA_ERR_INVALID_ARG, "move_tokens: rows must be 16-byte multiples");
-    if (row / 16 * num_kv_heads > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "move_tokens: too many heads");
+    if (row / 16 * num_kv_heads > kMaxList) return fail(PA_ERR_UNSUPPORTED, "move_tokens: too many heads");
+    if (max_accepted > kMaxList)
+        return fail(PA_ERR_UNSUPPORTED, "move_tokens: max_accepted %d > %d", max_accepted, kMaxList);
     if (num_seqs == 0 || num_layers == 0) return ok();
     if (!key_caches || !value_caches || !block_tables || !new_lens || !accepted || !num_accepted)
         return fail(PA_ERR_INVALID_ARG, "move_tokens: null pointer");

@@ -103,3 +103,10 @@ def test_lists_of_blocks_past_32_bit_steps_are_refused(pa, n, kw):
 def test_paths_past_32_bit_steps_are_refused_by_the_accept(pa, most):
     assert _accept(pa.raw(), most=most) == UNSUPPORTED
     assert "max_accepted" in _err(pa.raw())
+
+
+@pytest.mark.parametrize("kw,word", [(dict(most=2 ** 30 + 1), "max_accepted"), (dict(most=2 ** 31 - 1), "max_accepted"),
+                                     (dict(Hkv=2 ** 31 - 1, D=8), "heads"), (dict(Hkv=2 ** 30 + 1, D=8), "heads")])
+def test_paths_and_rows_past_32_bit_steps_are_refused_by_the_move(pa, kw, word):
+    assert _move(pa.raw(), **kw) == UNSUPPORTED
+    assert word in _err(pa.raw())
