@@ -572,9 +572,9 @@ pa_status pa_decode_tree_fp8(void* out, const void* query, const void* key_cache
  *   new_lens      int32 [num_seqs]: context_lens[s] - C + num_accepted[s]; may be context_lens
  *   draft_tokens, target_tokens  int64 [num_tokens]: each new token's id, and the id that the
  *                 model chooses after it
- * mask_words is at most 64 here, max_accepted 2^30.  Another rule of acceptance (sampling) can fill accepted,
- * num_accepted and new_lens itself.  Bad query_starts, or a context shorter than its tree, are
- * clamped and flagged PA_DEVERR_BAD_LEN. */
+ * mask_words is at most 64 here, max_accepted 2^30.  Another rule of acceptance (sampling) can
+ * fill accepted, num_accepted and new_lens itself.  Bad query_starts, or a context shorter than its
+ * tree, are clamped and flagged PA_DEVERR_BAD_LEN. */
 pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_accepted,
                          int64_t* next_tokens, int32_t* new_lens, const int64_t* draft_tokens,
                          const int64_t* target_tokens, const int32_t* tree_mask, int32_t mask_words,
@@ -589,11 +589,11 @@ pa_status pa_tree_accept(int32_t* accepted, int32_t max_accepted, int32_t* num_a
  * PA_DEVERR_BAD_SLOT, one past the block table's row PA_DEVERR_BAD_LEN, one in a block outside the
  * pool PA_DEVERR_BAD_BLOCK; num_accepted or new_lens out of range: the sequence is left out and
  * flagged PA_DEVERR_BAD_LEN.  key_caches / value_caches as for pa_move_blocks (PA_F16, PA_BF16 or
- * PA_FP8_E4M3, rows of a multiple of 16 bytes); max_accepted is at most 2^30.  The blocks that new tokens sit in must not be
- * shared between sequences (pa_alloc_reserve_batch sees to that), nor a pool named twice.  On the
- * host: reserve the blocks of the whole tree with pa_alloc_reserve_batch, take the slots from the
- * tables (position t's is table[t / block_size] * block_size + t % block_size), and append the
- * accepted tokens alone.  One launch per 64 layers. */
+ * PA_FP8_E4M3, rows of a multiple of 16 bytes); max_accepted is at most 2^30.  The blocks that new
+ * tokens sit in must not be shared between sequences (pa_alloc_reserve_batch sees to that), nor a
+ * pool named twice.  On the host: reserve the blocks of the whole tree with pa_alloc_reserve_batch,
+ * take the slots from the tables (position t's is table[t / block_size] * block_size + t %
+ * block_size), and append the accepted tokens alone.  One launch per 64 layers. */
 pa_status pa_move_tokens(void* const* key_caches, void* const* value_caches, int32_t num_layers,
                          const int32_t* block_tables, int32_t max_blocks_per_seq,
                          const int32_t* new_lens, const int32_t* accepted, int32_t max_accepted,

@@ -1,6 +1,5 @@
 // pa_tree_aux.cu -- what follows the attention of a tree of drafted tokens: the path that the
 // model's own choices accept, and its K / V rows moved together in every layer's pools.
-#include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -108,9 +107,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) move_tokens_kernel(co
     const int32_t layer = blockIdx.y >> 1;
     const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size;
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
-    uint4* const pool = layer < p.num_layers
-                            ? static_cast<uint4*>((blockIdx.y & 1) ? p.value[layer] : p.key[layer])
-                            : nullptr;
+    uint4* const pool = static_cast<uint4*>((blockIdx.y & 1) ? p.value[layer] : p.key[layer]);
     auto row_of = [&](int64_t pos) -> int64_t {
         const int32_t block = table[pos / p.block_size];
         if (block < 0 || block >= p.num_blocks) return -1;
@@ -140,7 +137,6 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) move_tokens_kernel(co
             to_s[i] = to;
         }
         __syncthreads();
-        if (!pool) continue;
         for (int32_t c = tid; c < columns; c += kMoveThreads) {
             const int32_t h = c / p.row_vecs;
             uint4* const col = pool + ((int64_t)h * p.block_size) * p.row_vecs + (c - h * p.row_vecs);
@@ -167,7 +163,7 @@ cudaError_t launch_tree_accept(const AcceptParams& p, cudaStream_t stream) {
 
 cudaError_t launch_move_tokens(const MoveTokensParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.num_seqs, (unsigned)std::max(2 * p.num_layers, 1));
+    cfg.gridDim = dim3((unsigned)p.num_seqs, (unsigned)(2 * p.num_layers));
     cfg.blockDim = dim3(kMoveThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
