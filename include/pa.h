@@ -663,11 +663,11 @@ pa_status pa_select_blocks(int32_t* selected, const void* query, const int8_t* b
  * selected blocks:
  *   out[s][j][h] = sum_t softmax_t(scale * q . k_t) v_t,
  *   t < context_lens[s] - q_len + j + 1 and t / block_size in selected[s][j][h / group].
- * A row of selected ascends; -1 entries are skipped, and entries that do not ascend or lie outside
- * the context are left out and flagged PA_DEVERR_BAD_BLOCK.  A row without tokens is a zero row; a
- * NaN score that it sees makes it NaN, a NaN value that element of it (an infinite one: infinite or
- * NaN).  A token with a score of -inf has no weight, and a row of such tokens alone is a zero row; a
- * score of +inf makes the row NaN.
+ * A row of selected ascends; negative entries are skipped, and entries that do not ascend or lie
+ * past the context are left out and flagged PA_DEVERR_BAD_BLOCK.  A row without tokens is a zero
+ * row; a NaN score that it sees makes it NaN, a NaN value that element of it (an infinite one:
+ * infinite or NaN).  A token with a score of -inf has no weight, and a row of such tokens alone is a
+ * zero row; a score of +inf makes the row NaN.
  * Other arguments, limits and accuracy as for pa_decode_auto (num_seqs * q_len * num_kv_heads at
  * most 2^24, num_selected at most 65536).  The present kernels need no workspace: the size is 0
  * and `workspace` may be NULL. */
