@@ -619,9 +619,11 @@ pa_status pa_move_tokens(void* const* key_caches, void* const* value_caches, int
  * An infinity counts as the type's largest number; a NaN is passed over and makes the step NaN.
  * Keys of fp8 pools are taken without their scale.  Blocks: those of sequence s that hold its last
  * query_starts[s+1] - query_starts[s] <= max_new_tokens tokens (query_starts int32 [num_seqs + 1];
- * NULL: max_new_tokens each), each anew from all its rows, so a block may be bounded any number of
- * times, and has to be after its tokens change (a rejected tree among them).  dtype is the pool's
- * (PA_F16, PA_BF16, PA_FP8_E4M3); head_size 64 or 128, block_size 16 or 32. */
+ * NULL: max_new_tokens each), or all of them where the context is shorter than that, each anew from
+ * all its rows, so a block may be bounded any number of times, and has to be after its tokens change
+ * (a rejected tree among them).  Sequences of one call that share a block hold the same number of
+ * tokens in it.  dtype is the pool's (PA_F16, PA_BF16, PA_FP8_E4M3); head_size 64 or 128, block_size
+ * 16 or 32. */
 pa_status pa_key_bounds(int8_t* bounds, float* bound_steps, const void* key_cache,
                         const int32_t* block_tables, int32_t max_blocks_per_seq,
                         const int32_t* context_lens, const int32_t* query_starts,
