@@ -1,12 +1,61 @@
-"""GPU: edges of the tree and sparse operators -- more new tokens than a context holds, negative
-entries of a list."""
+"""GPU: edges of the tree and sparse operators -- scores of -inf before and within a tree, more new
+tokens than a context holds, negative entries of a list."""
+import math
+
 import pytest
 import torch
 
+import chunk_reference as R
 import masked_reference as M
+from test_gpu_prefill import make
 from test_gpu_sparse import LARGEST, layout, pool_of, sparse_call, sparse_case, sparse_check
+from test_gpu_tree import call, trees
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,dtype", [
+    ([(20, 300), (1, 200), (40, 150)], 8, 2, 128, torch.bfloat16),
+    ([(8, 5000)], 8, 1, 64, torch.float16),                   # cut into shares, rows for one stream
+    ([(64, 9000), (33, 2600)], 16, 2, 128, torch.bfloat16),
+    ([(1 + i * 7 % 64, 200 + i * 131 % 1500) for i in range(60)], 4, 4, 64, torch.float16),
+])
+@pytest.mark.parametrize("where", ["first tile", "a late token", "all before the tree", "everything"])
+def test_scores_of_minus_infinity_in_and_before_a_tree(cuda_device, seqs, Hq, Hkv, D, dtype, where):
+    """Infinite keys where every query is positive: those tokens have no weight, and a row that sees
+    no other is a zero row."""
+    b = make(seqs, Hq, Hkv, D, 16, dtype, 19)
+    sees = trees(b, "paths", 4)
+    b["q"][..., 3] = b["q"][..., 3].abs() + 0.5
+    want = torch.zeros(b["q"].shape, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(want)
+    for s, (n, L) in enumerate(seqs):
+        hide = torch.zeros(L, dtype=torch.bool, device="cuda")
+        if where == "first tile":
+            hide[:64] = True
+        elif where == "a late token":
+            hide[L - n - 1:L - n + 1] = True
+        elif where == "all before the tree":
+            hide[:L - n] = True
+        else:
+            hide[:] = True
+        t = hide.nonzero()[:, 0]
+        b["kc"][b["tables"][s, t // 16].long(), :, t % 16, 3] = -math.inf
+        k = M.gather(b["kc"], b["tables"][s], L)
+        k[t] = 0
+        v = M.gather(b["vc"], b["tables"][s], L)
+        seen = torch.ones((n, L), dtype=torch.bool, device="cuda")
+        seen[:, L - n:] = sees[s].cuda().tril()
+        seen &= ~hide
+        a = int(b["starts"][s])
+        want[a:a + n], tol[a:a + n] = M.attend(b["q"][a:a + n], k, v, seen[:, None].expand(n, Hkv, L), b["scale"], dtype,
+                                               R.half_step(dtype), 2.0 ** -32 if dtype == torch.float16 else 0.0)
+    mask = M.masks(sees, 2, "cuda")
+    out = call(b, mask, torch.full_like(b["q"], 7.0))
+    assert bool(torch.isfinite(out).all())
+    assert bool(((out.double() - want).abs() <= tol).all())
+    if where == "everything":
+        assert not bool(out.any())
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.uint8])
