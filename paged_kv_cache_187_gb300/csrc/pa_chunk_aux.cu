@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
     // two neighbouring CTAs take the shares of a pair of row tiles, each its own, and keep in step:
     // the second read comes from L2.  (A row tile left over leaves a CTA idle meanwhile; pairs are
     // taken where that costs no more than a tenth.)  4 trees of 50-63 tokens, 8 heads to a kv head,
-    // behind 56-60 K: 370 us end to end, 330 in pairs; 415 and 362 at the power cap.
+    // behind 56-60 K: 370 us end to end, 330 in pairs; 415 and 361-380 at the power cap.
     long long paired = 0;
     int32_t lines = row_tiles;
     auto pair_cost = [&](int32_t i) {          // of the pair that begins at row tile i, 0: none does

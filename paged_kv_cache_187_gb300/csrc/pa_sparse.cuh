@@ -12,7 +12,7 @@
 // meet in shared memory, where every CTA joins its share of the row's elements out of the others'.
 //
 // Measured (device time a call, calls back to back; 8 kv heads of 128, floors at the measured copy
-// bandwidth in brackets).  One sequence, 64 blocks of 16 tokens a row, 32 query heads: 7.1 us [0.6];
+// bandwidth in brackets).  One sequence, 64 blocks of 16 tokens a row, 32 query heads: 7.1-7.6 us [0.6];
 // with the decode over tables that a kernel of its own made, 20.4.  48 sequences, 128 blocks: 64
 // [59.3], where the decode's partitions took 83, and slices of one size for every CTA, cut through
 // the rows and joined through memory, 71: CTAs with the same bytes finish up to 13 us apart, and
