@@ -1,10 +1,11 @@
-"""GPU: attention over selected blocks (pa_decode_sparse, _fp8) where scores are -inf: such a token
-has no weight, wherever it stands in the tiles of a row."""
+"""GPU: attention over selected blocks (pa_decode_sparse, _fp8) where scores are -inf (such a token
+has no weight, wherever it stands in the tiles of a row), and over the longest lists."""
 import math
 
 import pytest
 import torch
 
+import masked_reference as M
 from test_gpu_sparse import sparse_call, sparse_case, sparse_check, sparse_reference, sparse_run
 
 pytestmark = pytest.mark.gpu
@@ -115,3 +116,28 @@ def test_a_nan_beside_minus_infinity_is_nan(cuda_device, seqs, Hq, Hkv, D, dtype
     want = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
     want[0, 0, :g] = True
     assert torch.equal(torch.isnan(out), want)
+
+
+@pytest.mark.parametrize("seqs,Hq,dtype", [(300, 1, torch.bfloat16), (300, 4, torch.float16), (1, 4, torch.bfloat16)])
+def test_the_longest_lists(cuda_device, seqs, Hq, dtype):
+    """65,536 entries, in whole rows and in a cluster: every wait within its limit."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    blocks, bs, D = 65536, 16, 64
+    L = blocks * bs - 5
+    kc, vc = (torch.randn((blocks, 1, bs, D), generator=g, device="cuda").to(dtype) for _ in range(2))
+    kc[-1, :, bs - 5:] = vc[-1, :, bs - 5:] = math.nan
+    row = torch.arange(blocks, dtype=torch.int32, device="cuda")
+    b = dict(q=torch.randn((seqs, 1, Hq, D), generator=g, device="cuda").to(dtype), kc=kc, vc=vc,
+             tables=row.expand(seqs, blocks).contiguous(), lens=[L] * seqs,
+             lens_d=torch.full((seqs,), L, dtype=torch.int32, device="cuda"),
+             selected=row.expand(seqs, 1, 1, blocks).contiguous(), scale=D ** -0.5, fp8=False)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = sparse_call(b, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    k, v = kc.transpose(1, 2).reshape(-1, 1, D)[:L].double(), vc.transpose(1, 2).reshape(-1, 1, D)[:L].double()
+    seen = torch.ones((1, 1, L), dtype=torch.bool, device="cuda")
+    for s in sorted({0, seqs // 2, seqs - 1}):
+        want, tol = M.attend(b["q"][s], k, v, seen, b["scale"], dtype, 2.0 ** -16,
+                             2.0 ** -24 if dtype == torch.float16 else 0.0)
+        assert bool(((out[s].double() - want).abs() <= tol).all())
