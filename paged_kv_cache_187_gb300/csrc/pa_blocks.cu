@@ -381,7 +381,9 @@ __device__ __forceinline__ int32_t scored_of(const SelectParams& p, int32_t s) {
 // head: their weights in registers, and 16 bytes of upper and of lower bounds of four records on
 // their way; D / 16 lanes share a record.  Whole-number products, exact sums (below 2^24), one exact
 // product with the block's step.  All that the weights do not come with is read before the kernel
-// that writes them has finished.  Bound by HBM: 2 D + 4 bytes per block and kv head.
+// that writes them has finished.  Bound by HBM: 2 D + 4 bytes per block and kv head.  QT query tokens
+// share a fetch: with more than two a CTA fetches its chunk again for each further pair, and the
+// kernels of pairs spill 124 bytes at 128 registers (those of one token none).
 template <int D, int QT>
 __global__ void __launch_bounds__(kScoreThreads, 2) block_scores_kernel(const SelectParams p) {
     constexpr int kLanes = D / 16;                           // lanes per record
